@@ -14,6 +14,7 @@ importing this package without it raises ImportError.  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -29,6 +30,10 @@ GDR_ALPHA_SCALAR, GDR_ALPHA_CHANNEL = 0, 1
 GDR_BETA_SCALAR, GDR_BETA_SHARED, GDR_BETA_KV = 0, 1, 2
 GDR_FLAG_READ_BEFORE_WRITE = 0x10
 GDR_FLAG_UNDECAYED_PREDICTION = 0x20
+GDR_FLAG_LOG_GATE, GDR_FLAG_COUPLED = 0x40, 0x80
+GDR_NORM_NONE, GDR_NORM_L2, GDR_NORM_RMS = 0, 1, 2
+GDR_ROT_HALF, GDR_ROT_INTERLEAVED = 0, 1
+GDR_SCAN_BLOCK = 512
 PATH_MFMA, PATH_VALU = 1, 2
 
 
@@ -38,6 +43,15 @@ class Desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "T", "H", "dk", "dv", "chunk", "io_dtype", "gate_dtype", "alpha_mode",
                  "beta_mode", "flags")]
+
+
+class QkDesc(ctypes.Structure):
+    """Mirror of ``gdr_qk_desc``."""
+
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hk", "d", "io_dtype", "weight_dtype", "norm", "rot_layout",
+                                               "rot_dim")]
+                + [(n, ctypes.c_float) for n in ("eps", "q_scale", "rot_scale")]
+                + [(n, ctypes.c_int64) for n in ("ldq", "ldk")])
 
 
 if not os.path.exists(LIB_PATH):
@@ -83,12 +97,31 @@ _lib.gdr_context_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
 _lib.gdr_context_create.restype = ctypes.c_int
 _lib.gdr_context_destroy.argtypes = [_vp]
 _lib.gdr_context_destroy.restype = ctypes.c_int
+_qp = ctypes.POINTER(QkDesc)
+_i64 = ctypes.c_int64
+_lib.gdr_qk_prep_fwd.argtypes = [_qp] + [_vp] * 8 + [_vp]
+_lib.gdr_qk_prep_fwd.restype = ctypes.c_int
+_lib.gdr_qk_prep_bwd_workspace_size.argtypes = [_qp]
+_lib.gdr_qk_prep_bwd_workspace_size.restype = ctypes.c_size_t
+_lib.gdr_qk_prep_bwd.argtypes = [_qp] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
+_lib.gdr_qk_prep_bwd.restype = ctypes.c_int
+_lib.gdr_scan_workspace_size.argtypes = [_dp]
+_lib.gdr_scan_workspace_size.restype = ctypes.c_size_t
+_rows = [_vp, _i64] * 3  # x, alpha, beta with their strides
+_lib.gdr_scan_fwd.argtypes = [_dp] + _rows + [_vp, ctypes.c_int32] + [_vp] * 4 + [_vp, ctypes.c_size_t, _vp]
+_lib.gdr_scan_fwd.restype = ctypes.c_int
+_lib.gdr_scan_bwd.argtypes = [_dp] + _rows + [_vp, ctypes.c_int32] + [_vp] * 8 + [_vp, ctypes.c_size_t, _vp]
+_lib.gdr_scan_bwd.restype = ctypes.c_int
+_lib.gdr_scan_step.argtypes = [_dp] + _rows + [_vp] * 2 + [_vp]
+_lib.gdr_scan_step.restype = ctypes.c_int
 
 EXPORTED = ("gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd", "gdr_decode_step", "gdr_chunk_fwd_path",
             "gdr_status_string", "gdr_version", "gdr_chunk_fwd_ckpt", "gdr_mc_readout_workspace_size",
             "gdr_mc_readout", "gdr_osdn_precond_workspace_size", "gdr_osdn_precond",
             "gdr_sdm_workspace_size", "gdr_sdm_fwd", "gdr_context_create", "gdr_context_destroy",
-            "gdr_chunk_fwd_noalloc", "gdr_dmem_fwd", "gdr_chunk_fwd_ctx")
+            "gdr_chunk_fwd_noalloc", "gdr_dmem_fwd", "gdr_chunk_fwd_ctx", "gdr_qk_prep_fwd",
+            "gdr_qk_prep_bwd_workspace_size", "gdr_qk_prep_bwd", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_bwd",
+            "gdr_scan_step")
 
 
 class GdrError(RuntimeError):
@@ -355,6 +388,123 @@ def gdr_decode_step(desc: Desc, q, k, k_w, v, alpha, beta_k, beta_v, S, o, strea
                                     _ptr(beta_k), _ptr(beta_v), _ptr(S), _ptr(o), _stream(stream)))
 
 
+def _row_stride(name: str, t: torch.Tensor, inner: int) -> int:
+    """Elements between successive tokens of a tensor [..., heads, channels] whose last two
+    axes are dense and whose leading axes step evenly (a dense tensor, or a slice of a fused
+    projection's output); ValueError for any other strides, which the library cannot read."""
+    if t.is_contiguous():
+        return inner
+    size, stride = t.shape, t.stride()
+    if size[-1] > 1 and stride[-1] != 1 or size[-2] > 1 and stride[-2] != size[-1]:
+        raise ValueError(f"{name}: heads and channels must be dense, got strides {stride}")
+    ld, rows = 0, 1  # rows walked so far, from the last leading axis out
+    for n, s in zip(reversed(size[:-2]), reversed(stride[:-2])):
+        if n > 1:
+            if rows == 1:
+                ld = s
+            elif s != rows * ld:
+                raise ValueError(f"{name}: batch and token axes must step evenly, got strides {stride}")
+            rows *= n
+    if rows > 1 and ld < inner:
+        raise ValueError(f"{name}: overlapping tokens, got strides {stride}")
+    return ld if rows > 1 else inner
+
+
+def _addr(name: str, t, ld: int, inner: int):
+    """Device address of a tensor of rows `ld` elements apart (0: dense)."""
+    if isinstance(t, torch.Tensor) and t.numel():
+        if t.dim() < 3:
+            raise ValueError(f"{name}: expected heads and channels as the last two axes, got shape {tuple(t.shape)}")
+        have = _row_stride(name, t, inner)
+        if t.numel() > inner and have != (int(ld) or inner):
+            raise ValueError(f"{name}: tokens are {have} elements apart, not {int(ld) or inner}")
+    return None if t is None else t.data_ptr()
+
+
+def _check_qk(desc: QkDesc, specs) -> None:
+    if desc.io_dtype not in _TORCH_DTYPE or desc.weight_dtype not in _TORCH_DTYPE or min(
+            desc.B, desc.T, desc.Hq, desc.Hk, desc.d, desc.rot_dim) < 0:
+        return  # the library rejects the descriptor itself
+    n, io, wt = desc.B * desc.T, _TORCH_DTYPE[desc.io_dtype], _TORCH_DTYPE[desc.weight_dtype]
+    kind = {"q": (n * desc.Hq * desc.d, io), "k": (n * desc.Hk * desc.d, io), "w": (desc.d, wt),
+            "positions": (n, torch.int32), "inv_freq": (desc.rot_dim // 2, torch.float64), "dw": (desc.d, torch.float32)}
+    _check_all([(name, t) + kind[what] for name, what, t in specs])
+
+
+def gdr_qk_prep_fwd(desc: QkDesc, q, k, wq, wk, positions, inv_freq, q_out, k_out, stream=None) -> int:
+    _check_qk(desc, [("q", "q", q), ("k", "k", k), ("wq", "w", wq), ("wk", "w", wk), ("positions", "positions", positions),
+                     ("inv_freq", "inv_freq", inv_freq), ("q_out", "q", q_out), ("k_out", "k", k_out)])
+    return int(_lib.gdr_qk_prep_fwd(ctypes.byref(desc), _addr("q", q, desc.ldq, desc.Hq * desc.d),
+                                    _addr("k", k, desc.ldk, desc.Hk * desc.d), _ptr(wq), _ptr(wk), _ptr(positions),
+                                    _ptr(inv_freq), _ptr(q_out), _ptr(k_out), _stream(stream)))
+
+
+def gdr_qk_prep_bwd_workspace_size(desc: QkDesc) -> int:
+    return int(_lib.gdr_qk_prep_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def gdr_qk_prep_bwd(desc: QkDesc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                    workspace_bytes: int, stream=None) -> int:
+    _check_qk(desc, [("q", "q", q), ("k", "k", k), ("wq", "w", wq), ("wk", "w", wk), ("positions", "positions", positions),
+                     ("inv_freq", "inv_freq", inv_freq), ("dq_out", "q", dq_out), ("dk_out", "k", dk_out), ("dq", "q", dq),
+                     ("dk", "k", dk), ("dwq", "dw", dwq), ("dwk", "dw", dwk)])
+    _check_workspace(workspace, workspace_bytes)
+    return int(_lib.gdr_qk_prep_bwd(ctypes.byref(desc), _addr("q", q, desc.ldq, desc.Hq * desc.d),
+                                    _addr("k", k, desc.ldk, desc.Hk * desc.d), _ptr(wq), _ptr(wk), _ptr(positions),
+                                    _ptr(inv_freq), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
+                                    _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def gdr_scan_workspace_size(desc: Desc) -> int:
+    return int(_lib.gdr_scan_workspace_size(ctypes.byref(desc)))
+
+
+def _check_scan(desc: Desc, rows: int, n_seq, specs) -> None:  # n_seq: None where the rows are not packed
+    io, gt = _io(desc)
+    if io is None or min(desc.B, desc.T, desc.H, desc.dv, int(n_seq or 0)) < 0:
+        return  # the library rejects the descriptor itself
+    D = desc.H * desc.dv
+    blocks = (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK
+    kind = {"io": (rows * D, io), "gate": (rows * D, gt), "state": ((desc.B if n_seq is None else int(n_seq)) * D, torch.float32),
+            "ckpt": (desc.B * blocks * D, torch.float32), "seq_off": (int(n_seq or 0) + 1, torch.int32)}
+    _check_all([(name, t) + kind[what] for name, what, t in specs])
+
+
+def _scan_rows(desc: Desc, x, ldx, alpha, lda, beta, ldb):
+    D = desc.H * desc.dv
+    return (_addr("x", x, ldx, D), int(ldx), _addr("alpha", alpha, lda, D), int(lda), _addr("beta", beta, ldb, D), int(ldb))
+
+
+def gdr_scan_fwd(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, seq_off, n_seq: int, S0, y, ST, ckpt, workspace,
+                 workspace_bytes: int, stream=None) -> int:
+    _check_scan(desc, desc.B * desc.T, n_seq if seq_off is not None else None, [
+        ("x", "io", x), ("alpha", "gate", alpha), ("beta", "gate", beta), ("y", "io", y), ("S0", "state", S0),
+        ("ST", "state", ST), ("ckpt", "ckpt", ckpt), ("seq_off", "seq_off", seq_off)])
+    _check_workspace(workspace, workspace_bytes)
+    return int(_lib.gdr_scan_fwd(ctypes.byref(desc), *_scan_rows(desc, x, ldx, alpha, lda, beta, ldb), _ptr(seq_off),
+                                 int(n_seq), _ptr(S0), _ptr(y), _ptr(ST), _ptr(ckpt), _ptr(workspace), int(workspace_bytes),
+                                 _stream(stream)))
+
+
+def gdr_scan_bwd(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, seq_off, n_seq: int, S0, ckpt, dy, dST, dx,
+                 dalpha, dbeta, dS0, workspace, workspace_bytes: int, stream=None) -> int:
+    _check_scan(desc, desc.B * desc.T, n_seq if seq_off is not None else None, [
+        ("x", "io", x), ("alpha", "gate", alpha), ("beta", "gate", beta), ("dy", "io", dy), ("dx", "io", dx),
+        ("dalpha", "gate", dalpha), ("dbeta", "gate", dbeta), ("S0", "state", S0), ("dST", "state", dST),
+        ("dS0", "state", dS0), ("ckpt", "ckpt", ckpt), ("seq_off", "seq_off", seq_off)])
+    _check_workspace(workspace, workspace_bytes)
+    return int(_lib.gdr_scan_bwd(ctypes.byref(desc), *_scan_rows(desc, x, ldx, alpha, lda, beta, ldb), _ptr(seq_off),
+                                 int(n_seq), _ptr(S0), _ptr(ckpt), _ptr(dy), _ptr(dST), _ptr(dx), _ptr(dalpha), _ptr(dbeta),
+                                 _ptr(dS0), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def gdr_scan_step(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, S, y, stream=None) -> int:
+    _check_scan(desc, desc.B, None, [("x", "io", x), ("alpha", "gate", alpha), ("beta", "gate", beta), ("y", "io", y),
+                                  ("S", "state", S)])
+    return int(_lib.gdr_scan_step(ctypes.byref(desc), *_scan_rows(desc, x, ldx, alpha, lda, beta, ldb), _ptr(S), _ptr(y),
+                                  _stream(stream)))
+
+
 # ---------------------------------------------------------------------------
 # convenience wrappers (allocate outputs, raise on error)
 # ---------------------------------------------------------------------------
@@ -507,6 +657,176 @@ def decode_step(S, q, k, v, alpha, beta_k, *, k_w=None, beta_v=None, out=None, f
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_decode_step")
     return o
+
+
+def rope_inv_freq(rot_dim, *, base=10000.0, scaling=None, factor=1.0, original_len=None, fast=32.0, slow=1.0, device="cuda"):
+    """Frequencies of the rotation, ``inv_freq`` [rot_dim / 2] fp64, and ``rot_scale``, for qk_prep.
+
+    Plain: f_i = base^(-2 i / rot_dim), scale 1.  For contexts `factor` times longer than the
+    `original_len` tokens that a model was trained on, `scaling`:
+      "linear"  every frequency divided by the factor (positions interpolated);
+      "ntk"     the base raised by factor^(rot_dim / (rot_dim - 2)), which divides the lowest frequency by the
+                factor and leaves the highest as it is;
+      "yarn"    by wavelength: frequencies that turn more than `fast` times over original_len stay, those that
+                turn less than `slow` times are divided by the factor, those between are mixed linearly in the
+                channel's index; scale 0.1 ln(factor) + 1.
+    """
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and not negative, got {rot_dim}")
+    if not base > 0 or not factor >= 1:
+        raise ValueError(f"base must be positive and factor at least 1, got {base} and {factor}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f, scale = base ** (-2.0 * i / max(rot_dim, 1)), 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_len is None or not original_len > 0 or not fast > slow > 0:
+            raise ValueError("yarn needs original_len > 0 and fast > slow > 0")
+        # the (real) channel index whose frequency turns n times over original_len
+        at = lambda n: rot_dim * math.log(original_len / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot_dim - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f, scale = f * (1 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
+    return f.to(device), scale
+
+
+_NORMS = {None: GDR_NORM_NONE, "none": GDR_NORM_NONE, "l2": GDR_NORM_L2, "rms": GDR_NORM_RMS}
+_LAYOUTS = {"half": GDR_ROT_HALF, "interleaved": GDR_ROT_INTERLEAVED}
+
+
+def _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale) -> QkDesc:
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be None, 'none', 'l2' or 'rms', got {norm!r}")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3] or q.dtype != k.dtype:
+        raise ValueError(f"expected q [B, T, Hq, d] and k [B, T, Hk, d] of one type, got {tuple(q.shape)} {q.dtype} and "
+                         f"{tuple(k.shape)} {k.dtype}")
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise ValueError(f"wq and wk must have one type, got {wq.dtype} and {wk.dtype}")
+    B, T, Hq, d = q.shape
+    Hk = k.shape[2]
+    w = wq if wq is not None else wk
+    return QkDesc(B, T, Hq, Hk, d, _dtype_code(q), GDR_F32 if w is None else _dtype_code(w), _NORMS[norm], _LAYOUTS[layout],
+                  0 if inv_freq is None else 2 * inv_freq.numel(), eps, q_scale, rot_scale,
+                  _row_stride("q", q, Hq * d) if q.numel() else 0, _row_stride("k", k, Hk * d) if k.numel() else 0)
+
+
+def qk_prep(q, k, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv_freq=None, layout="half", rot_scale=1.0,
+            q_scale=1.0, out=None, stream=None):
+    """Norm of every head of q [B, T, Hq, d] and k [B, T, Hk, d] and the rotation by position, in one pass.
+
+    norm None, "l2" or "rms" with optional weights wq, wk [d]; inv_freq [rot_dim / 2] fp64 (rope_inv_freq) rotates the
+    first rot_dim channels by positions [B, T] int32 (default 0 .. T - 1), in the "half" or "interleaved" layout, times
+    rot_scale; q is multiplied by q_scale.  q and k may be slices of a fused projection's output.  Returns (q, k), dense;
+    `out` a pair of tensors to write instead (q, k themselves where dense)."""
+    desc = _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale)
+    qo, ko = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                                          torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    rc = gdr_qk_prep_fwd(desc, q, k, wq, wk, positions, inv_freq, qo, ko, stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_qk_prep_fwd")
+    return qo, ko
+
+
+def qk_prep_bwd(q, k, dq_out, dk_out, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv_freq=None,
+                layout="half", rot_scale=1.0, q_scale=1.0, workspace=None, stream=None):
+    """Backward pass of qk_prep, from its inputs and the (dense) gradients of its outputs.
+    Returns (dq, dk, dwq, dwk): dense gradients in q's type, weight gradients [d] in fp32 or None."""
+    desc = _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale)
+    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    dwq, dwk = (None if w is None else torch.empty(desc.d, dtype=torch.float32, device=q.device) for w in (wq, wk))
+    if dwq is not None or dwk is not None:
+        workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device)
+    rc = gdr_qk_prep_bwd(desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                         _nbytes(workspace), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_qk_prep_bwd")
+    return dq, dk, dwq, dwk
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _room(workspace, need: int, device):
+    """`workspace` where it holds `need` bytes, else a new one (None for 0)."""
+    return torch.empty(need, dtype=torch.uint8, device=device) if need and _nbytes(workspace) < need else workspace
+
+
+def _scan_desc(x, alpha, log_gate, coupled, step=False) -> Desc:
+    if x.dim() != (3 if step else 4) or alpha.shape != x.shape:
+        raise ValueError(f"expected x and alpha [B, {'' if step else 'T, '}H, dv], got {tuple(x.shape)} and {tuple(alpha.shape)}")
+    H, dv = x.shape[-2:]
+    flags = (GDR_FLAG_LOG_GATE if log_gate else 0) | (GDR_FLAG_COUPLED if coupled else 0)
+    return Desc(x.shape[0], 1 if step else x.shape[1], H, 1, dv, 64, _dtype_code(x), _dtype_code(alpha), GDR_ALPHA_CHANNEL, 0,
+                flags)
+
+
+def _strides(desc: Desc, x, alpha, beta):
+    D = desc.H * desc.dv
+    return tuple(0 if t is None or not t.numel() else _row_stride(n, t, D) for n, t in
+                 (("x", x), ("alpha", alpha), ("beta", beta)))
+
+
+def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq_offsets=None, want_state=True,
+             want_ckpt=False, workspace=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + b_t x_t over x [B, T, H, dv], y = h.
+
+    a = alpha [B, T, H, dv] (or exp(alpha) with log_gate); b = beta where given, 1 - a with coupled, else 1.
+    seq_offsets [n + 1] int32 cuts the T rows of a B = 1 batch into packed sequences; S0 [B or n, H, dv] fp32.
+    Returns (y like x, ST like S0 or None, ckpt [B, ceil(T / 512), H, dv] fp32 for scan_bwd or None).  Rows of y that
+    belong to no packed sequence are left unwritten."""
+    desc = _scan_desc(x, alpha, log_gate, coupled)
+    n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
+    H, dv, dev = desc.H, desc.dv, x.device
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    ST = torch.empty((desc.B if seq_offsets is None else n_seq, H, dv), dtype=torch.float32, device=dev) if want_state else None
+    ckpt = (torch.empty((desc.B, (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK, H, dv), dtype=torch.float32, device=dev)
+            if want_ckpt else None)
+    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
+    ldx, lda, ldb = _strides(desc, x, alpha, beta)
+    rc = gdr_scan_fwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, y, ST, ckpt, workspace, _nbytes(workspace),
+                      stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_scan_fwd")
+    return y, ST, ckpt
+
+
+def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0=None, dST=None, seq_offsets=None,
+             workspace=None, stream=None):
+    """Backward pass of scan_fwd with its inputs and its ckpt (None where T <= 512): gradients dy of y (dense) and
+    dST of ST.  Returns (dx, dalpha, dbeta or None, dS0): dalpha is the gradient of alpha as stored."""
+    desc = _scan_desc(x, alpha, log_gate, coupled)
+    n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
+    dev = x.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dalpha = torch.empty(x.shape, dtype=alpha.dtype, device=dev)
+    dbeta = None if beta is None else torch.empty(x.shape, dtype=alpha.dtype, device=dev)
+    dS0 = torch.empty((desc.B if seq_offsets is None else n_seq, desc.H, desc.dv), dtype=torch.float32, device=dev)
+    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
+    ldx, lda, ldb = _strides(desc, x, alpha, beta)
+    rc = gdr_scan_bwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, ckpt, dy, dST, dx, dalpha, dbeta, dS0,
+                      workspace, _nbytes(workspace), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_scan_bwd")
+    return dx, dalpha, dbeta, dS0
+
+
+def scan_step(S, x, alpha, *, beta=None, log_gate=False, coupled=False, out=None, stream=None):
+    """One token of the recurrence for every sequence: x, alpha, beta [B, H, dv]; S [B, H, dv] fp32 is updated in
+    place.  Returns y [B, H, dv]."""
+    desc = _scan_desc(x, alpha, log_gate, coupled, step=True)
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ldx, lda, ldb = _strides(desc, x, alpha, beta)
+    rc = gdr_scan_step(desc, x, ldx, alpha, lda, beta, ldb, S, y, stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_scan_step")
+    return y
 
 
 def loaded_library_path() -> str:

@@ -1,0 +1,370 @@
+// qk_prep.hip -- norms of queries and keys per head with the position rotation in the same
+// pass, and its backward pass (include/gdr.h: gdr_qk_prep_fwd, gdr_qk_prep_bwd).
+//
+// One row x in R^d per (token, head).  Forward, with kappa = 1 (L2) or 1/d (RMS):
+//     r = (kappa sum x^2 + eps)^{-1/2}   (0 where the bracket is 0; 1 without a norm)
+//     n = r w (.) x,   out = scale Rot_pos(n)
+// Rot turns channel pair i < rot/2 by theta = pos f_i and multiplies it by rot_scale.
+// Backward, from g = d loss / d out:
+//     m = scale Rot_pos^T(g),  t = w (.) m,  dw = sum over rows r m (.) x
+//     dx = r t - kappa r^3 (t . x) x
+//
+// Bound by HBM (forward 2 and backward 3 passes over the heads, under 10 operations per
+// byte), so the layout serves the loads.  Rotated channels are held as pairs: a lane owns
+// VP consecutive pairs of a row, read as 16-byte vectors from the two places where the
+// pairs' members lie, so the rotation needs no exchange between lanes; P = 2^k lanes hold
+// a row and only the norm's sum crosses lanes (log2 P xor shuffles).  A group of P lanes
+// works on up to `rows` heads of one token, so that the token's cosines and sines, held in
+// registers, are formed once for them.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr_device.hpp"
+#include "gdr_internal.hpp"
+#include "gdr_mfma.hpp"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Vectors of N elements from element-aligned addresses (the hardware takes any dword or
+// wider global access at any byte address).
+template <int BYTES> struct Words;
+template <> struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2))); };
+template <> struct Words<16> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+
+template <bool BF, int N>
+__device__ __forceinline__ void load_n(const void *base, long at, float (&f)[N]) {
+    if constexpr (BF) {
+        if constexpr (N == 16) {
+            const auto *p = reinterpret_cast<const Words<16>::type *>(static_cast<const uint16_t *>(base) + at);
+            const Words<16>::type a = p[0], b = p[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(a[i] << 16);
+                f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+                f[8 + 2 * i] = __uint_as_float(b[i] << 16);
+                f[8 + 2 * i + 1] = __uint_as_float(b[i] & 0xffff0000u);
+            }
+        } else {
+            const typename Words<2 * N>::type a =
+                *reinterpret_cast<const typename Words<2 * N>::type *>(static_cast<const uint16_t *>(base) + at);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                f[2 * i] = __uint_as_float(a[i] << 16);
+                f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            const Words<16>::type a = *reinterpret_cast<const Words<16>::type *>(static_cast<const float *>(base) + at + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[k + i] = __uint_as_float(a[i]);
+        }
+    }
+}
+
+template <bool BF, int N>
+__device__ __forceinline__ void store_n(void *base, long at, const float (&f)[N]) {
+    if constexpr (BF) {
+#pragma unroll
+        for (int k = 0; k < N; k += 8) {
+            constexpr int M = N < 8 ? N : 8;
+            typename Words<2 * M>::type a;
+#pragma unroll
+            for (int i = 0; i < M / 2; ++i) a[i] = pk_bf16(f[k + 2 * i], f[k + 2 * i + 1]);
+            *reinterpret_cast<typename Words<2 * M>::type *>(static_cast<uint16_t *>(base) + at + k) = a;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            Words<16>::type a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(f[k + i]);
+            *reinterpret_cast<Words<16>::type *>(static_cast<float *>(base) + at + k) = a;
+        }
+    }
+}
+
+// Where a lane's pairs lie in the row.
+//   kAdjacent  members side by side (interleaved rotation, or none): 2 VP elements at 2 i
+//   kSplit     VP elements at one place and VP at another (half rotation whose rot / 2 is
+//              a multiple of VP; lanes past it hold channels that are not rotated)
+//   kScattered each member at a place of its own (half rotation, any even rot)
+enum Layout { kAdjacent = 0, kSplit = 1, kScattered = 2 };
+
+template <bool BF, int VP, int LAY>
+struct Row {
+    int at[2];      // kAdjacent: [0]; kSplit: both
+    int i0, half;   // kScattered
+    __device__ __forceinline__ void place(int pair0, int half_, int) {
+        i0 = pair0;
+        half = half_;
+        if (LAY == kSplit && pair0 < half_) {
+            at[0] = pair0;
+            at[1] = pair0 + half_;
+        } else {
+            at[0] = 2 * pair0;
+            at[1] = 2 * pair0 + VP;
+        }
+    }
+    __device__ __forceinline__ int member(int j, int second) const {
+        const int i = i0 + j;
+        return i < half ? i + (second ? half : 0) : 2 * i + second;
+    }
+    __device__ __forceinline__ void load(const void *base, long row, float (&e)[VP], float (&o)[VP]) const {
+        if constexpr (LAY == kAdjacent) {
+            float f[2 * VP];
+            load_n<BF, 2 * VP>(base, row + at[0], f);
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                e[j] = f[2 * j];
+                o[j] = f[2 * j + 1];
+            }
+        } else if constexpr (LAY == kSplit) {
+            load_n<BF, VP>(base, row + at[0], e);
+            load_n<BF, VP>(base, row + at[1], o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                e[j] = ld_elem(base, row + member(j, 0), BF);
+                o[j] = ld_elem(base, row + member(j, 1), BF);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *base, long row, const float (&e)[VP], const float (&o)[VP]) const {
+        if constexpr (LAY == kAdjacent) {
+            float f[2 * VP];
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                f[2 * j] = e[j];
+                f[2 * j + 1] = o[j];
+            }
+            store_n<BF, 2 * VP>(base, row + at[0], f);
+        } else if constexpr (LAY == kSplit) {
+            store_n<BF, VP>(base, row + at[0], e);
+            store_n<BF, VP>(base, row + at[1], o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                st_elem(base, row + member(j, 0), e[j], BF);
+                st_elem(base, row + member(j, 1), o[j], BF);
+            }
+        }
+    }
+    // channel of pair j's first / second member
+    __device__ __forceinline__ int channel(int j, int second) const {
+        if constexpr (LAY == kAdjacent) return at[0] + 2 * j + second;
+        if constexpr (LAY == kSplit) return at[second] + j;
+        return member(j, second);
+    }
+};
+
+// sum over the P lanes of a row (P a power of two)
+__device__ __forceinline__ float row_sum(float x, int P) {
+    for (int s = 1; s < P; s <<= 1) x += __shfl_xor(x, s);
+    return x;
+}
+
+// Cosine and sine of pos * f for the lane's pairs, times rot_scale; pairs past the rotated
+// part get 1 and 0.  The angle is formed and reduced to a fraction of a turn in 64 bits: at
+// position 10^6 its 32-bit product would be off by 0.06.
+template <int VP>
+__device__ __forceinline__ void angles(const QkParams &p, long token, int i0, float (&c)[VP], float (&s)[VP]) {
+    const int half = p.rot / 2;
+    const double pos = p.pos ? (double)p.pos[token] : (double)(token % p.T);
+#pragma unroll
+    for (int j = 0; j < VP; ++j) {
+        c[j] = 1.f;
+        s[j] = 0.f;
+        if (i0 + j < half) {
+            double turn = pos * p.inv_freq[i0 + j] * 0.15915494309189535;
+            turn -= rint(turn);
+            float sn, cs;
+            sincospif(2.f * (float)turn, &sn, &cs);
+            c[j] = cs * p.rot_scale;
+            s[j] = sn * p.rot_scale;
+        }
+    }
+}
+
+// r of one row from its sum of squares (already over the P lanes)
+__device__ __forceinline__ float inverse_norm(const QkParams &p, float ss) {
+    if (p.norm == 0) return 1.f;
+    const float m = fmaf(p.kappa, ss, p.eps);
+    return m > 0.f || m != m ? 1.f / sqrtf(m) : 0.f;
+}
+
+template <bool BF, int VP, int LAY, bool BWD>
+__global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
+    const bool isk = blockIdx.x >= (unsigned)p.blocks_q;
+    const QkTensor &X = isk ? p.k : p.q;
+    const long block = isk ? (long)blockIdx.x - p.blocks_q : blockIdx.x;
+    const long nblocks = isk ? p.blocks_k : p.blocks_q;
+    const int P = p.lanes, groups = kThreads / P;
+    const int gl = threadIdx.x / P, lane = threadIdx.x % P;
+    const int i0 = lane * VP;
+    const bool holds = i0 < p.d / 2;  // lanes past the row only take part in the sums
+    Row<BF, VP, LAY> at;
+    at.place(holds ? i0 : 0, p.rot / 2, p.d);
+    float we[VP], wo[VP], ae[VP], ao[VP];
+#pragma unroll
+    for (int j = 0; j < VP; ++j) {
+        we[j] = X.w ? ld_elem(X.w, at.channel(j, 0), p.w_bf16) : 1.f;
+        wo[j] = X.w ? ld_elem(X.w, at.channel(j, 1), p.w_bf16) : 1.f;
+        ae[j] = ao[j] = 0.f;
+    }
+    const long items = p.tokens * X.slices;
+    for (long item = block * groups + gl; item < items; item += nblocks * groups) {
+        const long token = item / X.slices;
+        const int h0 = (int)(item % X.slices) * p.rows, h1 = min(h0 + p.rows, X.H);
+        float c[VP], s[VP];
+        angles<VP>(p, token, holds ? i0 : p.d, c, s);
+        for (int h = h0; h < h1; ++h) {
+            const long in = token * X.ld + (long)h * p.d, out = (token * X.H + h) * p.d;
+            float e[VP], o[VP];
+            at.load(X.x, in, e, o);
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < VP; ++j) ss = fmaf(e[j], e[j], fmaf(o[j], o[j], ss));
+            if (!holds) ss = 0.f;
+            const float r = inverse_norm(p, row_sum(ss, P));
+            if constexpr (!BWD) {
+                const float rs = r * X.scale;
+#pragma unroll
+                for (int j = 0; j < VP; ++j) {
+                    const float ne = e[j] * rs * we[j], no = o[j] * rs * wo[j];
+                    e[j] = c[j] * ne - s[j] * no;
+                    o[j] = s[j] * ne + c[j] * no;
+                }
+            } else {
+                float ge[VP], go[VP];
+                at.load(X.g, out, ge, go);
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < VP; ++j) {
+                    const float me = X.scale * (c[j] * ge[j] + s[j] * go[j]);
+                    const float mo = X.scale * (c[j] * go[j] - s[j] * ge[j]);
+                    const float xe = r * e[j], xo = r * o[j];
+                    ae[j] = fmaf(me, xe, ae[j]);
+                    ao[j] = fmaf(mo, xo, ao[j]);
+                    ge[j] = me * we[j];
+                    go[j] = mo * wo[j];
+                    dot = fmaf(ge[j], xe, fmaf(go[j], xo, dot));
+                    e[j] = xe;
+                    o[j] = xo;
+                }
+                if (!holds) dot = 0.f;
+                dot = p.kappa * row_sum(dot, P);
+#pragma unroll
+                for (int j = 0; j < VP; ++j) {
+                    e[j] = r * fmaf(-dot, e[j], ge[j]);
+                    o[j] = r * fmaf(-dot, o[j], go[j]);
+                }
+            }
+            if (holds) at.store(X.out, out, e, o);
+        }
+    }
+    if constexpr (BWD) {
+        if (!X.dw) return;  // uniform over the workgroup
+        __shared__ float sum[kThreads / 64][256];
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+            for (int k = P; k < 64; k <<= 1) {
+                ae[j] += __shfl_xor(ae[j], k);
+                ao[j] += __shfl_xor(ao[j], k);
+            }
+            if (holds && (threadIdx.x & 63) < P) {
+                sum[wave][at.channel(j, 0)] = ae[j];
+                sum[wave][at.channel(j, 1)] = ao[j];
+            }
+        }
+        __syncthreads();
+        for (int ch = threadIdx.x; ch < p.d; ch += kThreads) {
+            float a = 0.f;
+            for (int w = 0; w < kThreads / 64; ++w) a += sum[w][ch];
+            p.partial[(long)blockIdx.x * p.d + ch] = a;
+        }
+    }
+}
+
+// The workgroups' sums of the weight gradients, in the order of the workgroups: 16 channels
+// per block, 16 threads per channel.
+__global__ void __launch_bounds__(256) qk_weight_kernel(QkParams p) {
+    __shared__ float part[16][17];
+    const bool isk = blockIdx.y != 0;
+    float *dw = isk ? p.k.dw : p.q.dw;
+    if (!dw) return;
+    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4, ch = blockIdx.x * 16 + cl;
+    const long first = isk ? p.blocks_q : 0, n = isk ? p.blocks_k : p.blocks_q;
+    float a = 0.f;
+    if (ch < p.d)
+        for (long b = rl; b < n; b += 16) a += p.partial[(first + b) * p.d + ch];
+    part[rl][cl] = a;
+    __syncthreads();
+    if (rl == 0 && ch < p.d) {
+        for (int k = 1; k < 16; ++k) a += part[k][cl];
+        dw[ch] = a;
+    }
+}
+
+template <bool BF, int VP, bool BWD>
+const void *pick_layout(int lay) {
+    switch (lay) {
+    case kAdjacent: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, VP, kAdjacent, BWD>);
+    case kSplit: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, VP, kSplit, BWD>);
+    default: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, VP, kScattered, BWD>);
+    }
+}
+
+constexpr int kMaxBlocks = 1024;  // workgroups per tensor of a backward pass
+
+// Lanes, heads per group and workgroups of one call.
+void plan(QkParams &p, bool bwd, int &vp, int &lay) {
+    const int half = p.rot / 2;
+    vp = 4;
+    lay = !p.half_layout || half == 0 ? kAdjacent : (half % vp == 0 ? kSplit : kScattered);
+    p.lanes = 1;
+    while (p.lanes * vp < p.d / 2) p.lanes <<= 1;
+    p.rows = 8;
+    const int groups = kThreads / p.lanes;
+    QkTensor *all[] = {&p.q, &p.k};
+    long blocks[2];
+    for (int i = 0; i < 2; ++i) {
+        all[i]->slices = (all[i]->H + p.rows - 1) / p.rows;
+        blocks[i] = (p.tokens * all[i]->slices + groups - 1) / groups;
+        if (bwd && blocks[i] > kMaxBlocks) blocks[i] = kMaxBlocks;
+    }
+    p.blocks_q = (int)blocks[0];
+    p.blocks_k = (int)blocks[1];
+}
+
+}  // namespace
+
+size_t qk_prep_bwd_workspace(const QkParams &p0) {
+    QkParams p = p0;
+    int vp, lay;
+    plan(p, true, vp, lay);
+    return (size_t)(p.blocks_q + p.blocks_k) * p.d * sizeof(float);
+}
+
+hipError_t launch_qk_prep(const QkParams &p0, bool bwd, hipStream_t s) {
+    QkParams p = p0;
+    int vp, lay;
+    plan(p, bwd, vp, lay);
+    const long blocks = (long)p.blocks_q + p.blocks_k;
+    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    void *args[] = {&p};
+    const void *fn = p.io_bf16 ? (bwd ? pick_layout<true, 4, true>(lay) : pick_layout<true, 4, false>(lay))
+                               : (bwd ? pick_layout<false, 4, true>(lay) : pick_layout<false, 4, false>(lay));
+    hipError_t e = blocks > 0 ? hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(kThreads), args, 0, s) : hipSuccess;
+    if (e == hipSuccess && bwd && (p.q.dw || p.k.dw))
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&qk_weight_kernel), dim3((unsigned)((p.d + 15) / 16), 2),
+                            dim3(256), args, 0, s);
+    return e;
+}
+
+}  // namespace gdr

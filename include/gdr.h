@@ -92,6 +92,12 @@ typedef enum gdr_beta_mode { GDR_BETA_SCALAR = 0, GDR_BETA_SHARED = 1, GDR_BETA_
 #define GDR_FLAG_READ_BEFORE_WRITE 0x10
 #define GDR_FLAG_UNDECAYED_PREDICTION 0x20
 
+/* Flags of the gated linear recurrence (gdr_scan_fwd, gdr_scan_bwd, gdr_scan_step) only:
+ *   LOG_GATE:   alpha holds the logarithm of the decay, a = exp(alpha); -inf is a decay of 0
+ *   COUPLED:    the input factor is b = 1 - a (beta must be NULL) */
+#define GDR_FLAG_LOG_GATE 0x40
+#define GDR_FLAG_COUPLED 0x80
+
 /* Problem descriptor.
  *   B, H  >= 0; T >= 0 (prefill only; ignored by decode).
  *   dk, dv: multiples of 8 in [8, 128]                      (else GDR_EUNSUPPORTED)
@@ -358,6 +364,138 @@ int gdr_sdm_fwd(const gdr_desc *desc, int32_t n, int32_t W, int32_t R, const flo
  */
 int gdr_dmem_fwd(const gdr_desc *desc, int32_t J, const void *q, const void *k, const void *v, const void *lam,
                  const void *beta, const uint8_t *seg_end, float *M, void *out, void *stream);
+
+/*
+ * Query and key preparation: the norm of every head and the rotation by the token's
+ * position, in one pass over q and k; what gdr_chunk_fwd and gdr_decode_step read as q
+ * and k.  For each row x (d channels of one head of one token)
+ *
+ *     r   = (sum x^2 + eps)^(-1/2)         GDR_NORM_L2
+ *           (mean x^2 + eps)^(-1/2)        GDR_NORM_RMS
+ *           1                              GDR_NORM_NONE
+ *     n   = r w (.) x                      w = 1 when the weight is NULL; r = 0 where its
+ *                                          bracket is 0 (a zero row with eps = 0)
+ *     out = s R n                          s = q_scale for q, 1 for k
+ *
+ * R turns the channel pairs i < rot_dim / 2 of the first rot_dim channels by the angle
+ * positions[b, t] * inv_freq[i] and multiplies them by rot_scale,
+ *     (e, o) -> rot_scale (cos e - sin o, sin e + cos o)
+ * with e, o the channels (i, i + rot_dim / 2) for GDR_ROT_HALF and (2i, 2i + 1) for
+ * GDR_ROT_INTERLEAVED; the channels from rot_dim on are not rotated.  Angles are formed
+ * and reduced in 64 bits, so far positions lose nothing.  Frequencies scaled for long
+ * contexts are the caller's inv_freq and rot_scale.
+ */
+typedef enum gdr_norm { GDR_NORM_NONE = 0, GDR_NORM_L2 = 1, GDR_NORM_RMS = 2 } gdr_norm;
+typedef enum gdr_rot_layout { GDR_ROT_HALF = 0, GDR_ROT_INTERLEAVED = 1 } gdr_rot_layout;
+
+/* Descriptor of a query / key preparation.
+ *   B, T >= 0, B * T < 2^30; Hq, Hk in [0, 65536], Hq != Hk allowed, 0 leaves that tensor out
+ *   d        multiple of 8 in [8, 256]                     (else GDR_EUNSUPPORTED)
+ *   rot_dim  even, 0 (no rotation) to d                    (else GDR_EINVAL)
+ *   ldq, ldk elements between the rows of heads of successive tokens (b, t) of the inputs:
+ *            0 means dense (Hq * d, Hk * d); larger for slices of a fused projection's output
+ *   io_dtype: q, k, their outputs and gradients;  weight_dtype: wq, wk */
+typedef struct gdr_qk_desc {
+    int32_t B, T, Hq, Hk, d;
+    int32_t io_dtype;
+    int32_t weight_dtype;
+    int32_t norm;
+    int32_t rot_layout;
+    int32_t rot_dim;
+    float eps;
+    float q_scale;
+    float rot_scale;
+    int64_t ldq, ldk;
+} gdr_qk_desc;
+
+/*
+ *   q [B, T, Hq, d], k [B, T, Hk, d]   io_dtype, heads dense, ldq / ldk between tokens
+ *   wq, wk     [d] weight_dtype or NULL (must be NULL for GDR_NORM_NONE)
+ *   positions  [B, T] int32, or NULL for 0 .. T - 1 in every sequence
+ *   inv_freq   [rot_dim / 2] fp64 (required when rot_dim > 0)
+ *   q_out, k_out  dense, io_dtype; may be q, k themselves where those are dense, and
+ *              overlap nothing else
+ * Pointers need their element's alignment only.  Decode is T = 1 with positions [B, 1].
+ */
+int gdr_qk_prep_fwd(const gdr_qk_desc *desc, const void *q, const void *k, const void *wq, const void *wk,
+                    const int32_t *positions, const double *inv_freq, void *q_out, void *k_out, void *stream);
+
+/*
+ * Its backward pass, from the inputs and the gradients of the outputs:
+ *   dq_out, dk_out  dense, io_dtype: gradients of q_out, k_out
+ *   dq, dk          dense, io_dtype: gradients of q, k; may be dq_out, dk_out themselves,
+ *                   and overlap nothing else
+ *   dwq, dwk        [d] fp32 or NULL (not computed): sums over every row of that tensor
+ *   workspace       at least gdr_qk_prep_bwd_workspace_size(desc) bytes, 16-byte aligned,
+ *                   when dwq or dwk is given (0 bytes for GDR_NORM_NONE)
+ * Results are deterministic.  B * T == 0 or no heads: dwq, dwk are set to 0.
+ */
+size_t gdr_qk_prep_bwd_workspace_size(const gdr_qk_desc *desc);
+int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const void *wq, const void *wk,
+                    const int32_t *positions, const double *inv_freq, const void *dq_out, const void *dk_out, void *dq,
+                    void *dk, float *dwq, float *dwk, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated linear recurrence: the state of one (batch b, head h) is a vector of dv channels,
+ * each decayed and written on its own (the channel-gate decay of the delta rule without
+ * its keys),
+ *
+ *     h_t = a_t h_{t-1} + b_t x_t,   y_t = h_t
+ *
+ * with a = alpha, or exp(alpha) with GDR_FLAG_LOG_GATE, and b = beta where given, 1 - a
+ * with GDR_FLAG_COUPLED, else 1.  The sum runs in fp32 whatever the types.
+ *
+ *   desc       B, T, H, dv >= 1 (any), io_dtype (x, y, dy, dx), gate_dtype (alpha, beta and
+ *              their gradients), alpha_mode GDR_ALPHA_CHANNEL (else GDR_EUNSUPPORTED),
+ *              flags; dk, chunk and beta_mode are not used.  H * dv and B * T < 2^30.
+ *   x          [B, T, H, dv] io_dtype;  alpha, beta [B, T, H, dv] gate_dtype, beta may be
+ *              NULL; ldx, lda, ldb elements between successive tokens (b, t), 0 for dense
+ *              (H * dv), larger for slices of a fused projection's output
+ *   seq_off    NULL, or [n_seq + 1] int32 on the device with B == 1: sequence i is the rows
+ *              seq_off[i] .. seq_off[i + 1] - 1 of the T packed ones.  The offsets must not
+ *              decrease and lie in 0 .. T; a sequence may be empty; rows before the first
+ *              and behind the last one are neither read nor written.  Offsets that break
+ *              this give undefined values in y and the states, and no access outside the
+ *              tensors.  n_seq is 0 with a NULL seq_off.
+ *   S0, ST     [B, H, dv] fp32 ([n_seq, H, dv] when packed): state before and after each
+ *              sequence; S0 NULL means zero, ST NULL not written.  ST == S0 is allowed
+ *              (in-place resume) without seq_off; an empty sequence gives ST = S0.
+ *   y          [B, T, H, dv] io_dtype, dense
+ *   ckpt       NULL, or [B, N, H, dv] fp32 with N = ceil(T / GDR_SCAN_BLOCK): the state after
+ *              each block of GDR_SCAN_BLOCK tokens (of the rows, when packed), which the
+ *              backward pass starts from
+ *   workspace  at least gdr_scan_workspace_size(desc) bytes, 16-byte aligned (may be NULL
+ *              when that size is 0); its contents on entry do not matter.  One workspace
+ *              serves one call at a time: calls, or graphs, that may run at the same time
+ *              need one each.
+ * Pointers need their element's alignment only.  Outputs overlap no input and no other output.
+ */
+#define GDR_SCAN_BLOCK 512
+size_t gdr_scan_workspace_size(const gdr_desc *desc);
+int gdr_scan_fwd(const gdr_desc *desc, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
+                 int64_t ldb, const int32_t *seq_off, int32_t n_seq, const float *S0, void *y, float *ST, float *ckpt,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its backward pass, with the inputs of the forward call and the ckpt that it wrote.
+ *   dy [B, T, H, dv] io_dtype, dense: gradient of y;  dST: gradient of ST or NULL for zero
+ *   dx [B, T, H, dv] io_dtype; dalpha [B, T, H, dv] gate_dtype: gradient of alpha as stored
+ *   (of the logarithm with GDR_FLAG_LOG_GATE); dbeta likewise, required exactly when beta is
+ *   given; dS0 like S0, or NULL.  All dense; rows in no sequence are not written.
+ *   ckpt may be NULL when T <= GDR_SCAN_BLOCK.
+ */
+int gdr_scan_bwd(const gdr_desc *desc, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
+                 int64_t ldb, const int32_t *seq_off, int32_t n_seq, const float *S0, const float *ckpt, const void *dy,
+                 const float *dST, void *dx, void *dalpha, void *dbeta, float *dS0, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+/*
+ * One token for every sequence, applied in place to a resident state: x, alpha, beta
+ * [B, H, dv] (ldx, lda, ldb elements between sequences, 0 for dense), S [B, H, dv] fp32
+ * read and overwritten, y [B, H, dv] dense.  desc->T is ignored.
+ */
+int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
+                  int64_t ldb, float *S, void *y, void *stream);
 
 /* Which prefill kernel `desc` selects: 1 = bf16 matrix-core kernel,
  * 2 = fp32 vector-ALU kernel, or a negative gdr_status if desc is rejected. */

@@ -1,0 +1,319 @@
+"""Gated linear recurrence, forward, backward and single step, against its fp64 reference.
+
+Tolerances (u = 2^-24): with M_t = |a_t| M_{t-1} + |b_t x_t| the magnitudes that a state sums,
+a token adds at most 12 u M_t to the error that it takes over, |a_t| E_{t-1}: exp and expm1
+within 2 u each, two products and a sum of the token itself, and the products and sums of
+composed maps (3 steps over a wave's strands, 8 waves, one per block), each of which rounds
+what one token's own step would have rounded.  E follows the same recurrence, so it is the
+reference run on magnitudes.  Backward likewise from the last token; the products that form
+the gradients add their factors' errors.  Stored values add half a step of their type."""
+import numpy as np
+import pytest
+
+from oracle import scan as ref
+from tests.gpu_util import gpu, log, to_np
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+STEP = {"bf16": 2.0 ** -8, "f32": U}
+C = 12 * U
+
+
+def _inputs(torch, seed, B, T, H, dv, io, gate, form, kind, n=None, fused=False):
+    gen = torch.Generator().manual_seed(seed)
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    x = r(B, T, H, dv).to(t[io])
+    raw = -torch.nn.functional.softplus(r(B, T, H, dv) * 2 - 2)
+    alpha = (raw if form == "log" else raw.exp()).to(t[gate])
+    beta = torch.sigmoid(r(B, T, H, dv)).to(t[gate]) if kind == "beta" else None
+    dy, S0, dST = r(B, T, H, dv).to(t[io]), r(n or B, H, dv), r(n or B, H, dv)
+    dev = lambda v: None if v is None else v.cuda()  # noqa: E731
+    if fused:  # rows with a gap between them
+        gap = lambda v: torch.cat([v.flatten(2), r(B, T, 5).to(v.dtype)], -1).cuda()[..., :H * dv].unflatten(-1, (H, dv))  # noqa: E731
+        x, alpha = gap(x), gap(alpha)
+    return dev(x), dev(alpha), dict(beta=dev(beta), log_gate=form == "log", coupled=kind == "coupled", S0=dev(S0)), dev(dy), dev(dST)
+
+
+def _np3(t):
+    return None if t is None else to_np(t).reshape(t.shape[:-2] + (-1,))
+
+
+def _bounds(x, alpha, how, dy=None, dST=None, offsets=None):
+    """Reference values and error bounds of every output."""
+    kw = dict(log=how["log_gate"], coupled=how["coupled"], offsets=offsets)
+    beta, S0 = _np3(how["beta"]), _np3(how["S0"])
+    a, b = ref._factors(alpha, beta, kw["log"], kw["coupled"])
+    mag = dict(offsets=offsets)
+    y, ST = ref.forward(x, alpha, beta, S0=S0, **kw)
+    M, _ = ref.forward(np.abs(x), np.abs(a), np.abs(b), S0=np.abs(S0), **mag)
+    E, ES = ref.forward(C * np.nan_to_num(M), np.abs(a), **mag)
+    out = {"y": (y, E), "ST": (ST, ES)}
+    if dy is None:
+        return out
+    dx, da, db, dS0 = ref.backward(x, alpha, dy, beta, dST=dST, S0=S0, **kw)
+    # magnitudes of g and of what passes down, by the reference's own recurrence: x = 1, b = 1 gives dx = g
+    one = np.ones_like(x)
+    Mg, _, _, Md = ref.backward(one, np.abs(a), np.abs(dy), dST=np.abs(dST), **mag)
+    Eg, _, _, Ed = ref.backward(one, np.abs(a), C * np.nan_to_num(Mg), **mag)
+    # the states before each token, their magnitudes and errors: dalpha of a loss that is every g = 1
+    before = np.full_like(x, np.nan)
+    Mb, Eb = before.copy(), before.copy()
+    for row, i, p, q in ref._runs(x.shape[1], x.shape[0], offsets):
+        if q > p:
+            Mb[row, p:q] = np.concatenate([np.abs(S0[i:i + 1]), M[row, p:q - 1]])
+            Eb[row, p:q] = np.concatenate([np.zeros_like(S0[i:i + 1]), E[row, p:q - 1]])
+    Mw = Mb + (np.abs(x) if kw["coupled"] else 0)
+    Ea = Eg * Mw + Mg * (Eb + 4 * U * Mw) + 4 * U * Mg * Mw
+    out.update(dx=(dx, Eg * np.abs(b) + 4 * U * Mg * np.abs(b)), dS0=(dS0, Ed + C * Md),
+               dalpha=(da, Ea * np.abs(a) if kw["log"] else Ea))
+    if beta is not None:
+        out["dbeta"] = (db, Eg * np.abs(x) + 2 * U * Mg * np.abs(x))
+    return out
+
+
+def _check(name, got, want, step):
+    want, err = want
+    got = _np3(got)
+    rows = ~np.isnan(want)
+    bound = (step * np.abs(want) + err)[rows]
+    worst = float(np.max(np.abs(got[rows] - want[rows]) / np.maximum(bound, 1e-300))) if rows.any() else 0.0
+    log(f"[scan] {name}: error / bound {worst:.3f}")
+    assert worst <= 1.0, name
+
+
+def _run(torch, g, x, alpha, how, dy, dST, io, gate, offsets=None):
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    y, ST, ckpt = g.scan_fwd(x, alpha, want_ckpt=True, seq_offsets=off, **how)
+    dx, da, db, dS0 = g.scan_bwd(x, alpha, dy, ckpt, dST=dST, seq_offsets=off, **how)
+    torch.cuda.synchronize()
+    want = _bounds(_np3(x), _np3(alpha), how, _np3(dy), _np3(dST), offsets)
+    for name, got, step in (("y", y, STEP[io]), ("ST", ST, U), ("dx", dx, STEP[io]), ("dalpha", da, STEP[gate]),
+                            ("dbeta", db, STEP[gate]), ("dS0", dS0, U)):
+        if got is not None:
+            _check(name, got, want[name], step)
+    return y, ST, ckpt, dx, da, db, dS0
+
+
+CASES = [
+    # B, T, H, dv, io, gate, form, kind, fused
+    (1, 1, 1, 1, "f32", "f32", "value", "one", False),
+    (2, 2, 1, 3, "bf16", "bf16", "log", "coupled", False),
+    (3, 7, 1, 65, "bf16", "f32", "value", "beta", True),
+    (2, 8, 2, 8, "f32", "bf16", "log", "beta", False),
+    (1, 64, 1, 64, "bf16", "bf16", "value", "one", False),
+    (2, 65, 3, 11, "f32", "f32", "value", "coupled", True),
+    (1, 511, 1, 20, "bf16", "f32", "log", "one", False),
+    (1, 512, 2, 33, "f32", "f32", "log", "coupled", False),
+    (2, 513, 1, 40, "bf16", "bf16", "value", "beta", True),
+    (1, 1537, 1, 130, "f32", "f32", "value", "beta", False),
+    (2, 1100, 2, 36, "bf16", "f32", "log", "coupled", False),
+    (1, 6000, 1, 9, "f32", "f32", "log", "one", True),
+    (40, 520, 1, 5, "bf16", "bf16", "log", "beta", False),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_forward_and_backward(case):
+    torch, g = gpu()
+    log(f"[scan] {case}")
+    B, T, H, dv, io, gate, form, kind, fused = case
+    x, alpha, how, dy, dST = _inputs(torch, 21, B, T, H, dv, io, gate, form, kind, fused=fused)
+    _, _, ckpt, *_ = _run(torch, g, x, alpha, how, dy, dST, io, gate)
+    states = ref.block_states(_np3(x), _np3(alpha), _np3(how["beta"]), log=how["log_gate"], coupled=how["coupled"],
+                              S0=_np3(how["S0"]))
+    assert np.max(np.abs(_np3(ckpt) - states)) <= 1e-4 * max(1.0, np.max(np.abs(states)))
+
+
+PACKED = [
+    # rows, borders, channels, io, gate, form, kind
+    (9, [0, 9], 3, "f32", "f32", "value", "one"),
+    (30, [2, 2, 3, 11, 11, 12, 20, 29], 10, "bf16", "f32", "log", "coupled"),
+    (1200, [0, 1, 8, 16, 511, 512, 513, 1024, 1024, 1100], 20, "f32", "bf16", "value", "beta"),
+    (1100, [5, 600, 600, 1100], 70, "bf16", "bf16", "log", "one"),
+    (700, list(range(3, 690, 3)), 16, "f32", "f32", "value", "coupled"),   # a sequence every three rows
+    (2600, [1030, 1040], 12, "f32", "f32", "log", "beta"),                 # blocks without any
+    (1500, [0, 0, 0, 0], 12, "bf16", "f32", "log", "beta"),                # nothing but empty sequences
+]
+
+
+@pytest.mark.parametrize("case", PACKED, ids=lambda c: f"{c[0]}x{c[2]}-{len(c[1]) - 1}seqs-{c[3]}-{c[4]}-{c[5]}-{c[6]}")
+def test_packed_sequences(case):
+    torch, g = gpu()
+    T, offsets, D, io, gate, form, kind = case
+    log(f"[scan] packed {case[0]} rows, {len(offsets) - 1} sequences")
+    x, alpha, how, dy, dST = _inputs(torch, 22, 1, T, 1, D, io, gate, form, kind, n=len(offsets) - 1)
+    _run(torch, g, x, alpha, how, dy, dST, io, gate, offsets)
+    # without states: zero on entry, zero gradient
+    how["S0"] = None
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    y, ST, ck = g.scan_fwd(x, alpha, seq_offsets=off, want_ckpt=True, **how)
+    dx, _, _, dS0 = g.scan_bwd(x, alpha, dy, ck, seq_offsets=off, **how)
+    how["S0"] = torch.zeros(len(offsets) - 1, 1, D, device="cuda")
+    want = _bounds(_np3(x), _np3(alpha), how, _np3(dy), np.zeros((len(offsets) - 1, D)), offsets)
+    for name, got, step in (("y", y, STEP[io]), ("ST", ST, U), ("dx", dx, STEP[io]), ("dS0", dS0, U)):
+        _check(name, got, want[name], step)
+
+
+def test_rows_of_no_sequence_and_special_values_stay_apart():
+    """Infinities and NaN of one packed sequence, or of rows in none, reach no other sequence, and rows of
+    no sequence are left as they were."""
+    torch, g = gpu()
+    T, D, offsets = 1300, 24, [10, 400, 530, 530, 1040, 1290]
+    x, alpha, how, dy, dST = _inputs(torch, 23, 1, T, 1, D, "f32", "f32", "value", "beta", n=5)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    desc = g._scan_desc(x, alpha, False, False)
+    need = g.gdr_scan_workspace_size(desc)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+
+    def run(x, alpha, dy, S0):
+        outs = [torch.full_like(x, 7.0) for _ in range(4)]
+        ST, ck = torch.empty(5, 1, D, device="cuda"), torch.empty(1, 3, 1, D, device="cuda")
+        dS0 = torch.empty_like(ST)
+        assert g.gdr_scan_fwd(desc, x, 0, alpha, 0, how["beta"], 0, off, 5, S0, outs[0], ST, ck, ws, need) == g.GDR_OK
+        assert g.gdr_scan_bwd(desc, x, 0, alpha, 0, how["beta"], 0, off, 5, S0, ck, dy, dST, outs[1], outs[2], outs[3], dS0,
+                              ws, need) == g.GDR_OK
+        return outs, ST, dS0
+
+    clean, ST, dS0 = run(x, alpha, dy, how["S0"])
+    for o in clean:
+        assert (o[:, :10] == 7).all() and (o[:, 1290:] == 7).all() and (o[:, 10:1290] != 7).any(-1).all()
+    x2, a2, dy2, S2 = x.clone(), alpha.clone(), dy.clone(), how["S0"].clone()
+    for t in (x2, a2, dy2):
+        t[:, :10], t[:, 1290:] = float("nan"), float("inf")
+    x2[0, 450], dy2[0, 480], a2[0, 500], S2[1] = float("inf"), float("nan"), float("nan"), float("inf")  # sequence 1
+    bad, ST2, dS2 = run(x2, a2, dy2, S2)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[400:530] = False
+    assert all(torch.equal(p[:, keep], q[:, keep]) for p, q in zip(clean, bad))
+    others = [0, 2, 3, 4]
+    assert torch.equal(ST[others], ST2[others]) and torch.equal(dS0[others], dS2[others])
+    assert not ST2[1].isfinite().any() and not dS2[1].isfinite().any()
+
+
+def test_special_gates_of_a_dense_batch():
+    torch, g = gpu()
+    x, alpha, how, dy, dST = _inputs(torch, 24, 2, 1200, 1, 16, "f32", "f32", "value", "one")
+    alpha[:, 600] = 0                                                        # a hard reset
+    alpha[:, 700:] = 1                                                       # a plain sum
+    _run(torch, g, x, alpha, how, dy, dST, "f32", "f32")
+    raw = alpha.log()
+    assert raw[0, 600, 0, 0] == float("-inf")
+    how["log_gate"] = True
+    y, ST, ck = g.scan_fwd(x, raw, want_ckpt=True, **how)
+    da = g.scan_bwd(x, raw, dy, ck, dST=dST, **how)[1]
+    assert y.isfinite().all() and not da[:, 600].any()
+    want = _bounds(_np3(x), _np3(raw), how)
+    _check("y", y, want["y"], U)
+    # NaN stays in its channel, from its token on, and in its batch row
+    x[0, 650, 0, 3] = float("nan")
+    z, _, _ = g.scan_fwd(x, raw, **how)
+    hit = z.isnan()
+    assert hit[0, 650:, 0, 3].all() and int(hit.sum()) == 550
+    # negative decays alternate
+    x, alpha, how, dy, dST = _inputs(torch, 25, 1, 700, 1, 12, "f32", "f32", "value", "beta")
+    _run(torch, g, x, -alpha, how, dy, dST, "f32", "f32")
+
+
+@pytest.mark.parametrize("B,H,dv,io,gate,form,kind", [
+    (1, 1, 1, "f32", "f32", "value", "one"), (5, 3, 7, "bf16", "f32", "log", "coupled"),
+    (64, 2, 128, "bf16", "bf16", "value", "beta"), (3, 1, 1001, "f32", "bf16", "log", "one"),
+])
+def test_step_equals_one_token(B, H, dv, io, gate, form, kind):
+    torch, g = gpu()
+    x, alpha, how, _, _ = _inputs(torch, 26, B, 4, H, dv, io, gate, form, kind)
+    S = how.pop("S0")
+    want = _bounds(_np3(x), _np3(alpha), dict(how, S0=S))
+    keep = S.clone()
+    ys = [g.scan_step(S, *(t[:, i] for t in (x, alpha)), **dict(how, beta=None if how["beta"] is None else how["beta"][:, i]))
+          for i in range(4)]
+    _check("steps", torch.stack(ys, 1), want["y"], STEP[io])
+    _check("state", S, want["ST"], U)
+    y, ST, _ = g.scan_fwd(x[:, :1].contiguous(), alpha[:, :1].contiguous(),
+                          **dict(how, S0=keep, beta=None if how["beta"] is None else how["beta"][:, :1].contiguous()))
+    assert torch.equal(y[:, 0], ys[0])
+
+
+def test_resume_in_place_and_empty():
+    torch, g = gpu()
+    x, alpha, how, dy, dST = _inputs(torch, 27, 2, 1500, 2, 10, "bf16", "f32", "log", "coupled")
+    y, ST, _ = g.scan_fwd(x, alpha, **how)
+    S = how["S0"].clone()
+    parts = []
+    for p, q in ((0, 700), (700, 700), (700, 1500)):
+        xs, al = x[:, p:q].contiguous(), alpha[:, p:q].contiguous()
+        desc = g._scan_desc(xs, al, True, True)
+        o, need = torch.empty_like(xs), g.gdr_scan_workspace_size(desc)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        assert g.gdr_scan_fwd(desc, xs, 0, al, 0, None, 0, None, 0, S, o, S, None, ws, need) == g.GDR_OK
+        parts.append(o)
+    want = _bounds(_np3(x), _np3(alpha), how)
+    _check("resumed", torch.cat(parts, 1), want["y"], STEP["bf16"])
+    _check("state", S, want["ST"], U)
+    # no tokens: the state and its gradient pass through, or are zero
+    e = x[:, :0].contiguous()
+    _, S1, _ = g.scan_fwd(e, e.float(), S0=S)
+    assert torch.equal(S1, S) and not g.scan_fwd(e, e.float())[1].any()
+    assert torch.equal(g.scan_bwd(e, e.float(), e, None, dST=dST)[3], dST)
+    # no channels, no sequences
+    assert g.scan_fwd(x[:, :, :0].contiguous(), alpha[:, :, :0].contiguous())[0].numel() == 0
+    off = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert g.scan_fwd(x[:1], alpha[:1], seq_offsets=off)[1].shape == (0, 2, 10)
+
+
+def test_deterministic_captured_and_side_by_side():
+    """The same bits every time: eager, replayed from a graph with other calls between the replays, and on two
+    streams at once with a workspace each."""
+    torch, g = gpu()
+    sets = [_inputs(torch, 28 + i, 2, 3000, 1, 200, "bf16", "f32", "log", "coupled") for i in range(2)]
+
+    def step(s, stream=None):
+        x, alpha, how, dy, dST = s
+        y, ST, ck = g.scan_fwd(x, alpha, want_ckpt=True, stream=stream, **how)
+        return (y, ST, ck) + tuple(t for t in g.scan_bwd(x, alpha, dy, ck, dST=dST, stream=stream, **how) if t is not None)
+
+    want = [step(s) for s in sets]
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want[0], step(sets[0])))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        outs = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                outs.append(step(s, st))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, o in zip(want, outs) for a, b in zip(w, o))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        out = step(sets[0])
+    x = sets[0][0]
+    for rep in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step(sets[0]))), rep
+        step(sets[1])
+        x.copy_(torch.randn(x.shape, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """2.6 billion elements: the last rows, behind a reset, equal a call on them alone."""
+    torch, g = gpu()
+    T, D, cut = 65000, 40000, 64300
+    x = torch.empty(1, T, 1, D, dtype=torch.bfloat16, device="cuda")
+    alpha = torch.empty_like(x)
+    for t in range(0, T, 5000):
+        x[:, t:t + 5000] = torch.randn(1, min(5000, T - t), 1, D, device="cuda")
+        alpha[:, t:t + 5000] = torch.rand(1, min(5000, T - t), 1, D, device="cuda")
+    alpha[:, cut] = 0
+    y, ST, ck = g.scan_fwd(x, alpha, want_ckpt=True)
+    xt, at = x[:, cut:].contiguous(), alpha[:, cut:].contiguous()
+    yt, St, ct = g.scan_fwd(xt, at, want_ckpt=True)
+    torch.testing.assert_close(y[:, cut:], yt, rtol=2.0 ** -7, atol=1e-5)
+    torch.testing.assert_close(ST, St, rtol=1e-5, atol=1e-5)
+    dx, da, _, _ = g.scan_bwd(x, alpha, y, ck)
+    dxt, dat, _, _ = g.scan_bwd(xt, at, y[:, cut:].contiguous(), ct)
+    torch.testing.assert_close(dx[:, cut:], dxt, rtol=2.0 ** -7, atol=1e-4)
+    torch.testing.assert_close(da[:, cut + 1:], dat[:, 1:], rtol=2.0 ** -7, atol=1e-4)
+    assert dx[:, :5].isfinite().all()

@@ -1,0 +1,125 @@
+"""Pins of the fp64 references of the query / key preparation and of the gated linear
+recurrence: closed forms, and every gradient against central differences."""
+import math
+
+import numpy as np
+import pytest
+from scipy.signal import lfilter
+
+from oracle import qk_prep, scan
+
+
+def _differences(f, x, h=1e-5):
+    g = np.zeros_like(x)
+    for i in np.ndindex(*x.shape):
+        up, down = x.copy(), x.copy()
+        up[i] += h
+        down[i] -= h
+        g[i] = (f(up) - f(down)) / (2 * h)
+    return g
+
+
+# central differences of a smooth function of size ~1: h^2 / 6 third derivatives ~ 1e-10 and
+# cancellation eps * |f| / h ~ 1e-16 * 1e2 / 1e-5 = 1e-9
+CLOSE = dict(rtol=1e-6, atol=1e-7)
+
+
+@pytest.mark.parametrize("log,kind", [(False, "one"), (False, "beta"), (False, "coupled"), (True, "one"), (True, "coupled"),
+                                      (True, "beta")])
+@pytest.mark.parametrize("offsets", [None, [0, 2, 2, 5]])
+def test_scan_gradients_against_differences(log, kind, offsets):
+    rng = np.random.default_rng(3)
+    B, T, D = (2 if offsets is None else 1), 5, 3
+    n = B if offsets is None else len(offsets) - 1
+    x, dy = rng.normal(size=(2, B, T, D))
+    alpha = rng.uniform(-1, -0.1, size=(B, T, D)) if log else rng.uniform(0.2, 1, size=(B, T, D))
+    beta = rng.uniform(0.2, 1, size=(B, T, D)) if kind == "beta" else None
+    S0, dST = rng.normal(size=(2, n, D))
+    kw = dict(log=log, coupled=kind == "coupled", offsets=offsets)
+
+    def loss(x=x, alpha=alpha, beta=beta, S0=S0):
+        y, ST = scan.forward(x, alpha, beta, S0=S0, **kw)
+        return (y * dy).sum() + (ST * dST).sum()
+
+    dx, da, db, dS = scan.backward(x, alpha, dy, beta, dST=dST, S0=S0, **kw)
+    np.testing.assert_allclose(dx, _differences(lambda v: loss(x=v), x), **CLOSE)
+    np.testing.assert_allclose(da, _differences(lambda v: loss(alpha=v), alpha), **CLOSE)
+    np.testing.assert_allclose(dS, _differences(lambda v: loss(S0=v), S0), **CLOSE)
+    if beta is not None:
+        np.testing.assert_allclose(db, _differences(lambda v: loss(beta=v), beta), **CLOSE)
+
+
+def test_scan_closed_forms():
+    rng = np.random.default_rng(4)
+    x = rng.normal(size=(1, 40, 2))
+    # a constant decay is a first-order filter
+    y, _ = scan.forward(x, np.full_like(x, 0.9))
+    np.testing.assert_allclose(y[0], lfilter([1.0], [1.0, -0.9], x[0], axis=0), rtol=1e-12)
+    # a = 1 sums, a = 0 copies, coupled with a = 1 keeps the state
+    np.testing.assert_allclose(scan.forward(x, np.ones_like(x))[0], np.cumsum(x, 1), rtol=1e-12)
+    assert np.array_equal(scan.forward(x, np.zeros_like(x), S0=np.ones((1, 2)))[0], x)
+    assert np.array_equal(scan.forward(x, np.ones_like(x), coupled=True, S0=np.ones((1, 2)))[0], np.ones_like(x))
+    # log gates are the same recurrence; packed sequences are separate calls
+    a = rng.uniform(0.1, 1, size=x.shape)
+    np.testing.assert_allclose(scan.forward(x, np.log(a), log=True)[0], scan.forward(x, a)[0], rtol=1e-12)
+    S0 = rng.normal(size=(3, 2))
+    y, ST = scan.forward(x, a, S0=S0, offsets=[4, 10, 10, 37])
+    for i, (p, q) in enumerate([(4, 10), (10, 10), (10, 37)]):
+        yi, Si = scan.forward(x[:, p:q], a[:, p:q], S0=S0[i:i + 1])
+        assert np.array_equal(y[:, p:q], yi) and np.array_equal(ST[i:i + 1], Si)
+    assert np.isnan(y[:, :4]).all() and np.isnan(y[:, 37:]).all()
+    assert np.array_equal(scan.block_states(x, a, block=16), scan.forward(x, a)[0][:, [15, 31, 39]])
+
+
+@pytest.mark.parametrize("norm", ["none", "l2", "rms"])
+@pytest.mark.parametrize("layout,half", [("half", 4), ("half", 3), ("interleaved", 4), ("interleaved", 2), ("half", 0)])
+def test_qk_gradients_against_differences(norm, layout, half):
+    rng = np.random.default_rng(5)
+    x, g = rng.normal(size=(2, 1, 3, 2, 8))
+    w = None if norm == "none" else rng.uniform(0.5, 1.5, size=8)
+    kw = dict(norm=norm, eps=0.3, pos=np.array([[0, 7, -50]]), inv_freq=10.0 ** -np.arange(half), layout=layout,
+              rot_scale=1.3, scale=0.7)
+    dx, dw = qk_prep.backward(x, g, w, **kw)
+    np.testing.assert_allclose(dx, _differences(lambda v: (qk_prep.forward(v, w, **kw) * g).sum(), x), **CLOSE)
+    if w is not None:
+        np.testing.assert_allclose(dw, _differences(lambda v: (qk_prep.forward(x, v, **kw) * g).sum(), w), **CLOSE)
+
+
+def test_qk_closed_forms():
+    rng = np.random.default_rng(6)
+    q, k = rng.normal(size=(2, 1, 1, 1, 16))
+    f = 100.0 ** (-np.arange(8) / 8)
+    for layout in ("half", "interleaved"):
+        at = lambda x, p: qk_prep.forward(x, norm="none", pos=np.array([[p]]), inv_freq=f, layout=layout)  # noqa: E731
+        # products of rotated rows depend on the distance alone, and position 0 changes nothing
+        np.testing.assert_allclose((at(q, 905) * at(k, 900)).sum(), (at(q, 5) * at(k, 0)).sum(), rtol=1e-10)
+        assert np.array_equal(at(q, 0), q)
+        # one quarter turn of pair 0: (e, o) -> (-o, e)
+        e, o = (0, 1) if layout == "interleaved" else (0, 8)
+        turned = qk_prep.forward(q, norm="none", pos=np.array([[1]]), inv_freq=np.r_[math.pi / 2, np.zeros(7)], layout=layout)
+        np.testing.assert_allclose(turned[..., [e, o]], np.stack([-q[..., o], q[..., e]], -1), atol=1e-15)
+    np.testing.assert_allclose((qk_prep.forward(q, norm="l2") ** 2).sum(), 1, rtol=1e-12)
+    np.testing.assert_allclose((qk_prep.forward(q, norm="rms") ** 2).mean(), 1, rtol=1e-12)
+    z = np.zeros((1, 1, 1, 16))
+    assert not qk_prep.forward(z, norm="l2").any() and not qk_prep.backward(z, q, norm="rms")[0].any()
+
+
+def test_rope_inv_freq():
+    import gated_delta_rule_84_amd as g
+
+    plain, one = g.rope_inv_freq(64, device="cpu")
+    np.testing.assert_allclose(plain.numpy(), 10000.0 ** (-np.arange(0, 64, 2) / 64), rtol=1e-14)
+    assert one == 1.0
+    np.testing.assert_allclose(g.rope_inv_freq(64, scaling="linear", factor=4, device="cpu")[0], plain / 4, rtol=1e-14)
+    ntk = g.rope_inv_freq(64, scaling="ntk", factor=4, device="cpu")[0].numpy()
+    np.testing.assert_allclose(ntk[[0, -1]], [1.0, plain[-1] / 4], rtol=1e-12)
+    yarn, scale = g.rope_inv_freq(64, scaling="yarn", factor=8, original_len=4096, device="cpu")
+    turns = 4096 * plain.numpy() / (2 * math.pi)
+    ratio = (yarn / plain).numpy()
+    assert np.all(ratio[turns > 40] == 1.0) and np.allclose(ratio[turns < 0.7], 1 / 8) and np.all(np.diff(ratio) <= 0)
+    np.testing.assert_allclose(scale, 0.1 * math.log(8) + 1)
+    assert g.rope_inv_freq(0, device="cpu")[0].numel() == 0
+    for bad in (dict(rot_dim=3), dict(rot_dim=-2), dict(rot_dim=8, base=0), dict(rot_dim=8, factor=0.5),
+                dict(rot_dim=8, scaling="other"), dict(rot_dim=8, scaling="yarn", factor=2)):
+        with pytest.raises(ValueError):
+            g.rope_inv_freq(**bad, device="cpu")
