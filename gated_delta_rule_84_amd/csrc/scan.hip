@@ -33,6 +33,7 @@ constexpr int kLR = 8;                // lanes per row
 constexpr int kStrands = kBlk / kL;   // 64
 constexpr int kThreads = kStrands * kLR;
 constexpr int kWaves = kThreads / 64;
+constexpr int kChainHead = 256;       // bytes before the chain's words: the counter of blocks
 
 typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
@@ -173,22 +174,98 @@ struct Marks {
     }
 };
 
+// ---------------------------------------------------------------------------
+// The chain of blocks.  Every block publishes its composed map as soon as it has it and the
+// state behind it once that is known; a block takes the state that enters it from the nearest
+// block before it whose state is there and applies the maps in between, in the order of the
+// blocks.  That is the arithmetic of a walk from block to block whatever was ready first, so
+// the results do not depend on timing.  Words are stored and loaded whole with relaxed atomics
+// that all eight L2 caches see; a word is there once it is no longer kNone, which no value
+// is stored as, so no order between words matters.  Blocks are numbered by a counter when
+// they begin: every block before a waiting one is running or done, so each wait ends.
+constexpr uint32_t kNone = 0xffffffffu;  // what launch_fill leaves
+constexpr uint32_t kCut = 0xfffffffeu;   // in a map's factor: nothing of what enters gets through
+constexpr int kWindow = 8;               // blocks looked back over at a time
+constexpr int kMaxPolls = 1 << 22;       // some seconds: a bound that a sound run never meets
+
+__device__ __forceinline__ uint32_t word(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u >= kCut ? 0x7fc00000u : u;  // two NaN patterns are taken
+}
+
+__device__ __forceinline__ float apply(uint32_t A, float U, float h) { return A == kCut ? U : fmaf(__uint_as_float(A), h, U); }
+
+// The chain's words of one sequence and tile of channels: [nblk][CH] maps, [nblk][CH] states.
+template <int CH>
+struct Chain {
+    uint64_t *map;
+    uint32_t *state;
+
+    __device__ __forceinline__ Chain(const ScanParams &p, long column, long columns) {
+        char *ws = static_cast<char *>(p.ws) + kChainHead;
+        map = reinterpret_cast<uint64_t *>(ws) + column * p.nblk * CH;
+        state = reinterpret_cast<uint32_t *>(ws + columns * p.nblk * CH * 8) + column * p.nblk * CH;
+    }
+    __device__ __forceinline__ void put_map(int at, int c, uint32_t A, float U) const {
+        __hip_atomic_store(map + (long)at * CH + c, (uint64_t)A << 32 | __float_as_uint(U), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ void put_state(int at, int c, float h) const {
+        __hip_atomic_store(state + (long)at * CH + c, word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // The state behind block `at - 1` of channel c (at > 0; block 0 gives its state without a map).
+    __device__ __forceinline__ float enter(int at, int c) const {
+        for (int poll = 0; poll < kMaxPolls; ++poll) {
+            uint32_t h[kWindow];
+            uint64_t m[kWindow];
+#pragma unroll
+            for (int w = 0; w < kWindow; ++w) {
+                const int j = at - 1 - w;
+                h[w] = kNone;
+                m[w] = ~0ull;
+                if (j < 0) continue;
+                h[w] = __hip_atomic_load(state + (long)j * CH + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                m[w] = __hip_atomic_load(map + (long)j * CH + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            // nearest block whose state is there for every channel, with every map after it
+            int from = -1;
+            bool maps = true;
+#pragma unroll
+            for (int w = 0; w < kWindow; ++w) {
+                if (from >= 0 || !maps) continue;
+                if (__all(h[w] != kNone)) from = w;
+                else maps = __all((uint32_t)(m[w] >> 32) != kNone);
+            }
+            if (from >= 0) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = kWindow - 1; w >= 0; --w) {
+                    if (w == from) s = __uint_as_float(h[w]);
+                    if (w < from) s = apply((uint32_t)(m[w] >> 32), __uint_as_float((uint32_t)m[w]), s);
+                }
+                return s;
+            }
+            __builtin_amdgcn_s_sleep(1);
+        }
+        return __uint_as_float(0x7fc00000u);
+    }
+};
+
 struct Shared {
     float A[kWaves][kLR * 8], U[kWaves][kLR * 8];  // a wave's composed map, per channel
     int cut[kWaves];                               // it holds a border of sequences
-    float carry[2][kLR * 8];
+    float in[kWaves][kLR * 8];                     // the state that enters a wave's strands
+    int ticket;
 };
 
-// Composes the strands of a workgroup: on entry (A, U) is the lane's own map, on return `h`
-// is the state that enters the lane's strand when `carry` (shared, slot `slot`) enters the
-// block.  REV: the strands are taken from the last to the first.  A strand with a border of
-// sequences (`cut`) lets nothing of what enters it through: a flag and not A = 0, which would
-// turn an infinity of one sequence into a NaN of the next.
+// Composes the strands of a wave: (A, U) is the lane's own map, afterwards that of the
+// wave's strands up to and with its own.  The wave's map goes to shared memory.  REV: the
+// strands are taken from the last to the first.  A strand with a border of sequences (`cut`)
+// lets nothing of what enters it through: a flag and not A = 0, which would turn an infinity
+// of one sequence into a NaN of the next.
 template <int V, bool REV, bool PACKED>
-__device__ __forceinline__ void enter(Shared &sh, int slot, int waves, float (&A)[V], float (&U)[V], bool cut, float (&h)[V]) {
+__device__ __forceinline__ void compose(Shared &sh, float (&A)[V], float (&U)[V], bool &cut) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
     const int strand = REV ? 63 / kLR - lane / kLR : lane / kLR;
-    // inclusive over the wave's strands
 #pragma unroll
     for (int s = 1; s < 64 / kLR; s <<= 1) {
 #pragma unroll
@@ -213,37 +290,87 @@ __device__ __forceinline__ void enter(Shared &sh, int slot, int waves, float (&A
             sh.U[wave][cl + v] = U[v];
         }
     }
-    __syncthreads();
+}
+
+// One lane per channel: the composed map of the workgroup's waves, in the order of the strands.
+template <bool REV, bool PACKED>
+__device__ __forceinline__ void block_map(const Shared &sh, int waves, int c, uint32_t &A, float &U) {
+    float a = 1.f, u = 0.f;
+    bool cut = false;
+    for (int i = 0; i < waves; ++i) {
+        const int w = REV ? waves - 1 - i : i;
+        if (PACKED && sh.cut[w]) {
+            cut = true;
+            u = sh.U[w][c];
+        } else {
+            u = fmaf(sh.A[w][c], u, sh.U[w][c]);
+            a *= sh.A[w][c];
+        }
+    }
+    A = cut ? kCut : word(a);
+    U = u;
+}
+
+// One lane per channel: the state that enters each wave when h enters the block.
+template <bool REV, bool PACKED>
+__device__ __forceinline__ void wave_states(Shared &sh, int waves, int c, float h) {
+    for (int i = 0; i < waves; ++i) {
+        const int w = REV ? waves - 1 - i : i;
+        sh.in[w][c] = h;
+        h = PACKED && sh.cut[w] ? sh.U[w][c] : fmaf(sh.A[w][c], h, sh.U[w][c]);
+    }
+}
+
+// The state that enters the lane's strand.
+template <int V, bool REV, bool PACKED>
+__device__ __forceinline__ void strand_states(const Shared &sh, const float (&A)[V], const float (&U)[V], bool cut, float (&h)[V]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
+    const int strand = REV ? 63 / kLR - lane / kLR : lane / kLR;
     const int before = PACKED ? (REV ? __shfl_down((int)cut, kLR) : __shfl_up((int)cut, kLR)) : 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float c = sh.carry[slot][cl + v];
-        for (int i = 0; i < (REV ? waves - 1 - wave : wave); ++i) {
-            const int w = REV ? waves - 1 - i : i;
-            c = PACKED && sh.cut[w] ? sh.U[w][cl + v] : fmaf(sh.A[w][cl + v], c, sh.U[w][cl + v]);
-        }
-        // exclusive: the map of the strands before this one
+        const float c = sh.in[wave][cl + v];
         const float a = REV ? __shfl_down(A[v], kLR) : __shfl_up(A[v], kLR);
         const float u = REV ? __shfl_down(U[v], kLR) : __shfl_up(U[v], kLR);
         h[v] = strand ? (PACKED && before ? u : fmaf(a, c, u)) : c;
     }
 }
 
+// This workgroup's place: blocks in the order of the recurrence, all channels of one block
+// before the next (neighbours read neighbouring memory, and a block's predecessors began long
+// before it).
+__device__ __forceinline__ long place(const ScanParams &p, Shared &sh) {
+    if (p.nblk == 1) return blockIdx.x;
+    if (threadIdx.x == 0) sh.ticket = (int)(atomicAdd(static_cast<uint32_t *>(p.ws), 1u) + 1u);  // starts at kNone
+    __syncthreads();
+    return (uint32_t)sh.ticket;
+}
+
 template <bool IOB, bool GB, bool BETA, bool PACKED, int V>
 __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
+    constexpr int CH = kLR * V;
     __shared__ Shared sh;
-    const int waves = blockDim.x >> 6, tiles = (p.D + kLR * V - 1) / (kLR * V);
-    const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int waves = blockDim.x >> 6, tiles = (p.D + CH - 1) / CH;
+    const long columns = (long)p.B * tiles, id = place(p, sh), column = id % columns;
+    const int k = (int)(id / columns), b = (int)(column / tiles), tile = (int)(column % tiles);
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const bool tail = strand == waves * (64 / kLR) - 1;  // holds the block's last tokens
-    if (strand == 0) {
-        float c[V];
-        load_state<V>(PACKED || !p.S0 ? nullptr : p.S0 + (int64_t)b * p.D + ch, n, c);
+    const long t0 = (long)k * kBlk + strand * kL, row = (long)b * p.T + t0;
+    Marks<PACKED> m;
+    m.find(p, b, t0);
+    Pack<IOB, V> x[kL];
+    Pack<GB, V> al[kL], be[BETA ? kL : 1];
 #pragma unroll
-        for (int v = 0; v < V; ++v) sh.carry[0][lr * V + v] = c[v];
+    for (int j = 0; j < kL; ++j) {
+        x[j].clear();
+        al[j].clear();
+        if (BETA) be[j].clear();
+        if (!(m.in >> j & 1)) continue;
+        x[j].load(p.x, (row + j) * p.ldx + ch, n);
+        al[j].load(p.alpha, (row + j) * p.lda + ch, n);
+        if (BETA) be[j].load(p.beta, (row + j) * p.ldb + ch, n);
     }
-    if (PACKED && p.ST) {  // empty sequences end as they begin
+    if (PACKED && p.ST && k == 0) {  // empty sequences end as they begin
         for (int i = strand; i < p.nseq; i += waves * (64 / kLR)) {
             if (p.off[i + 1] > p.off[i]) continue;
             float c[V];
@@ -251,92 +378,102 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
             store_state<V>(p.ST + (int64_t)i * p.D + ch, n, c);
         }
     }
-    float h[V];
-    for (int k = 0; k < p.nblk; ++k) {
-        const long t0 = (long)k * kBlk + strand * kL, row = (long)b * p.T + t0;
-        Marks<PACKED> m;
-        m.find(p, b, t0);
-        Pack<IOB, V> x[kL];
-        Pack<GB, V> al[kL], be[BETA ? kL : 1];
+    float A[V], U[V], h[V];
 #pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            x[j].clear();
-            al[j].clear();
-            if (BETA) be[j].clear();
-            if (!(m.in >> j & 1)) continue;
-            x[j].load(p.x, (row + j) * p.ldx + ch, n);
-            al[j].load(p.alpha, (row + j) * p.lda + ch, n);
-            if (BETA) be[j].load(p.beta, (row + j) * p.ldb + ch, n);
-        }
-        float A[V], U[V];
+    for (int v = 0; v < V; ++v) {
+        A[v] = 1.f;
+        U[v] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kL; ++j) {
+        if (!(m.in >> j & 1)) continue;
+        float s0[V];
+        const bool first = PACKED && (m.first >> j & 1);
+        if (first) load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, s0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            A[v] = 1.f;
-            U[v] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            if (!(m.in >> j & 1)) continue;
-            float s0[V];
-            const bool first = PACKED && (m.first >> j & 1);
-            if (first) load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, s0);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float a, bb;
-                gates<BETA>(p, al[j].get(v), BETA ? be[BETA ? j : 0].get(v) : 0.f, a, bb);
-                const float u = bb * x[j].get(v);
-                if (first) {
-                    U[v] = fmaf(a, s0[v], u);
-                    A[v] = 0.f;
-                } else {
-                    U[v] = fmaf(a, U[v], u);
-                    A[v] *= a;
-                }
+            float a, bb;
+            gates<BETA>(p, al[j].get(v), BETA ? be[BETA ? j : 0].get(v) : 0.f, a, bb);
+            const float u = bb * x[j].get(v);
+            if (first) {
+                U[v] = fmaf(a, s0[v], u);
+                A[v] = 0.f;
+            } else {
+                U[v] = fmaf(a, U[v], u);
+                A[v] *= a;
             }
         }
-        enter<V, false, PACKED>(sh, k & 1, waves, A, U, m.first != 0, h);
-#pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            if (!(m.in >> j & 1)) continue;
-            if (PACKED && (m.first >> j & 1))
-                load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, h);
-#pragma unroll
-            for (int v = 0; v < V; v += 2) {
-#pragma unroll
-                for (int e = v; e < v + 2; ++e) {
-                    float a, bb;
-                    gates<BETA>(p, al[j].get(e), BETA ? be[BETA ? j : 0].get(e) : 0.f, a, bb);
-                    h[e] = fmaf(a, h[e], bb * x[j].get(e));
-                }
-                x[j].set2(v, h[v], h[v + 1]);
-            }
-            x[j].store(p.y, (row + j) * p.D + ch, n);
-            if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch, n, h);
-        }
-        if (tail) {
-            if (p.ckpt) store_state<V>(p.ckpt + ((int64_t)b * p.nblk + k) * p.D + ch, n, h);
-#pragma unroll
-            for (int v = 0; v < V; ++v) sh.carry[(k + 1) & 1][lr * V + v] = h[v];
-        }
-        __syncthreads();  // the carry is written and this block's maps are read
     }
-    if (!PACKED && tail && p.ST) store_state<V>(p.ST + (int64_t)b * p.D + ch, n, h);
+    bool cut = m.first != 0;
+    compose<V, false, PACKED>(sh, A, U, cut);
+    __syncthreads();
+    if (threadIdx.x < CH) {
+        const int c = threadIdx.x, cc = tile * CH + c;
+        const Chain<CH> chain(p, column, columns);
+        uint32_t ba;
+        float bu, in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f;
+        block_map<false, PACKED>(sh, waves, c, ba, bu);
+        if (p.nblk > 1) {
+            if (k > 0 && k < p.nblk - 1) chain.put_map(k, c, ba, bu);
+            if (k > 0) in = chain.enter(k, c);
+        }
+        const float out = apply(ba, bu, in);
+        if (k < p.nblk - 1) chain.put_state(k, c, out);
+        wave_states<false, PACKED>(sh, waves, c, in);
+        if (p.ckpt && cc < p.D) p.ckpt[((int64_t)b * p.nblk + k) * p.D + cc] = out;
+    }
+    __syncthreads();
+    strand_states<V, false, PACKED>(sh, A, U, cut, h);
+#pragma unroll
+    for (int j = 0; j < kL; ++j) {
+        if (!(m.in >> j & 1)) continue;
+        if (PACKED && (m.first >> j & 1))
+            load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, h);
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+#pragma unroll
+            for (int e = v; e < v + 2; ++e) {
+                float a, bb;
+                gates<BETA>(p, al[j].get(e), BETA ? be[BETA ? j : 0].get(e) : 0.f, a, bb);
+                h[e] = fmaf(a, h[e], bb * x[j].get(e));
+            }
+            x[j].set2(v, h[v], h[v + 1]);
+        }
+        x[j].store(p.y, (row + j) * p.D + ch, n);
+        if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch, n, h);
+    }
+    if (!PACKED && p.ST && k == p.nblk - 1 && strand == waves * (64 / kLR) - 1)
+        store_state<V>(p.ST + (int64_t)b * p.D + ch, n, h);
 }
 
 template <bool IOB, bool GB, bool BETA, bool PACKED, int V>
 __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
+    constexpr int CH = kLR * V;
     __shared__ Shared sh, sg;
-    const int waves = blockDim.x >> 6, tiles = (p.D + kLR * V - 1) / (kLR * V);
-    const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int waves = blockDim.x >> 6, tiles = (p.D + CH - 1) / CH;
+    const long columns = (long)p.B * tiles, id = place(p, sh), column = id % columns;
+    const int step = (int)(id / columns), k = p.nblk - 1 - step;  // blocks from the last to the first
+    const int b = (int)(column / tiles), tile = (int)(column % tiles);
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    if (strand == 0) {
-        float c[V];
-        load_state<V>(PACKED || !p.dST ? nullptr : p.dST + (int64_t)b * p.D + ch, n, c);
+    const long t0 = (long)k * kBlk + strand * kL, row = (long)b * p.T + t0;
+    Marks<PACKED> m;
+    m.find(p, b, t0);
+    Pack<IOB, V> x[kL], dy[kL];
+    Pack<GB, V> al[kL], be[BETA ? kL : 1];
 #pragma unroll
-        for (int v = 0; v < V; ++v) sg.carry[0][lr * V + v] = c[v];
+    for (int j = 0; j < kL; ++j) {
+        x[j].clear();
+        dy[j].clear();
+        al[j].clear();
+        if (BETA) be[j].clear();
+        if (!(m.in >> j & 1)) continue;
+        x[j].load(p.x, (row + j) * p.ldx + ch, n);
+        dy[j].load(p.dy, (row + j) * p.D + ch, n);
+        al[j].load(p.alpha, (row + j) * p.lda + ch, n);
+        if (BETA) be[j].load(p.beta, (row + j) * p.ldb + ch, n);
     }
-    if (PACKED && p.dS0) {
+    if (PACKED && p.dS0 && k == 0) {
         for (int i = strand; i < p.nseq; i += waves * (64 / kLR)) {
             if (p.off[i + 1] > p.off[i]) continue;
             float c[V];
@@ -344,137 +481,137 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
             store_state<V>(p.dS0 + (int64_t)i * p.D + ch, n, c);
         }
     }
-    float G[V];
-    for (int step = 0; step < p.nblk; ++step) {
-        const int k = p.nblk - 1 - step;
-        const long t0 = (long)k * kBlk + strand * kL, row = (long)b * p.T + t0;
-        Marks<PACKED> m;
-        m.find(p, b, t0);
-        Pack<IOB, V> x[kL], dy[kL];
-        Pack<GB, V> al[kL], be[BETA ? kL : 1];
+    float A[V], U[V], GA[V], GU[V], h[V], G[V];
 #pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            x[j].clear();
-            dy[j].clear();
-            al[j].clear();
-            if (BETA) be[j].clear();
-            if (!(m.in >> j & 1)) continue;
-            x[j].load(p.x, (row + j) * p.ldx + ch, n);
-            dy[j].load(p.dy, (row + j) * p.D + ch, n);
-            al[j].load(p.alpha, (row + j) * p.lda + ch, n);
-            if (BETA) be[j].load(p.beta, (row + j) * p.ldb + ch, n);
-        }
-        if (strand == 0) {  // the state that enters the block
-            float c[V];
-            load_state<V>(k > 0 ? p.ckpt + ((int64_t)b * p.nblk + k - 1) * p.D + ch
-                                : (PACKED || !p.S0 ? nullptr : p.S0 + (int64_t)b * p.D + ch), n, c);
+    for (int v = 0; v < V; ++v) {
+        A[v] = GA[v] = 1.f;
+        U[v] = GU[v] = 0.f;
+    }
 #pragma unroll
-            for (int v = 0; v < V; ++v) sh.carry[0][lr * V + v] = c[v];
-        }
-        float A[V], U[V], GA[V], GU[V], h[V];
+    for (int j = 0; j < kL; ++j) {
+        if (!(m.in >> j & 1)) continue;
+        float s0[V];
+        const bool first = PACKED && (m.first >> j & 1);
+        if (first) load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, s0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            A[v] = GA[v] = 1.f;
-            U[v] = GU[v] = 0.f;
+            float a, bb;
+            gates<BETA>(p, al[j].get(v), BETA ? be[BETA ? j : 0].get(v) : 0.f, a, bb);
+            const float u = bb * x[j].get(v);
+            if (first) {
+                U[v] = fmaf(a, s0[v], u);
+                A[v] = 0.f;
+            } else {
+                U[v] = fmaf(a, U[v], u);
+                A[v] *= a;
+            }
         }
+    }
 #pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            if (!(m.in >> j & 1)) continue;
-            float s0[V];
-            const bool first = PACKED && (m.first >> j & 1);
-            if (first) load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, s0);
+    for (int j = kL - 1; j >= 0; --j) {
+        if (!(m.in >> j & 1)) continue;
+        float st[V];
+        const bool last = PACKED && (m.last >> j & 1);
+        if (last) load_state<V>(p.dST ? p.dST + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, st);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+        for (int v = 0; v < V; ++v) {
+            float a, bb;
+            gates<BETA>(p, al[j].get(v), 0.f, a, bb);
+            if (last) {
+                GU[v] = a * (dy[j].get(v) + st[v]);
+                GA[v] = 0.f;
+            } else {
+                GU[v] = a * (dy[j].get(v) + GU[v]);
+                GA[v] *= a;
+            }
+        }
+    }
+    bool cut = m.first != 0, gcut = m.last != 0;
+    compose<V, false, PACKED>(sh, A, U, cut);
+    compose<V, true, PACKED>(sg, GA, GU, gcut);
+    __syncthreads();
+    {
+        // one wave joins the chain of gradients while another one takes the kept state into the block
+        const int c = threadIdx.x & 63, cc = tile * CH + c, wave = threadIdx.x >> 6;
+        if (wave == 0 && c < CH) {
+            const Chain<CH> chain(p, column, columns);
+            uint32_t ba;
+            float bu, in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f;
+            block_map<true, PACKED>(sg, waves, c, ba, bu);
+            if (step > 0 && step < p.nblk - 1) chain.put_map(step, c, ba, bu);
+            if (step > 0) in = chain.enter(step, c);
+            if (step < p.nblk - 1) chain.put_state(step, c, apply(ba, bu, in));
+            wave_states<true, PACKED>(sg, waves, c, in);
+        }
+        if (wave == (waves > 1 ? 1 : 0) && c < CH) {
+            float in = 0.f;
+            if (cc < p.D) {
+                if (k > 0) in = p.ckpt[((int64_t)b * p.nblk + k - 1) * p.D + cc];
+                else if (!PACKED && p.S0) in = p.S0[(int64_t)b * p.D + cc];
+            }
+            wave_states<false, PACKED>(sh, waves, c, in);
+        }
+    }
+    __syncthreads();
+    strand_states<V, false, PACKED>(sh, A, U, cut, h);
+    strand_states<V, true, PACKED>(sg, GA, GU, gcut, G);
+    // two channels at a time: the states before each token, then the gradients from the last token back
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+        float before[2][kL];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float s = h[v + e];
+#pragma unroll
+            for (int j = 0; j < kL; ++j) {
+                before[e][j] = 0.f;
+                if (!(m.in >> j & 1)) continue;
+                if (PACKED && (m.first >> j & 1))
+                    s = p.S0 && v + e < n ? p.S0[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] : 0.f;
+                before[e][j] = s;
                 float a, bb;
-                gates<BETA>(p, al[j].get(v), BETA ? be[BETA ? j : 0].get(v) : 0.f, a, bb);
-                const float u = bb * x[j].get(v);
-                if (first) {
-                    U[v] = fmaf(a, s0[v], u);
-                    A[v] = 0.f;
-                } else {
-                    U[v] = fmaf(a, U[v], u);
-                    A[v] *= a;
-                }
+                gates<BETA>(p, al[j].get(v + e), BETA ? be[BETA ? j : 0].get(v + e) : 0.f, a, bb);
+                s = fmaf(a, s, bb * x[j].get(v + e));
             }
         }
 #pragma unroll
         for (int j = kL - 1; j >= 0; --j) {
             if (!(m.in >> j & 1)) continue;
-            float st[V];
-            const bool last = PACKED && (m.last >> j & 1);
-            if (last) load_state<V>(p.dST ? p.dST + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, st);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float a, bb;
-                gates<BETA>(p, al[j].get(v), 0.f, a, bb);
-                if (last) {
-                    GU[v] = a * (dy[j].get(v) + st[v]);
-                    GA[v] = 0.f;
-                } else {
-                    GU[v] = a * (dy[j].get(v) + GU[v]);
-                    GA[v] *= a;
-                }
-            }
-        }
-        enter<V, false, PACKED>(sh, 0, waves, A, U, m.first != 0, h);
-        enter<V, true, PACKED>(sg, step & 1, waves, GA, GU, m.last != 0, G);
-        // two channels at a time: the states before each token, then the gradients from the last token back
-#pragma unroll
-        for (int v = 0; v < V; v += 2) {
-            float before[2][kL];
+            float dx[2], da[2], db[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float s = h[v + e];
-#pragma unroll
-                for (int j = 0; j < kL; ++j) {
-                    before[e][j] = 0.f;
-                    if (!(m.in >> j & 1)) continue;
-                    if (PACKED && (m.first >> j & 1))
-                        s = p.S0 && v + e < n ? p.S0[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] : 0.f;
-                    before[e][j] = s;
-                    float a, bb;
-                    gates<BETA>(p, al[j].get(v + e), BETA ? be[BETA ? j : 0].get(v + e) : 0.f, a, bb);
-                    s = fmaf(a, s, bb * x[j].get(v + e));
-                }
+                float a, bb;
+                gates<BETA>(p, al[j].get(v + e), BETA ? be[BETA ? j : 0].get(v + e) : 0.f, a, bb);
+                if (PACKED && (m.last >> j & 1))
+                    G[v + e] = p.dST && v + e < n ? p.dST[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] : 0.f;
+                const float g = dy[j].get(v + e) + G[v + e], xv = x[j].get(v + e);
+                dx[e] = bb * g;
+                db[e] = g * xv;
+                da[e] = g * (p.coupled ? before[e][j] - xv : before[e][j]);
+                if (p.log_gate) da[e] *= a;
+                G[v + e] = a * g;
+                if (PACKED && p.dS0 && (m.first >> j & 1) && v + e < n)
+                    p.dS0[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] = G[v + e];
             }
-#pragma unroll
-            for (int j = kL - 1; j >= 0; --j) {
-                if (!(m.in >> j & 1)) continue;
-                float dx[2], da[2], db[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float a, bb;
-                    gates<BETA>(p, al[j].get(v + e), BETA ? be[BETA ? j : 0].get(v + e) : 0.f, a, bb);
-                    if (PACKED && (m.last >> j & 1))
-                        G[v + e] = p.dST && v + e < n ? p.dST[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] : 0.f;
-                    const float g = dy[j].get(v + e) + G[v + e], xv = x[j].get(v + e);
-                    dx[e] = bb * g;
-                    db[e] = g * xv;
-                    da[e] = g * (p.coupled ? before[e][j] - xv : before[e][j]);
-                    if (p.log_gate) da[e] *= a;
-                    G[v + e] = a * g;
-                    if (PACKED && p.dS0 && (m.first >> j & 1) && v + e < n)
-                        p.dS0[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] = G[v + e];
-                }
-                dy[j].set2(v, dx[0], dx[1]);
-                al[j].set2(v, da[0], da[1]);
-                if (BETA) be[BETA ? j : 0].set2(v, db[0], db[1]);
-            }
+            dy[j].set2(v, dx[0], dx[1]);
+            al[j].set2(v, da[0], da[1]);
+            if (BETA) be[BETA ? j : 0].set2(v, db[0], db[1]);
         }
-#pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            if (!(m.in >> j & 1)) continue;
-            dy[j].store(p.dx, (row + j) * p.D + ch, n);
-            al[j].store(p.dalpha, (row + j) * p.D + ch, n);
-            if (BETA) be[BETA ? j : 0].store(p.dbeta, (row + j) * p.D + ch, n);
-        }
-        if (strand == 0) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) sg.carry[(step + 1) & 1][lr * V + v] = G[v];
-        }
-        __syncthreads();
     }
-    if (!PACKED && strand == 0 && p.dS0) store_state<V>(p.dS0 + (int64_t)b * p.D + ch, n, G);
+#pragma unroll
+    for (int j = 0; j < kL; ++j) {
+        if (!(m.in >> j & 1)) continue;
+        dy[j].store(p.dx, (row + j) * p.D + ch, n);
+        al[j].store(p.dalpha, (row + j) * p.D + ch, n);
+        if (BETA) be[BETA ? j : 0].store(p.dbeta, (row + j) * p.D + ch, n);
+    }
+    if (!PACKED && strand == 0 && k == 0 && p.dS0) store_state<V>(p.dS0 + (int64_t)b * p.D + ch, n, G);
+}
+
+// Every word of the chain to kNone (a kernel, so that a captured graph replays it).
+__global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) ws[i] = (u32x4){kNone, kNone, kNone, kNone};
 }
 
 // One token for every batch row: the state is read and written in place.
@@ -542,21 +679,40 @@ hipError_t copy_states(const float *src, float *dst, long n, hipStream_t s) {
                            args, 0, s);
 }
 
+// Bytes of the chain's words: a map and a state per block, sequence and channel of whole tiles.
+long chain_bytes(const ScanParams &p, int v) {
+    if (p.nblk <= 1) return 0;
+    const long ch = kLR * v, columns = (long)p.B * ((p.D + ch - 1) / ch);
+    return kChainHead + (columns * p.nblk * ch * 12 + 15) / 16 * 16;
+}
+
 template <Kind K>
 hipError_t launch(const ScanParams &p, hipStream_t s) {
     int v = 0;
     const void *fn = pick<K>(p, v);
     const int waves = (int)(((p.T < kBlk ? p.T : kBlk) + 63) / 64);
-    ScanParams q = p;
-    void *args[] = {&q};
-    const long blocks = (long)p.B * ((p.D + kLR * v - 1) / (kLR * v));
+    const long ch = kLR * v, blocks = (long)p.B * ((p.D + ch - 1) / ch) * p.nblk;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    ScanParams q = p;
+    if (p.nblk > 1) {
+        u32x4 *ws = static_cast<u32x4 *>(p.ws);
+        long n = chain_bytes(p, v) / 16;
+        void *args[] = {&ws, &n};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&scan_fill_kernel), dim3((unsigned)((n + 255) / 256)),
+                                             dim3(256), args, 0, s);
+        if (e != hipSuccess) return e;
+    }
+    void *args[] = {&q};
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * waves), args, 0, s);
 }
 
 }  // namespace
 
-size_t scan_workspace(const ScanParams &) { return 0; }
+size_t scan_workspace(const ScanParams &p) {
+    int v = 0;
+    (void)pick<kFwd>(p, v);
+    return (size_t)chain_bytes(p, v);
+}
 
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s) {
     if (p.T == 0) return copy_states(p.S0, p.ST, (long)(p.off ? p.nseq : p.B) * p.D, s);
