@@ -33,7 +33,7 @@ GDR_FLAG_UNDECAYED_PREDICTION = 0x20
 GDR_FLAG_LOG_GATE, GDR_FLAG_COUPLED = 0x40, 0x80
 GDR_NORM_NONE, GDR_NORM_L2, GDR_NORM_RMS = 0, 1, 2
 GDR_ROT_HALF, GDR_ROT_INTERLEAVED = 0, 1
-GDR_SCAN_BLOCK = 512
+GDR_SCAN_BLOCK = 256
 PATH_MFMA, PATH_VALU = 1, 2
 
 
@@ -779,7 +779,7 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
 
     a = alpha [B, T, H, dv] (or exp(alpha) with log_gate); b = beta where given, 1 - a with coupled, else 1.
     seq_offsets [n + 1] int32 cuts the T rows of a B = 1 batch into packed sequences; S0 [B or n, H, dv] fp32.
-    Returns (y like x, ST like S0 or None, ckpt [B, ceil(T / 512), H, dv] fp32 for scan_bwd or None).  Rows of y that
+    Returns (y like x, ST like S0 or None, ckpt [B, ceil(T / 256), H, dv] fp32 for scan_bwd or None).  Rows of y that
     belong to no packed sequence are left unwritten."""
     desc = _scan_desc(x, alpha, log_gate, coupled)
     n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
@@ -799,7 +799,7 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
 
 def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0=None, dST=None, seq_offsets=None,
              workspace=None, stream=None):
-    """Backward pass of scan_fwd with its inputs and its ckpt (None where T <= 512): gradients dy of y (dense) and
+    """Backward pass of scan_fwd with its inputs and its ckpt (None where T <= 256): gradients dy of y (dense) and
     dST of ST.  Returns (dx, dalpha, dbeta or None, dS0): dalpha is the gradient of alpha as stored."""
     desc = _scan_desc(x, alpha, log_gate, coupled)
     n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)

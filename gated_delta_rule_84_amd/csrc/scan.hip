@@ -12,7 +12,7 @@
 // and h_{t-1} is formed again inside each block from the state that the forward pass kept
 // at the block's border, so no state of a token is stored or read.
 //
-// Layout: a workgroup takes blocks of 512 tokens x CH channels.  8 lanes hold a row of the
+// Layout: a workgroup takes a block of 256 tokens x CH channels.  8 lanes hold a row of the
 // block (V channels each: 16-byte loads, 128-byte rows of bf16) and a lane holds 8 tokens
 // one after the other (a strand), all of its inputs in registers between the reduction and
 // the second pass, so every input is read once.
@@ -28,12 +28,22 @@ namespace gdr {
 namespace {
 
 constexpr int kBlk = GDR_SCAN_BLOCK;  // tokens per block
-constexpr int kL = 8;                 // tokens per strand
 constexpr int kLR = 8;                // lanes per row
-constexpr int kStrands = kBlk / kL;   // 64
-constexpr int kThreads = kStrands * kLR;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWS = 64 / kLR;         // strands per wave
 constexpr int kChainHead = 256;       // bytes before the chain's words: the counter of blocks
+
+// How the input factor b is given.
+enum Factor { kOne = 0, kGiven = 1, kCoupled = 2 };
+
+// Channels per lane, tokens per strand and lanes per workgroup for a pair of types.
+template <bool IOB, bool GB>
+struct Shape {
+    static constexpr int V = IOB && GB ? 8 : 4;
+    static constexpr int L = 32 / V;
+    static constexpr int threads = kBlk / L * kLR;
+    static constexpr int waves = threads / 64;
+    static constexpr int CH = kLR * V;  // channels per workgroup
+};
 
 typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
@@ -132,22 +142,49 @@ __device__ __forceinline__ void store_state(float *p, int n, const float (&f)[V]
         if (v < n) p[v] = f[v];
 }
 
-// Decay and input factor of one token and channel from the stored gate values.
-template <bool BETA>
-__device__ __forceinline__ void gates(const ScanParams &p, float raw, float beta, float &a, float &b) {
-    a = p.log_gate ? expf(raw) : raw;
-    b = BETA ? beta : (p.coupled ? (p.log_gate ? -expm1f(raw) : 1.f - raw) : 1.f);
+// exp(x) and 1 - exp(x), both to about 2 units in the last place.  With n = rint(x / ln 2) and
+// r = x - n ln 2 (ln 2 in two parts), exp(x) = s + s q and exp(x) - 1 = (s - 1) + s q for s = 2^n and
+// q = exp(r) - 1, a polynomial on |r| <= 0.35 whose last term left out is r^8 / 8! < 2^-26 r.
+// For x near 0, where 1 - exp(x) would cancel, s = 1 and the result is q itself.
+__device__ __forceinline__ void exp_both(float x, float &a, float &b) {
+    x = x < -150.f ? -150.f : (x > 150.f ? 150.f : x);  // past the range of fp32 either way; NaN stays
+    const float n = rintf(x * 1.44269504f);
+    float r = fmaf(n, -0.693145752f, x);
+    r = fmaf(n, -1.42860677e-6f, r);
+    float q = fmaf(r, 1.f / 5040, 1.f / 720);
+    q = fmaf(r, q, 1.f / 120);
+    q = fmaf(r, q, 1.f / 24);
+    q = fmaf(r, q, 1.f / 6);
+    q = fmaf(r, q, 0.5f);
+    q = fmaf(r * r, q, r);
+    const int e = (int)n;
+    a = ldexpf(1.f + q, e);
+    const float s = ldexpf(1.f, e);
+    b = x > 1.f ? 1.f - a : -fmaf(s, q, s - 1.f);  // s may be infinite for large x
 }
 
-// The tokens t0 .. t0 + 7 of a strand: bit j of `in` where the token belongs to a sequence,
+// Decays and input factors of a lane's channels of one token (b is 1 for kOne).
+template <int F, bool GB, int V>
+__device__ __forceinline__ void gates(bool log, const Pack<GB, V> &al, const Pack<GB, V> &be, float (&a)[V], float (&b)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float g = al.get(v);
+        float c = 1.f - g;
+        a[v] = g;
+        if (log) exp_both(g, a[v], c);
+        b[v] = F == kGiven ? be.get(v) : (F == kCoupled ? c : 1.f);
+    }
+}
+
+// The tokens t0 .. t0 + L - 1 of a strand: bit j of `in` where the token belongs to a sequence,
 // of `first` / `last` where it opens / closes one; seq[j] its sequence.  Offsets are read
 // with sequence numbers clamped to 0 .. nseq, whatever they hold.
-template <bool PACKED>
+template <bool PACKED, int L>
 struct Marks {
     unsigned in = 0, first = 0, last = 0;
-    int seq[PACKED ? kL : 1];
+    int seq[L];
 
-    __device__ __forceinline__ void find(const ScanParams &p, int b, long t0) {
+    __device__ __forceinline__ void find(const ScanParams &p, long t0) {
         if constexpr (PACKED) {
             int lo = 0, hi = p.nseq;  // first sequence that ends after t0
             while (lo < hi) {
@@ -157,7 +194,7 @@ struct Marks {
             }
             int i = lo;
 #pragma unroll
-            for (int j = 0; j < kL; ++j) {
+            for (int j = 0; j < L; ++j) {
                 const long t = t0 + j;
                 while (i < p.nseq && p.off[i + 1] <= t) ++i;
                 const bool ok = i < p.nseq && t < p.T && p.off[i] <= t;
@@ -168,8 +205,7 @@ struct Marks {
             }
         } else {
             const long n = p.T - t0;
-            in = n >= kL ? (1u << kL) - 1 : (n > 0 ? (1u << n) - 1 : 0);
-            seq[0] = b;
+            in = n >= L ? (1u << L) - 1 : (n > 0 ? (1u << n) - 1 : 0);
         }
     }
 };
@@ -250,11 +286,11 @@ struct Chain {
     }
 };
 
+template <int W, int CH>
 struct Shared {
-    float A[kWaves][kLR * 8], U[kWaves][kLR * 8];  // a wave's composed map, per channel
-    int cut[kWaves];                               // it holds a border of sequences
-    float in[kWaves][kLR * 8];                     // the state that enters a wave's strands
-    int ticket;
+    float A[W][CH], U[W][CH];  // a wave's composed map, per channel
+    int cut[W];                // it holds a border of sequences
+    float in[W][CH];           // the state that enters a wave's strands
 };
 
 // Composes the strands of a wave: (A, U) is the lane's own map, afterwards that of the
@@ -262,12 +298,12 @@ struct Shared {
 // strands are taken from the last to the first.  A strand with a border of sequences (`cut`)
 // lets nothing of what enters it through: a flag and not A = 0, which would turn an infinity
 // of one sequence into a NaN of the next.
-template <int V, bool REV, bool PACKED>
-__device__ __forceinline__ void compose(Shared &sh, float (&A)[V], float (&U)[V], bool &cut) {
+template <int V, bool REV, bool PACKED, class S>
+__device__ __forceinline__ void compose(S &sh, float (&A)[V], float (&U)[V], bool &cut) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
-    const int strand = REV ? 63 / kLR - lane / kLR : lane / kLR;
+    const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
 #pragma unroll
-    for (int s = 1; s < 64 / kLR; s <<= 1) {
+    for (int s = 1; s < kWS; s <<= 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float a = REV ? __shfl_down(A[v], s * kLR) : __shfl_up(A[v], s * kLR);
@@ -282,7 +318,7 @@ __device__ __forceinline__ void compose(Shared &sh, float (&A)[V], float (&U)[V]
             if (strand >= s) cut = cut || c;
         }
     }
-    if (strand == 64 / kLR - 1) {
+    if (strand == kWS - 1) {
         if (PACKED) sh.cut[wave] = cut;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -293,8 +329,8 @@ __device__ __forceinline__ void compose(Shared &sh, float (&A)[V], float (&U)[V]
 }
 
 // One lane per channel: the composed map of the workgroup's waves, in the order of the strands.
-template <bool REV, bool PACKED>
-__device__ __forceinline__ void block_map(const Shared &sh, int waves, int c, uint32_t &A, float &U) {
+template <bool REV, bool PACKED, class S>
+__device__ __forceinline__ void block_map(const S &sh, int waves, int c, uint32_t &A, float &U) {
     float a = 1.f, u = 0.f;
     bool cut = false;
     for (int i = 0; i < waves; ++i) {
@@ -312,8 +348,8 @@ __device__ __forceinline__ void block_map(const Shared &sh, int waves, int c, ui
 }
 
 // One lane per channel: the state that enters each wave when h enters the block.
-template <bool REV, bool PACKED>
-__device__ __forceinline__ void wave_states(Shared &sh, int waves, int c, float h) {
+template <bool REV, bool PACKED, class S>
+__device__ __forceinline__ void wave_states(S &sh, int waves, int c, float h) {
     for (int i = 0; i < waves; ++i) {
         const int w = REV ? waves - 1 - i : i;
         sh.in[w][c] = h;
@@ -322,10 +358,10 @@ __device__ __forceinline__ void wave_states(Shared &sh, int waves, int c, float 
 }
 
 // The state that enters the lane's strand.
-template <int V, bool REV, bool PACKED>
-__device__ __forceinline__ void strand_states(const Shared &sh, const float (&A)[V], const float (&U)[V], bool cut, float (&h)[V]) {
+template <int V, bool REV, bool PACKED, class S>
+__device__ __forceinline__ void strand_states(const S &sh, const float (&A)[V], const float (&U)[V], bool cut, float (&h)[V]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
-    const int strand = REV ? 63 / kLR - lane / kLR : lane / kLR;
+    const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
     const int before = PACKED ? (REV ? __shfl_down((int)cut, kLR) : __shfl_up((int)cut, kLR)) : 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -339,69 +375,63 @@ __device__ __forceinline__ void strand_states(const Shared &sh, const float (&A)
 // This workgroup's place: blocks in the order of the recurrence, all channels of one block
 // before the next (neighbours read neighbouring memory, and a block's predecessors began long
 // before it).
-__device__ __forceinline__ long place(const ScanParams &p, Shared &sh) {
+__device__ __forceinline__ unsigned place(const ScanParams &p, int &ticket) {
     if (p.nblk == 1) return blockIdx.x;
-    if (threadIdx.x == 0) sh.ticket = (int)(atomicAdd(static_cast<uint32_t *>(p.ws), 1u) + 1u);  // starts at kNone
+    if (threadIdx.x == 0) ticket = (int)(atomicAdd(static_cast<uint32_t *>(p.ws), 1u) + 1u);  // starts at kNone
     __syncthreads();
-    return (uint32_t)sh.ticket;
+    return (unsigned)ticket;
 }
 
-template <bool IOB, bool GB, bool BETA, bool PACKED, int V>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
-    constexpr int CH = kLR * V;
-    __shared__ Shared sh;
-    const int waves = blockDim.x >> 6, tiles = (p.D + CH - 1) / CH;
-    const long columns = (long)p.B * tiles, id = place(p, sh), column = id % columns;
-    const int k = (int)(id / columns), b = (int)(column / tiles), tile = (int)(column % tiles);
+template <bool IOB, bool GB, int F, bool PACKED>
+__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(ScanParams p) {
+    typedef Shape<IOB, GB> Sh;
+    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH;
+    __shared__ Shared<Sh::waves, CH> sh;
+    __shared__ int ticket;
+    const int waves = blockDim.x >> 6;
+    const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
+    const unsigned column = id % columns, k = id / columns, b = column / tiles, tile = column % tiles;
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const long t0 = (long)k * kBlk + strand * kL, row = (long)b * p.T + t0;
-    Marks<PACKED> m;
-    m.find(p, b, t0);
-    Pack<IOB, V> x[kL];
-    Pack<GB, V> al[kL], be[BETA ? kL : 1];
+    const long t0 = (long)k * kBlk + strand * L, row = (long)b * p.T + t0;
+    Marks<PACKED, L> m;
+    m.find(p, t0);
+    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
+    Pack<IOB, V> x[L];
+    Pack<GB, V> al[L], be[F == kGiven ? L : 1];
 #pragma unroll
-    for (int j = 0; j < kL; ++j) {
-        x[j].clear();
-        al[j].clear();
-        if (BETA) be[j].clear();
-        if (!(m.in >> j & 1)) continue;
-        x[j].load(p.x, (row + j) * p.ldx + ch, n);
-        al[j].load(p.alpha, (row + j) * p.lda + ch, n);
-        if (BETA) be[j].load(p.beta, (row + j) * p.ldb + ch, n);
+    for (int j = 0; j < L; ++j) {
+        if (m.in >> j & 1) {
+            x[j].load(p.x, (row + j) * p.ldx + ch, n);
+            al[j].load(p.alpha, (row + j) * p.lda + ch, n);
+            if (F == kGiven) be[F == kGiven ? j : 0].load(p.beta, (row + j) * p.ldb + ch, n);
+        }
     }
     if (PACKED && p.ST && k == 0) {  // empty sequences end as they begin
-        for (int i = strand; i < p.nseq; i += waves * (64 / kLR)) {
+        for (int i = strand; i < p.nseq; i += waves * kWS) {
             if (p.off[i + 1] > p.off[i]) continue;
             float c[V];
             load_state<V>(p.S0 ? p.S0 + (int64_t)i * p.D + ch : nullptr, n, c);
             store_state<V>(p.ST + (int64_t)i * p.D + ch, n, c);
         }
     }
-    float A[V], U[V], h[V];
+    float a[L][V], u[L][V], A[V], U[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         A[v] = 1.f;
         U[v] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < kL; ++j) {
+    for (int j = 0; j < L; ++j) {
         if (!(m.in >> j & 1)) continue;
-        float s0[V];
+        gates<F, GB, V>(p.log_gate, al[j], be[F == kGiven ? j : 0], a[j], u[j]);
         const bool first = PACKED && (m.first >> j & 1);
-        if (first) load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, s0);
+        if (first) load_state<V>(state(p.S0, j), n, U);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float a, bb;
-            gates<BETA>(p, al[j].get(v), BETA ? be[BETA ? j : 0].get(v) : 0.f, a, bb);
-            const float u = bb * x[j].get(v);
-            if (first) {
-                U[v] = fmaf(a, s0[v], u);
-                A[v] = 0.f;
-            } else {
-                U[v] = fmaf(a, U[v], u);
-                A[v] *= a;
-            }
+            u[j][v] *= x[j].get(v);
+            U[v] = fmaf(a[j][v], U[v], u[j][v]);
+            A[v] = first ? 0.f : A[v] * a[j][v];
         }
     }
     bool cut = m.first != 0;
@@ -413,9 +443,9 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
         uint32_t ba;
         float bu, in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f;
         block_map<false, PACKED>(sh, waves, c, ba, bu);
-        if (p.nblk > 1) {
-            if (k > 0 && k < p.nblk - 1) chain.put_map(k, c, ba, bu);
-            if (k > 0) in = chain.enter(k, c);
+        if (k > 0) {
+            if (k < p.nblk - 1) chain.put_map(k, c, ba, bu);
+            in = chain.enter(k, c);
         }
         const float out = apply(ba, bu, in);
         if (k < p.nblk - 1) chain.put_state(k, c, out);
@@ -425,105 +455,82 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
     __syncthreads();
     strand_states<V, false, PACKED>(sh, A, U, cut, h);
 #pragma unroll
-    for (int j = 0; j < kL; ++j) {
+    for (int j = 0; j < L; ++j) {
         if (!(m.in >> j & 1)) continue;
-        if (PACKED && (m.first >> j & 1))
-            load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, h);
+        if (PACKED && (m.first >> j & 1)) load_state<V>(state(p.S0, j), n, h);
 #pragma unroll
-        for (int v = 0; v < V; v += 2) {
+        for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], u[j][v]);
 #pragma unroll
-            for (int e = v; e < v + 2; ++e) {
-                float a, bb;
-                gates<BETA>(p, al[j].get(e), BETA ? be[BETA ? j : 0].get(e) : 0.f, a, bb);
-                h[e] = fmaf(a, h[e], bb * x[j].get(e));
-            }
-            x[j].set2(v, h[v], h[v + 1]);
-        }
+        for (int v = 0; v < V; v += 2) x[j].set2(v, h[v], h[v + 1]);
         x[j].store(p.y, (row + j) * p.D + ch, n);
-        if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch, n, h);
+        if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[j] * p.D + ch, n, h);
     }
-    if (!PACKED && p.ST && k == p.nblk - 1 && strand == waves * (64 / kLR) - 1)
+    if (!PACKED && p.ST && k == p.nblk - 1 && strand == waves * kWS - 1)
         store_state<V>(p.ST + (int64_t)b * p.D + ch, n, h);
 }
 
-template <bool IOB, bool GB, bool BETA, bool PACKED, int V>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
-    constexpr int CH = kLR * V;
-    __shared__ Shared sh, sg;
-    const int waves = blockDim.x >> 6, tiles = (p.D + CH - 1) / CH;
-    const long columns = (long)p.B * tiles, id = place(p, sh), column = id % columns;
-    const int step = (int)(id / columns), k = p.nblk - 1 - step;  // blocks from the last to the first
-    const int b = (int)(column / tiles), tile = (int)(column % tiles);
+template <bool IOB, bool GB, int F, bool PACKED>
+__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(ScanParams p) {
+    typedef Shape<IOB, GB> Sh;
+    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH;
+    __shared__ Shared<Sh::waves, CH> sh, sg;
+    __shared__ int ticket;
+    const int waves = blockDim.x >> 6;
+    const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
+    const unsigned column = id % columns, step = id / columns, k = p.nblk - 1 - step;  // from the last block to the first
+    const unsigned b = column / tiles, tile = column % tiles;
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const long t0 = (long)k * kBlk + strand * kL, row = (long)b * p.T + t0;
-    Marks<PACKED> m;
-    m.find(p, b, t0);
-    Pack<IOB, V> x[kL], dy[kL];
-    Pack<GB, V> al[kL], be[BETA ? kL : 1];
+    const long t0 = (long)k * kBlk + strand * L, row = (long)b * p.T + t0;
+    Marks<PACKED, L> m;
+    m.find(p, t0);
+    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
+    Pack<IOB, V> x[L], dy[L];
+    Pack<GB, V> al[L], be[F == kGiven ? L : 1];
 #pragma unroll
-    for (int j = 0; j < kL; ++j) {
-        x[j].clear();
-        dy[j].clear();
-        al[j].clear();
-        if (BETA) be[j].clear();
-        if (!(m.in >> j & 1)) continue;
-        x[j].load(p.x, (row + j) * p.ldx + ch, n);
-        dy[j].load(p.dy, (row + j) * p.D + ch, n);
-        al[j].load(p.alpha, (row + j) * p.lda + ch, n);
-        if (BETA) be[j].load(p.beta, (row + j) * p.ldb + ch, n);
+    for (int j = 0; j < L; ++j) {
+        if (m.in >> j & 1) {
+            x[j].load(p.x, (row + j) * p.ldx + ch, n);
+            dy[j].load(p.dy, (row + j) * p.D + ch, n);
+            al[j].load(p.alpha, (row + j) * p.lda + ch, n);
+            if (F == kGiven) be[F == kGiven ? j : 0].load(p.beta, (row + j) * p.ldb + ch, n);
+        }
     }
     if (PACKED && p.dS0 && k == 0) {
-        for (int i = strand; i < p.nseq; i += waves * (64 / kLR)) {
+        for (int i = strand; i < p.nseq; i += waves * kWS) {
             if (p.off[i + 1] > p.off[i]) continue;
             float c[V];
             load_state<V>(p.dST ? p.dST + (int64_t)i * p.D + ch : nullptr, n, c);
             store_state<V>(p.dS0 + (int64_t)i * p.D + ch, n, c);
         }
     }
-    float A[V], U[V], GA[V], GU[V], h[V], G[V];
+    float a[L][V], bb[L][V], A[V], U[V], GA[V], GU[V], h[V], G[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         A[v] = GA[v] = 1.f;
         U[v] = GU[v] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < kL; ++j) {
+    for (int j = 0; j < L; ++j) {
         if (!(m.in >> j & 1)) continue;
-        float s0[V];
+        gates<F, GB, V>(p.log_gate, al[j], be[F == kGiven ? j : 0], a[j], bb[j]);
         const bool first = PACKED && (m.first >> j & 1);
-        if (first) load_state<V>(p.S0 ? p.S0 + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, s0);
+        if (first) load_state<V>(state(p.S0, j), n, U);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float a, bb;
-            gates<BETA>(p, al[j].get(v), BETA ? be[BETA ? j : 0].get(v) : 0.f, a, bb);
-            const float u = bb * x[j].get(v);
-            if (first) {
-                U[v] = fmaf(a, s0[v], u);
-                A[v] = 0.f;
-            } else {
-                U[v] = fmaf(a, U[v], u);
-                A[v] *= a;
-            }
+            U[v] = fmaf(a[j][v], U[v], bb[j][v] * x[j].get(v));
+            A[v] = first ? 0.f : A[v] * a[j][v];
         }
     }
 #pragma unroll
-    for (int j = kL - 1; j >= 0; --j) {
+    for (int j = L - 1; j >= 0; --j) {
         if (!(m.in >> j & 1)) continue;
-        float st[V];
         const bool last = PACKED && (m.last >> j & 1);
-        if (last) load_state<V>(p.dST ? p.dST + (int64_t)m.seq[PACKED ? j : 0] * p.D + ch : nullptr, n, st);
+        if (last) load_state<V>(state(p.dST, j), n, GU);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float a, bb;
-            gates<BETA>(p, al[j].get(v), 0.f, a, bb);
-            if (last) {
-                GU[v] = a * (dy[j].get(v) + st[v]);
-                GA[v] = 0.f;
-            } else {
-                GU[v] = a * (dy[j].get(v) + GU[v]);
-                GA[v] *= a;
-            }
+            GU[v] = a[j][v] * (dy[j].get(v) + GU[v]);
+            GA[v] = last ? 0.f : GA[v] * a[j][v];
         }
     }
     bool cut = m.first != 0, gcut = m.last != 0;
@@ -538,8 +545,10 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
             uint32_t ba;
             float bu, in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f;
             block_map<true, PACKED>(sg, waves, c, ba, bu);
-            if (step > 0 && step < p.nblk - 1) chain.put_map(step, c, ba, bu);
-            if (step > 0) in = chain.enter(step, c);
+            if (step > 0) {
+                if (step < p.nblk - 1) chain.put_map(step, c, ba, bu);
+                in = chain.enter(step, c);
+            }
             if (step < p.nblk - 1) chain.put_state(step, c, apply(ba, bu, in));
             wave_states<true, PACKED>(sg, waves, c, in);
         }
@@ -558,52 +567,45 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
     // two channels at a time: the states before each token, then the gradients from the last token back
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
-        float before[2][kL];
+        float before[2][L];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float s = h[v + e];
 #pragma unroll
-            for (int j = 0; j < kL; ++j) {
-                before[e][j] = 0.f;
+            for (int j = 0; j < L; ++j) {
                 if (!(m.in >> j & 1)) continue;
-                if (PACKED && (m.first >> j & 1))
-                    s = p.S0 && v + e < n ? p.S0[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] : 0.f;
+                if (PACKED && (m.first >> j & 1)) s = p.S0 && v + e < n ? state(p.S0, j)[v + e] : 0.f;
                 before[e][j] = s;
-                float a, bb;
-                gates<BETA>(p, al[j].get(v + e), BETA ? be[BETA ? j : 0].get(v + e) : 0.f, a, bb);
-                s = fmaf(a, s, bb * x[j].get(v + e));
+                s = fmaf(a[j][v + e], s, bb[j][v + e] * x[j].get(v + e));
             }
         }
 #pragma unroll
-        for (int j = kL - 1; j >= 0; --j) {
+        for (int j = L - 1; j >= 0; --j) {
             if (!(m.in >> j & 1)) continue;
             float dx[2], da[2], db[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float a, bb;
-                gates<BETA>(p, al[j].get(v + e), BETA ? be[BETA ? j : 0].get(v + e) : 0.f, a, bb);
-                if (PACKED && (m.last >> j & 1))
-                    G[v + e] = p.dST && v + e < n ? p.dST[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] : 0.f;
+                if (PACKED && (m.last >> j & 1)) G[v + e] = p.dST && v + e < n ? state(p.dST, j)[v + e] : 0.f;
                 const float g = dy[j].get(v + e) + G[v + e], xv = x[j].get(v + e);
-                dx[e] = bb * g;
+                dx[e] = bb[j][v + e] * g;
                 db[e] = g * xv;
-                da[e] = g * (p.coupled ? before[e][j] - xv : before[e][j]);
-                if (p.log_gate) da[e] *= a;
-                G[v + e] = a * g;
+                da[e] = g * (F == kCoupled ? before[e][j] - xv : before[e][j]);
+                G[v + e] = a[j][v + e] * g;
+                if (p.log_gate) da[e] *= a[j][v + e];
                 if (PACKED && p.dS0 && (m.first >> j & 1) && v + e < n)
-                    p.dS0[(int64_t)m.seq[PACKED ? j : 0] * p.D + ch + v + e] = G[v + e];
+                    p.dS0[(int64_t)m.seq[j] * p.D + ch + v + e] = G[v + e];
             }
             dy[j].set2(v, dx[0], dx[1]);
             al[j].set2(v, da[0], da[1]);
-            if (BETA) be[BETA ? j : 0].set2(v, db[0], db[1]);
+            if (F == kGiven) be[F == kGiven ? j : 0].set2(v, db[0], db[1]);
         }
     }
 #pragma unroll
-    for (int j = 0; j < kL; ++j) {
+    for (int j = 0; j < L; ++j) {
         if (!(m.in >> j & 1)) continue;
         dy[j].store(p.dx, (row + j) * p.D + ch, n);
         al[j].store(p.dalpha, (row + j) * p.D + ch, n);
-        if (BETA) be[BETA ? j : 0].store(p.dbeta, (row + j) * p.D + ch, n);
+        if (F == kGiven) be[F == kGiven ? j : 0].store(p.dbeta, (row + j) * p.D + ch, n);
     }
     if (!PACKED && strand == 0 && k == 0 && p.dS0) store_state<V>(p.dS0 + (int64_t)b * p.D + ch, n, G);
 }
@@ -615,30 +617,26 @@ __global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
 }
 
 // One token for every batch row: the state is read and written in place.
-template <bool IOB, bool GB, bool BETA, int V>
+template <bool IOB, bool GB, int F>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
-    const long groups = (p.D + V - 1) / V, i = (long)blockIdx.x * 256 + threadIdx.x;
-    const long b = i / groups;
-    const int ch = (int)(i % groups) * V, n = min(V, p.D - ch);
+    constexpr int V = Shape<IOB, GB>::V;
+    const unsigned groups = (p.D + V - 1) / V;
+    const long i = (long)blockIdx.x * 256 + threadIdx.x, b = i / groups;
+    const int ch = (int)(i - b * groups) * V, n = min(V, p.D - ch);
     if (b >= p.B) return;
     Pack<IOB, V> x;
     Pack<GB, V> al, be;
     float *S = p.ST + b * p.D + ch;
-    float h[V];
+    float a[V], u[V], h[V];
     x.load(p.x, b * p.ldx + ch, n);
     al.load(p.alpha, b * p.lda + ch, n);
-    if (BETA) be.load(p.beta, b * p.ldb + ch, n);
+    if (F == kGiven) be.load(p.beta, b * p.ldb + ch, n);
     load_state<V>(S, n, h);
+    gates<F, GB, V>(p.log_gate, al, be, a, u);
 #pragma unroll
-    for (int v = 0; v < V; v += 2) {
+    for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], h[v], u[v] * x.get(v));
 #pragma unroll
-        for (int e = v; e < v + 2; ++e) {
-            float a, bb;
-            gates<BETA>(p, al.get(e), BETA ? be.get(e) : 0.f, a, bb);
-            h[e] = fmaf(a, h[e], bb * x.get(e));
-        }
-        x.set2(v, h[v], h[v + 1]);
-    }
+    for (int v = 0; v < V; v += 2) x.set2(v, h[v], h[v + 1]);
     store_state<V>(S, n, h);
     x.store(p.y, b * p.D + ch, n);
 }
@@ -651,25 +649,35 @@ __global__ void __launch_bounds__(256) scan_copy_kernel(const float *src, float 
 
 enum Kind { kFwd, kBwd, kStep };
 
-template <Kind K, bool IOB, bool GB, bool BETA, bool PACKED, int V>
+template <Kind K, bool IOB, bool GB, int F, bool PACKED>
 const void *kernel() {
-    if constexpr (K == kFwd) return reinterpret_cast<const void *>(&scan_fwd_kernel<IOB, GB, BETA, PACKED, V>);
-    if constexpr (K == kBwd) return reinterpret_cast<const void *>(&scan_bwd_kernel<IOB, GB, BETA, PACKED, V>);
-    return reinterpret_cast<const void *>(&scan_step_kernel<IOB, GB, BETA, V>);
+    if constexpr (K == kFwd) return reinterpret_cast<const void *>(&scan_fwd_kernel<IOB, GB, F, PACKED>);
+    if constexpr (K == kBwd) return reinterpret_cast<const void *>(&scan_bwd_kernel<IOB, GB, F, PACKED>);
+    return reinterpret_cast<const void *>(&scan_step_kernel<IOB, GB, F>);
+}
+
+// The kernel of a call, with its Shape's numbers.
+struct Pick {
+    const void *fn;
+    int V, L, CH;
+};
+
+template <Kind K, bool IOB, bool GB, int F>
+Pick pick_packed(const ScanParams &p) {
+    typedef Shape<IOB, GB> Sh;
+    return {p.off ? kernel<K, IOB, GB, F, true>() : kernel<K, IOB, GB, F, false>(), Sh::V, Sh::L, Sh::CH};
 }
 
 template <Kind K, bool IOB, bool GB>
-const void *pick2(const ScanParams &p, int &v) {
-    constexpr int V = IOB && GB ? 8 : 4;
-    v = V;
-    if (p.beta) return p.off ? kernel<K, IOB, GB, true, true, V>() : kernel<K, IOB, GB, true, false, V>();
-    return p.off ? kernel<K, IOB, GB, false, true, V>() : kernel<K, IOB, GB, false, false, V>();
+Pick pick_factor(const ScanParams &p) {
+    if (p.beta) return pick_packed<K, IOB, GB, kGiven>(p);
+    return p.coupled ? pick_packed<K, IOB, GB, kCoupled>(p) : pick_packed<K, IOB, GB, kOne>(p);
 }
 
 template <Kind K>
-const void *pick(const ScanParams &p, int &v) {
-    if (p.io_bf16) return p.gate_bf16 ? pick2<K, true, true>(p, v) : pick2<K, true, false>(p, v);
-    return p.gate_bf16 ? pick2<K, false, true>(p, v) : pick2<K, false, false>(p, v);
+Pick pick(const ScanParams &p) {
+    if (p.io_bf16) return p.gate_bf16 ? pick_factor<K, true, true>(p) : pick_factor<K, true, false>(p);
+    return p.gate_bf16 ? pick_factor<K, false, true>(p) : pick_factor<K, false, false>(p);
 }
 
 hipError_t copy_states(const float *src, float *dst, long n, hipStream_t s) {
@@ -680,39 +688,34 @@ hipError_t copy_states(const float *src, float *dst, long n, hipStream_t s) {
 }
 
 // Bytes of the chain's words: a map and a state per block, sequence and channel of whole tiles.
-long chain_bytes(const ScanParams &p, int v) {
+long chain_bytes(const ScanParams &p, int ch) {
     if (p.nblk <= 1) return 0;
-    const long ch = kLR * v, columns = (long)p.B * ((p.D + ch - 1) / ch);
+    const long columns = (long)p.B * ((p.D + ch - 1) / ch);
     return kChainHead + (columns * p.nblk * ch * 12 + 15) / 16 * 16;
 }
 
 template <Kind K>
 hipError_t launch(const ScanParams &p, hipStream_t s) {
-    int v = 0;
-    const void *fn = pick<K>(p, v);
-    const int waves = (int)(((p.T < kBlk ? p.T : kBlk) + 63) / 64);
-    const long ch = kLR * v, blocks = (long)p.B * ((p.D + ch - 1) / ch) * p.nblk;
+    const Pick k = pick<K>(p);
+    const int strands = ((p.T < kBlk ? p.T : kBlk) + k.L - 1) / k.L, waves = (strands + kWS - 1) / kWS;
+    const long blocks = (long)p.B * ((p.D + k.CH - 1) / k.CH) * p.nblk;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    ScanParams q = p;
     if (p.nblk > 1) {
         u32x4 *ws = static_cast<u32x4 *>(p.ws);
-        long n = chain_bytes(p, v) / 16;
+        long n = chain_bytes(p, k.CH) / 16;
         void *args[] = {&ws, &n};
         const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&scan_fill_kernel), dim3((unsigned)((n + 255) / 256)),
                                              dim3(256), args, 0, s);
         if (e != hipSuccess) return e;
     }
+    ScanParams q = p;
     void *args[] = {&q};
-    return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * waves), args, 0, s);
+    return hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(64 * waves), args, 0, s);
 }
 
 }  // namespace
 
-size_t scan_workspace(const ScanParams &p) {
-    int v = 0;
-    (void)pick<kFwd>(p, v);
-    return (size_t)chain_bytes(p, v);
-}
+size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p, pick<kFwd>(p).CH); }
 
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s) {
     if (p.T == 0) return copy_states(p.S0, p.ST, (long)(p.off ? p.nseq : p.B) * p.D, s);
@@ -725,13 +728,12 @@ hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t s) {
 }
 
 hipError_t launch_scan_step(const ScanParams &p, hipStream_t s) {
-    int v = 0;
-    const void *fn = pick<kStep>(p, v);
-    const long threads = (long)p.B * ((p.D + v - 1) / v);
+    const Pick k = pick<kStep>(p);
+    const long threads = (long)p.B * ((p.D + k.V - 1) / k.V);
     if ((threads + 255) / 256 > 0x7fffffffL) return hipErrorInvalidValue;
     ScanParams q = p;
     void *args[] = {&q};
-    return hipLaunchKernel(fn, dim3((unsigned)((threads + 255) / 256)), dim3(256), args, 0, s);
+    return hipLaunchKernel(k.fn, dim3((unsigned)((threads + 255) / 256)), dim3(256), args, 0, s);
 }
 
 }  // namespace gdr

@@ -470,7 +470,7 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *              need one each.
  * Pointers need their element's alignment only.  Outputs overlap no input and no other output.
  */
-#define GDR_SCAN_BLOCK 512
+#define GDR_SCAN_BLOCK 256
 size_t gdr_scan_workspace_size(const gdr_desc *desc);
 int gdr_scan_fwd(const gdr_desc *desc, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
                  int64_t ldb, const int32_t *seq_off, int32_t n_seq, const float *S0, void *y, float *ST, float *ckpt,

@@ -55,7 +55,7 @@ def backward(x, alpha, dy, beta=None, *, dST=None, log=False, coupled=False, S0=
     return dx, da * a if log else da, None if beta is None else db, dS
 
 
-def block_states(x, alpha, beta=None, *, block=512, **kw):
+def block_states(x, alpha, beta=None, *, block, **kw):
     """State after each block of `block` rows of a dense batch."""
     y, _ = forward(x, alpha, beta, **kw)
     T = x.shape[1]

@@ -120,7 +120,7 @@ def test_forward_and_backward(case):
     B, T, H, dv, io, gate, form, kind, fused = case
     x, alpha, how, dy, dST = _inputs(torch, 21, B, T, H, dv, io, gate, form, kind, fused=fused)
     _, _, ckpt, *_ = _run(torch, g, x, alpha, how, dy, dST, io, gate)
-    states = ref.block_states(_np3(x), _np3(alpha), _np3(how["beta"]), log=how["log_gate"], coupled=how["coupled"],
+    states = ref.block_states(_np3(x), _np3(alpha), _np3(how["beta"]), block=g.GDR_SCAN_BLOCK, log=how["log_gate"], coupled=how["coupled"],
                               S0=_np3(how["S0"]))
     assert np.max(np.abs(_np3(ckpt) - states)) <= 1e-4 * max(1.0, np.max(np.abs(states)))
 
@@ -168,7 +168,7 @@ def test_rows_of_no_sequence_and_special_values_stay_apart():
 
     def run(x, alpha, dy, S0):
         outs = [torch.full_like(x, 7.0) for _ in range(4)]
-        ST, ck = torch.empty(5, 1, D, device="cuda"), torch.empty(1, 3, 1, D, device="cuda")
+        ST, ck = torch.empty(5, 1, D, device="cuda"), torch.empty(1, -(-T // g.GDR_SCAN_BLOCK), 1, D, device="cuda")
         dS0 = torch.empty_like(ST)
         assert g.gdr_scan_fwd(desc, x, 0, alpha, 0, how["beta"], 0, off, 5, S0, outs[0], ST, ck, ws, need) == g.GDR_OK
         assert g.gdr_scan_bwd(desc, x, 0, alpha, 0, how["beta"], 0, off, 5, S0, ck, dy, dST, outs[1], outs[2], outs[3], dS0,
