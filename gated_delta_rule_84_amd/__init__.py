@@ -139,9 +139,9 @@ def _ptr(t: Optional[torch.Tensor]):
     if isinstance(t, torch.Tensor):
         if not t.is_contiguous():
             raise ValueError("expected a contiguous (dense row-major) tensor")
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"expected a device tensor, got one on {t.device}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 _TORCH_DTYPE = {GDR_BF16: torch.bfloat16, GDR_F32: torch.float32}
@@ -155,18 +155,24 @@ def _check_all(specs) -> None:
     dtype); sizes and dtypes are checked for all before devices.  An object that is not
     a tensor but has data_ptr() is a raw device address: it is passed as it is, and
     the caller answers for its size."""
-    specs = [s for s in specs if isinstance(s[1], torch.Tensor)]
+    here = wrong = None
     for name, t, count, dtype in specs:
+        if t is None or not isinstance(t, torch.Tensor):
+            continue
         if t.dtype != dtype:
             raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
         if t.numel() != count:
             raise ValueError(f"{name}: expected {count} elements for this descriptor, got {t.numel()} "
                              f"(shape {tuple(t.shape)})")
-    for name, t, _, _ in specs:
-        if t.device.type != "cuda":
+        if here is None:
+            here = torch.cuda.current_device() if t.is_cuda else -2
+        if wrong is None and t.get_device() != here:
+            wrong = name, t
+    if wrong is not None:
+        name, t = wrong
+        if not t.is_cuda:
             raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
-        if t.device.index is not None and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: tensor on {t.device}, current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{name}: tensor on {t.device}, current device is cuda:{torch.cuda.current_device()}")
 
 
 def _check_workspace(workspace, workspace_bytes: int) -> None:
@@ -197,8 +203,8 @@ def _prefill_specs(desc: Desc, q, k, k_w, v, alpha, beta_k, beta_v, S0, o, ST) -
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle without building a Stream object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -412,28 +418,33 @@ def _row_stride(name: str, t: torch.Tensor, inner: int) -> int:
 
 def _addr(name: str, t, ld: int, inner: int):
     """Device address of a tensor of rows `ld` elements apart (0: dense)."""
-    if isinstance(t, torch.Tensor) and t.numel():
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and not (t.is_contiguous() and ld in (0, inner)) and t.numel():
         if t.dim() < 3:
             raise ValueError(f"{name}: expected heads and channels as the last two axes, got shape {tuple(t.shape)}")
         have = _row_stride(name, t, inner)
         if t.numel() > inner and have != (int(ld) or inner):
             raise ValueError(f"{name}: tokens are {have} elements apart, not {int(ld) or inner}")
-    return None if t is None else t.data_ptr()
+    return t.data_ptr()
 
 
-def _check_qk(desc: QkDesc, specs) -> None:
-    if desc.io_dtype not in _TORCH_DTYPE or desc.weight_dtype not in _TORCH_DTYPE or min(
-            desc.B, desc.T, desc.Hq, desc.Hk, desc.d, desc.rot_dim) < 0:
-        return  # the library rejects the descriptor itself
-    n, io, wt = desc.B * desc.T, _TORCH_DTYPE[desc.io_dtype], _TORCH_DTYPE[desc.weight_dtype]
-    kind = {"q": (n * desc.Hq * desc.d, io), "k": (n * desc.Hk * desc.d, io), "w": (desc.d, wt),
-            "positions": (n, torch.int32), "inv_freq": (desc.rot_dim // 2, torch.float64), "dw": (desc.d, torch.float32)}
-    _check_all([(name, t) + kind[what] for name, what, t in specs])
+def _qk_kinds(desc: QkDesc):
+    """(count, dtype) of q, k, the weights, positions and inv_freq; None for a descriptor that the library rejects."""
+    io, wt = _TORCH_DTYPE.get(desc.io_dtype), _TORCH_DTYPE.get(desc.weight_dtype)
+    B, T, Hq, Hk, d, rot = desc.B, desc.T, desc.Hq, desc.Hk, desc.d, desc.rot_dim
+    if io is None or wt is None or min(B, T, Hq, Hk, d, rot) < 0:
+        return None
+    n = B * T
+    return (n * Hq * d, io), (n * Hk * d, io), (d, wt), (n, torch.int32), (rot // 2, torch.float64)
 
 
 def gdr_qk_prep_fwd(desc: QkDesc, q, k, wq, wk, positions, inv_freq, q_out, k_out, stream=None) -> int:
-    _check_qk(desc, [("q", "q", q), ("k", "k", k), ("wq", "w", wq), ("wk", "w", wk), ("positions", "positions", positions),
-                     ("inv_freq", "inv_freq", inv_freq), ("q_out", "q", q_out), ("k_out", "k", k_out)])
+    kinds = _qk_kinds(desc)
+    if kinds is not None:
+        nq, nk, nw, npos, nf = kinds
+        _check_all((("q", q) + nq, ("k", k) + nk, ("wq", wq) + nw, ("wk", wk) + nw, ("positions", positions) + npos,
+                    ("inv_freq", inv_freq) + nf, ("q_out", q_out) + nq, ("k_out", k_out) + nk))
     return int(_lib.gdr_qk_prep_fwd(ctypes.byref(desc), _addr("q", q, desc.ldq, desc.Hq * desc.d),
                                     _addr("k", k, desc.ldk, desc.Hk * desc.d), _ptr(wq), _ptr(wk), _ptr(positions),
                                     _ptr(inv_freq), _ptr(q_out), _ptr(k_out), _stream(stream)))
@@ -445,9 +456,13 @@ def gdr_qk_prep_bwd_workspace_size(desc: QkDesc) -> int:
 
 def gdr_qk_prep_bwd(desc: QkDesc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                     workspace_bytes: int, stream=None) -> int:
-    _check_qk(desc, [("q", "q", q), ("k", "k", k), ("wq", "w", wq), ("wk", "w", wk), ("positions", "positions", positions),
-                     ("inv_freq", "inv_freq", inv_freq), ("dq_out", "q", dq_out), ("dk_out", "k", dk_out), ("dq", "q", dq),
-                     ("dk", "k", dk), ("dwq", "dw", dwq), ("dwk", "dw", dwk)])
+    kinds = _qk_kinds(desc)
+    if kinds is not None:
+        nq, nk, nw, npos, nf = kinds
+        dw = desc.d, torch.float32
+        _check_all((("q", q) + nq, ("k", k) + nk, ("wq", wq) + nw, ("wk", wk) + nw, ("positions", positions) + npos,
+                    ("inv_freq", inv_freq) + nf, ("dq_out", dq_out) + nq, ("dk_out", dk_out) + nk, ("dq", dq) + nq,
+                    ("dk", dk) + nk, ("dwq", dwq) + dw, ("dwk", dwk) + dw))
     _check_workspace(workspace, workspace_bytes)
     return int(_lib.gdr_qk_prep_bwd(ctypes.byref(desc), _addr("q", q, desc.ldq, desc.Hq * desc.d),
                                     _addr("k", k, desc.ldk, desc.Hk * desc.d), _ptr(wq), _ptr(wk), _ptr(positions),
@@ -725,8 +740,7 @@ def qk_prep(q, k, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv
     rot_scale; q is multiplied by q_scale.  q and k may be slices of a fused projection's output.  Returns (q, k), dense;
     `out` a pair of tensors to write instead (q, k themselves where dense)."""
     desc = _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale)
-    qo, ko = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                                          torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    qo, ko = out if out is not None else (q.new_empty(q.shape), k.new_empty(k.shape))
     rc = gdr_qk_prep_fwd(desc, q, k, wq, wk, positions, inv_freq, qo, ko, stream)
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_qk_prep_fwd")
@@ -738,7 +752,7 @@ def qk_prep_bwd(q, k, dq_out, dk_out, *, norm="rms", wq=None, wk=None, eps=1e-6,
     """Backward pass of qk_prep, from its inputs and the (dense) gradients of its outputs.
     Returns (dq, dk, dwq, dwk): dense gradients in q's type, weight gradients [d] in fp32 or None."""
     desc = _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale)
-    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
     dwq, dwk = (None if w is None else torch.empty(desc.d, dtype=torch.float32, device=q.device) for w in (wq, wk))
     if dwq is not None or dwk is not None:
         workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device)
@@ -784,7 +798,7 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
     desc = _scan_desc(x, alpha, log_gate, coupled)
     n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
     H, dv, dev = desc.H, desc.dv, x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = x.new_empty(x.shape)
     ST = torch.empty((desc.B if seq_offsets is None else n_seq, H, dv), dtype=torch.float32, device=dev) if want_state else None
     ckpt = (torch.empty((desc.B, (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK, H, dv), dtype=torch.float32, device=dev)
             if want_ckpt else None)
@@ -804,9 +818,8 @@ def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0
     desc = _scan_desc(x, alpha, log_gate, coupled)
     n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
     dev = x.device
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dalpha = torch.empty(x.shape, dtype=alpha.dtype, device=dev)
-    dbeta = None if beta is None else torch.empty(x.shape, dtype=alpha.dtype, device=dev)
+    dx, dalpha = x.new_empty(x.shape), alpha.new_empty(x.shape)
+    dbeta = None if beta is None else alpha.new_empty(x.shape)
     dS0 = torch.empty((desc.B if seq_offsets is None else n_seq, desc.H, desc.dv), dtype=torch.float32, device=dev)
     workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
@@ -821,7 +834,7 @@ def scan_step(S, x, alpha, *, beta=None, log_gate=False, coupled=False, out=None
     """One token of the recurrence for every sequence: x, alpha, beta [B, H, dv]; S [B, H, dv] fp32 is updated in
     place.  Returns y [B, H, dv]."""
     desc = _scan_desc(x, alpha, log_gate, coupled, step=True)
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = out if out is not None else x.new_empty(x.shape)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
     rc = gdr_scan_step(desc, x, ldx, alpha, lda, beta, ldb, S, y, stream)
     if rc != GDR_OK:

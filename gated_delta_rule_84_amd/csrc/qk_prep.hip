@@ -28,65 +28,49 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Vectors of N elements from element-aligned addresses (the hardware takes any dword or
-// wider global access at any byte address).
-template <int BYTES> struct Words;
-template <> struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2))); };
-template <> struct Words<16> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
-
+// N elements of a row as they are stored, from an element-aligned address (the hardware takes
+// a global access of a dword or more at any byte address).
 template <bool BF, int N>
-__device__ __forceinline__ void load_n(const void *base, long at, float (&f)[N]) {
-    if constexpr (BF) {
-        if constexpr (N == 16) {
-            const auto *p = reinterpret_cast<const Words<16>::type *>(static_cast<const uint16_t *>(base) + at);
-            const Words<16>::type a = p[0], b = p[1];
+struct Elems {
+    static constexpr int W = BF ? N / 2 : N;
+    uint32_t w[W];
+
+    template <int K> struct Words { typedef uint32_t type __attribute__((ext_vector_type(K), aligned(2))); };
+    static constexpr int K = W < 4 ? W : 4;  // words per access
+
+    __device__ __forceinline__ void load(const void *base, long at) {
+        const char *p = static_cast<const char *>(base) + at * (BF ? 2 : 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(a[i] << 16);
-                f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-                f[8 + 2 * i] = __uint_as_float(b[i] << 16);
-                f[8 + 2 * i + 1] = __uint_as_float(b[i] & 0xffff0000u);
-            }
+        for (int k = 0; k < W; k += K) {
+            const typename Words<K>::type a = *reinterpret_cast<const typename Words<K>::type *>(p + 4 * k);
+#pragma unroll
+            for (int i = 0; i < K; ++i) w[k + i] = a[i];
+        }
+    }
+    __device__ __forceinline__ void store(void *base, long at) const {
+        char *p = static_cast<char *>(base) + at * (BF ? 2 : 4);
+#pragma unroll
+        for (int k = 0; k < W; k += K) {
+            typename Words<K>::type a;
+#pragma unroll
+            for (int i = 0; i < K; ++i) a[i] = w[k + i];
+            *reinterpret_cast<typename Words<K>::type *>(p + 4 * k) = a;
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (BF) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        return __uint_as_float(w[i]);
+    }
+    // elements i and i + 1 (i even)
+    __device__ __forceinline__ void set2(int i, float a, float b) {
+        if constexpr (BF) {
+            w[i / 2] = pk_bf16(a, b);
         } else {
-            const typename Words<2 * N>::type a =
-                *reinterpret_cast<const typename Words<2 * N>::type *>(static_cast<const uint16_t *>(base) + at);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                f[2 * i] = __uint_as_float(a[i] << 16);
-                f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-            const Words<16>::type a = *reinterpret_cast<const Words<16>::type *>(static_cast<const float *>(base) + at + k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[k + i] = __uint_as_float(a[i]);
+            w[i] = __float_as_uint(a);
+            w[i + 1] = __float_as_uint(b);
         }
     }
-}
-
-template <bool BF, int N>
-__device__ __forceinline__ void store_n(void *base, long at, const float (&f)[N]) {
-    if constexpr (BF) {
-#pragma unroll
-        for (int k = 0; k < N; k += 8) {
-            constexpr int M = N < 8 ? N : 8;
-            typename Words<2 * M>::type a;
-#pragma unroll
-            for (int i = 0; i < M / 2; ++i) a[i] = pk_bf16(f[k + 2 * i], f[k + 2 * i + 1]);
-            *reinterpret_cast<typename Words<2 * M>::type *>(static_cast<uint16_t *>(base) + at + k) = a;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-            Words<16>::type a;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(f[k + i]);
-            *reinterpret_cast<Words<16>::type *>(static_cast<float *>(base) + at + k) = a;
-        }
-    }
-}
+};
 
 // Where a lane's pairs lie in the row.
 //   kAdjacent  members side by side (interleaved rotation, or none): 2 VP elements at 2 i
@@ -95,11 +79,18 @@ __device__ __forceinline__ void store_n(void *base, long at, const float (&f)[N]
 //   kScattered each member at a place of its own (half rotation, any even rot)
 enum Layout { kAdjacent = 0, kSplit = 1, kScattered = 2 };
 
+// A lane's pairs of one row, as stored.
+template <bool BF, int VP, int LAY>
+struct Held {
+    Elems<BF, LAY == kAdjacent ? 2 * VP : VP> a, b;  // kAdjacent uses only a
+    float e[LAY == kScattered ? VP : 1], o[LAY == kScattered ? VP : 1];
+};
+
 template <bool BF, int VP, int LAY>
 struct Row {
     int at[2];      // kAdjacent: [0]; kSplit: both
     int i0, half;   // kScattered
-    __device__ __forceinline__ void place(int pair0, int half_, int) {
+    __device__ __forceinline__ void place(int pair0, int half_) {
         i0 = pair0;
         half = half_;
         if (LAY == kSplit && pair0 < half_) {
@@ -110,55 +101,62 @@ struct Row {
             at[1] = 2 * pair0 + VP;
         }
     }
-    __device__ __forceinline__ int member(int j, int second) const {
-        const int i = i0 + j;
-        return i < half ? i + (second ? half : 0) : 2 * i + second;
-    }
-    __device__ __forceinline__ void load(const void *base, long row, float (&e)[VP], float (&o)[VP]) const {
-        if constexpr (LAY == kAdjacent) {
-            float f[2 * VP];
-            load_n<BF, 2 * VP>(base, row + at[0], f);
-#pragma unroll
-            for (int j = 0; j < VP; ++j) {
-                e[j] = f[2 * j];
-                o[j] = f[2 * j + 1];
-            }
-        } else if constexpr (LAY == kSplit) {
-            load_n<BF, VP>(base, row + at[0], e);
-            load_n<BF, VP>(base, row + at[1], o);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VP; ++j) {
-                e[j] = ld_elem(base, row + member(j, 0), BF);
-                o[j] = ld_elem(base, row + member(j, 1), BF);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(void *base, long row, const float (&e)[VP], const float (&o)[VP]) const {
-        if constexpr (LAY == kAdjacent) {
-            float f[2 * VP];
-#pragma unroll
-            for (int j = 0; j < VP; ++j) {
-                f[2 * j] = e[j];
-                f[2 * j + 1] = o[j];
-            }
-            store_n<BF, 2 * VP>(base, row + at[0], f);
-        } else if constexpr (LAY == kSplit) {
-            store_n<BF, VP>(base, row + at[0], e);
-            store_n<BF, VP>(base, row + at[1], o);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VP; ++j) {
-                st_elem(base, row + member(j, 0), e[j], BF);
-                st_elem(base, row + member(j, 1), o[j], BF);
-            }
-        }
-    }
     // channel of pair j's first / second member
     __device__ __forceinline__ int channel(int j, int second) const {
         if constexpr (LAY == kAdjacent) return at[0] + 2 * j + second;
         if constexpr (LAY == kSplit) return at[second] + j;
-        return member(j, second);
+        const int i = i0 + j;
+        return i < half ? i + (second ? half : 0) : 2 * i + second;
+    }
+    __device__ __forceinline__ void load(const void *base, long row, Held<BF, VP, LAY> &r) const {
+        if constexpr (LAY == kScattered) {
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                r.e[j] = ld_elem(base, row + channel(j, 0), BF);
+                r.o[j] = ld_elem(base, row + channel(j, 1), BF);
+            }
+        } else {
+            r.a.load(base, row + at[0]);
+            if constexpr (LAY == kSplit) r.b.load(base, row + at[1]);
+        }
+    }
+    __device__ __forceinline__ void unpack(const Held<BF, VP, LAY> &r, float (&e)[VP], float (&o)[VP]) const {
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+            if constexpr (LAY == kAdjacent) {
+                e[j] = r.a.get(2 * j);
+                o[j] = r.a.get(2 * j + 1);
+            } else if constexpr (LAY == kSplit) {
+                e[j] = r.a.get(j);
+                o[j] = r.b.get(j);
+            } else {
+                e[j] = r.e[j];
+                o[j] = r.o[j];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *base, long row, const float (&e)[VP], const float (&o)[VP]) const {
+        if constexpr (LAY == kScattered) {
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                st_elem(base, row + channel(j, 0), e[j], BF);
+                st_elem(base, row + channel(j, 1), o[j], BF);
+            }
+        } else {
+            Held<BF, VP, LAY> r;
+#pragma unroll
+            for (int j = 0; j < VP; j += 2) {
+                if constexpr (LAY == kAdjacent) {
+                    r.a.set2(2 * j, e[j], o[j]);
+                    r.a.set2(2 * j + 2, e[j + 1], o[j + 1]);
+                } else {
+                    r.a.set2(j, e[j], e[j + 1]);
+                    r.b.set2(j, o[j], o[j + 1]);
+                }
+            }
+            r.a.store(base, row + at[0]);
+            if constexpr (LAY == kSplit) r.b.store(base, row + at[1]);
+        }
     }
 };
 
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
     const int i0 = lane * VP;
     const bool holds = i0 < p.d / 2;  // lanes past the row only take part in the sums
     Row<BF, VP, LAY> at;
-    at.place(holds ? i0 : 0, p.rot / 2, p.d);
+    at.place(holds ? i0 : 0, p.rot / 2);
     float we[VP], wo[VP], ae[VP], ao[VP];
 #pragma unroll
     for (int j = 0; j < VP; ++j) {
@@ -220,12 +218,21 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
     for (long item = block * groups + gl; item < items; item += nblocks * groups) {
         const long token = item / X.slices;
         const int h0 = (int)(item % X.slices) * p.rows, h1 = min(h0 + p.rows, X.H);
+        // each row is loaded while the one before it is worked on, the first under the angles
+        Held<BF, VP, LAY> next, gnext;
+        auto fetch = [&](int h) __attribute__((always_inline)) {
+            at.load(X.x, token * X.ld + (long)h * p.d, next);
+            if constexpr (BWD) at.load(X.g, (token * X.H + h) * p.d, gnext);
+        };
+        fetch(h0);
         float c[VP], s[VP];
         angles<VP>(p, token, holds ? i0 : p.d, c, s);
         for (int h = h0; h < h1; ++h) {
-            const long in = token * X.ld + (long)h * p.d, out = (token * X.H + h) * p.d;
-            float e[VP], o[VP];
-            at.load(X.x, in, e, o);
+            const long out = (token * X.H + h) * p.d;
+            float e[VP], o[VP], ge[VP], go[VP];
+            at.unpack(next, e, o);
+            if constexpr (BWD) at.unpack(gnext, ge, go);
+            if (h + 1 < h1) fetch(h + 1);
             float ss = 0.f;
 #pragma unroll
             for (int j = 0; j < VP; ++j) ss = fmaf(e[j], e[j], fmaf(o[j], o[j], ss));
@@ -240,8 +247,6 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
                     o[j] = s[j] * ne + c[j] * no;
                 }
             } else {
-                float ge[VP], go[VP];
-                at.load(X.g, out, ge, go);
                 float dot = 0.f;
 #pragma unroll
                 for (int j = 0; j < VP; ++j) {
@@ -291,23 +296,28 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
     }
 }
 
-// The workgroups' sums of the weight gradients, in the order of the workgroups: 16 channels
-// per block, 16 threads per channel.
+// The workgroups' sums of the weight gradients, always in the same order: 16 channels per
+// block, 4 lanes of 4 channels in 64 rows of threads.
 __global__ void __launch_bounds__(256) qk_weight_kernel(QkParams p) {
-    __shared__ float part[16][17];
+    __shared__ f32x4 part[64][4];
     const bool isk = blockIdx.y != 0;
     float *dw = isk ? p.k.dw : p.q.dw;
     if (!dw) return;
-    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4, ch = blockIdx.x * 16 + cl;
-    const long first = isk ? p.blocks_q : 0, n = isk ? p.blocks_k : p.blocks_q;
-    float a = 0.f;
-    if (ch < p.d)
-        for (long b = rl; b < n; b += 16) a += p.partial[(first + b) * p.d + ch];
+    const int cl = threadIdx.x & 3, rl = threadIdx.x >> 2, ch = blockIdx.x * 16 + cl * 4;
+    const int first = isk ? p.blocks_q : 0, n = isk ? p.blocks_k : p.blocks_q;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+    if (ch < p.d) {  // d is a multiple of 8
+#pragma unroll 4
+        for (int b = rl; b < n; b += 64) a += *reinterpret_cast<const f32x4 *>(p.partial + (long)(first + b) * p.d + ch);
+    }
     part[rl][cl] = a;
-    __syncthreads();
+    for (int k = 32; k > 0; k >>= 1) {
+        __syncthreads();
+        if (rl < k) part[rl][cl] += part[rl + k][cl];
+    }
     if (rl == 0 && ch < p.d) {
-        for (int k = 1; k < 16; ++k) a += part[k][cl];
-        dw[ch] = a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[ch + i] = part[0][cl][i];
     }
 }
 
@@ -320,7 +330,7 @@ const void *pick_layout(int lay) {
     }
 }
 
-constexpr int kMaxBlocks = 1024;  // workgroups per tensor of a backward pass
+constexpr int kMaxBlocks = 768;  // workgroups per tensor of a backward pass: about what the chip holds at once
 
 // Lanes, heads per group and workgroups of one call.
 void plan(QkParams &p, bool bwd, int &vp, int &lay) {
@@ -329,8 +339,12 @@ void plan(QkParams &p, bool bwd, int &vp, int &lay) {
     lay = !p.half_layout || half == 0 ? kAdjacent : (half % vp == 0 ? kSplit : kScattered);
     p.lanes = 1;
     while (p.lanes * vp < p.d / 2) p.lanes <<= 1;
-    p.rows = 8;
     const int groups = kThreads / p.lanes;
+    // Up to 8 heads share a token's angles and follow each other in the pipeline of loads; fewer
+    // where that leaves the chip's 1024 SIMDs without 4 waves each and latency is what counts.
+    const long rows = p.tokens * (p.q.H > p.k.H ? p.q.H : p.k.H) * p.lanes / 64;
+    p.rows = 8;
+    while (p.rows > 1 && rows / p.rows < 4096) p.rows >>= 1;
     QkTensor *all[] = {&p.q, &p.k};
     long blocks[2];
     for (int i = 0; i < 2; ++i) {
