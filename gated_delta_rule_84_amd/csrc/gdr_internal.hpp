@@ -118,6 +118,7 @@ hipError_t launch_qk_prep(const QkParams &p, bool bwd, hipStream_t s);
 size_t scan_workspace(const ScanParams &p);
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t s);
+hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s);  // src NULL: zeros
 hipError_t launch_scan_step(const ScanParams &p, hipStream_t s);
 hipError_t launch_decode(const DecodeParams &p, hipStream_t s);
 hipError_t launch_dmem(const DmemParams &p, hipStream_t s);

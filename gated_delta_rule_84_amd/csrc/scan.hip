@@ -1,623 +1,11 @@
-// scan.hip -- gated linear recurrence per channel: forward over long sequences, backward and
-// the single-token step (include/gdr.h: gdr_scan_fwd, gdr_scan_bwd, gdr_scan_step).
-//
-//     h_t = a_t h_{t-1} + b_t x_t,   y_t = h_t        (per channel, state in fp32)
-//
-// A token is the affine map h -> a h + u with u = b x; maps compose associatively,
-// (A2, U2) o (A1, U1) = (A2 A1, A2 U1 + U2), so a block of tokens is reduced in parallel.
-// The backward pass is the same recurrence run from the end.  With G_t the gradient that
-// token t hands to t - 1,
-//     g_t = dy_t + G_{t+1},  G_t = a_t g_t        (G_{T+1} = dS_T, dS_0 = G_1)
-//     dx = b g,  dbeta = g x,  da = g h_{t-1}  (- g x where b = 1 - a)
-// and h_{t-1} is formed again inside each block from the state that the forward pass kept
-// at the block's border, so no state of a token is stored or read.
-//
-// Layout: a workgroup takes a block of 256 tokens x CH channels.  8 lanes hold a row of the
-// block (V channels each: 16-byte loads, 128-byte rows of bf16) and a lane holds 8 tokens
-// one after the other (a strand), all of its inputs in registers between the reduction and
-// the second pass, so every input is read once.
-#include <hip/hip_runtime.h>
-#include <stdint.h>
-
-#include "gdr.h"
-#include "gdr_device.hpp"
-#include "gdr_internal.hpp"
-#include "gdr_mfma.hpp"
+// scan.hip -- gated linear recurrence: the single-token step (see scan_impl.hpp).
+#include "scan_impl.hpp"
 
 namespace gdr {
 namespace {
 
-constexpr int kBlk = GDR_SCAN_BLOCK;  // tokens per block
-constexpr int kLR = 8;                // lanes per row
-constexpr int kWS = 64 / kLR;         // strands per wave
-constexpr int kChainHead = 256;       // bytes before the chain's words: the counter of blocks
-
-// How the input factor b is given.
-enum Factor { kOne = 0, kGiven = 1, kCoupled = 2 };
-
-// Channels per lane, tokens per strand and lanes per workgroup for a pair of types.
-template <bool IOB, bool GB>
-struct Shape {
-    static constexpr int V = IOB && GB ? 8 : 4;
-    static constexpr int L = 32 / V;
-    static constexpr int threads = kBlk / L * kLR;
-    static constexpr int waves = threads / 64;
-    static constexpr int CH = kLR * V;  // channels per workgroup
-};
-
-typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
-typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
-
-// V elements of one token, packed as they are stored.
-template <bool BF, int V>
-struct Pack {
-    static constexpr int N = BF ? V / 2 : V;
-    uint32_t w[N];
-
-    __device__ __forceinline__ float get(int v) const {
-        if constexpr (BF) return (v & 1) ? __uint_as_float(w[v / 2] & 0xffff0000u) : __uint_as_float(w[v / 2] << 16);
-        return __uint_as_float(w[v]);
-    }
-    // members v and v + 1 (v even)
-    __device__ __forceinline__ void set2(int v, float a, float b) {
-        if constexpr (BF) {
-            w[v / 2] = pk_bf16(a, b);
-        } else {
-            w[v] = __float_as_uint(a);
-            w[v + 1] = __float_as_uint(b);
-        }
-    }
-    // `n` of the V elements are inside the row
-    __device__ __forceinline__ void load(const void *base, int64_t at, int n) {
-        if (n == V) {
-            const char *p = static_cast<const char *>(base) + at * (BF ? 2 : 4);
-            if constexpr (N == 2) {
-                const w2 a = *reinterpret_cast<const w2 *>(p);
-                w[0] = a[0];
-                w[1] = a[1];
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; k += 4) {
-                    const w4 a = *reinterpret_cast<const w4 *>(p + 4 * k);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[k + i] = a[i];
-                }
-            }
-        } else {
-            clear();
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (v >= n) continue;
-                if constexpr (BF)
-                    w[v / 2] |= (uint32_t) static_cast<const uint16_t *>(base)[at + v] << (16 * (v & 1));
-                else
-                    w[v] = static_cast<const uint32_t *>(base)[at + v];
-            }
-        }
-    }
-    __device__ __forceinline__ void store(void *base, int64_t at, int n) const {
-        if (n == V) {
-            char *p = static_cast<char *>(base) + at * (BF ? 2 : 4);
-            if constexpr (N == 2) {
-                w2 a;
-                a[0] = w[0];
-                a[1] = w[1];
-                *reinterpret_cast<w2 *>(p) = a;
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; k += 4) {
-                    w4 a;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) a[i] = w[k + i];
-                    *reinterpret_cast<w4 *>(p + 4 * k) = a;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (v >= n) continue;
-                if constexpr (BF)
-                    static_cast<uint16_t *>(base)[at + v] = (uint16_t)(w[v / 2] >> (16 * (v & 1)));
-                else
-                    static_cast<uint32_t *>(base)[at + v] = w[v];
-            }
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = 0;
-    }
-};
-
-// n of V floats
-template <int V>
-__device__ __forceinline__ void load_state(const float *p, int n, float (&f)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = p && v < n ? p[v] : 0.f;
-}
-template <int V>
-__device__ __forceinline__ void store_state(float *p, int n, const float (&f)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (v < n) p[v] = f[v];
-}
-
-// exp(x) and 1 - exp(x), both to about 2 units in the last place.  With n = rint(x / ln 2) and
-// r = x - n ln 2 (ln 2 in two parts), exp(x) = s + s q and exp(x) - 1 = (s - 1) + s q for s = 2^n and
-// q = exp(r) - 1, a polynomial on |r| <= 0.35 whose last term left out is r^8 / 8! < 2^-26 r.
-// For x near 0, where 1 - exp(x) would cancel, s = 1 and the result is q itself.
-__device__ __forceinline__ void exp_both(float x, float &a, float &b) {
-    x = x < -150.f ? -150.f : (x > 150.f ? 150.f : x);  // past the range of fp32 either way; NaN stays
-    const float n = rintf(x * 1.44269504f);
-    float r = fmaf(n, -0.693145752f, x);
-    r = fmaf(n, -1.42860677e-6f, r);
-    float q = fmaf(r, 1.f / 5040, 1.f / 720);
-    q = fmaf(r, q, 1.f / 120);
-    q = fmaf(r, q, 1.f / 24);
-    q = fmaf(r, q, 1.f / 6);
-    q = fmaf(r, q, 0.5f);
-    q = fmaf(r * r, q, r);
-    const int e = (int)n;
-    a = ldexpf(1.f + q, e);
-    const float s = ldexpf(1.f, e);
-    b = x > 1.f ? 1.f - a : -fmaf(s, q, s - 1.f);  // s may be infinite for large x
-}
-
-// Decays and input factors of a lane's channels of one token (b is 1 for kOne).
-template <int F, bool GB, int V>
-__device__ __forceinline__ void gates(bool log, const Pack<GB, V> &al, const Pack<GB, V> &be, float (&a)[V], float (&b)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float g = al.get(v);
-        float c = 1.f - g;
-        a[v] = g;
-        if (log) exp_both(g, a[v], c);
-        b[v] = F == kGiven ? be.get(v) : (F == kCoupled ? c : 1.f);
-    }
-}
-
-// The tokens t0 .. t0 + L - 1 of a strand: bit j of `in` where the token belongs to a sequence,
-// of `first` / `last` where it opens / closes one; seq[j] its sequence.  Offsets are read
-// with sequence numbers clamped to 0 .. nseq, whatever they hold.
-template <bool PACKED, int L>
-struct Marks {
-    unsigned in = 0, first = 0, last = 0;
-    int seq[L];
-
-    __device__ __forceinline__ void find(const ScanParams &p, long t0) {
-        if constexpr (PACKED) {
-            int lo = 0, hi = p.nseq;  // first sequence that ends after t0
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (p.off[mid + 1] <= t0) lo = mid + 1;
-                else hi = mid;
-            }
-            int i = lo;
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                const long t = t0 + j;
-                while (i < p.nseq && p.off[i + 1] <= t) ++i;
-                const bool ok = i < p.nseq && t < p.T && p.off[i] <= t;
-                seq[j] = ok ? i : 0;
-                in |= (unsigned)ok << j;
-                first |= (unsigned)(ok && p.off[i] == t) << j;
-                last |= (unsigned)(ok && p.off[i + 1] == t + 1) << j;
-            }
-        } else {
-            const long n = p.T - t0;
-            in = n >= L ? (1u << L) - 1 : (n > 0 ? (1u << n) - 1 : 0);
-        }
-    }
-};
-
-// ---------------------------------------------------------------------------
-// The chain of blocks.  Every block publishes its composed map as soon as it has it and the
-// state behind it once that is known; a block takes the state that enters it from the nearest
-// block before it whose state is there and applies the maps in between, in the order of the
-// blocks.  That is the arithmetic of a walk from block to block whatever was ready first, so
-// the results do not depend on timing.  Words are stored and loaded whole with relaxed atomics
-// that all eight L2 caches see; a word is there once it is no longer kNone, which no value
-// is stored as, so no order between words matters.  Blocks are numbered by a counter when
-// they begin: every block before a waiting one is running or done, so each wait ends.
-constexpr uint32_t kNone = 0xffffffffu;  // what launch_fill leaves
-constexpr uint32_t kCut = 0xfffffffeu;   // in a map's factor: nothing of what enters gets through
-constexpr int kWindow = 8;               // blocks looked back over at a time
-constexpr int kMaxPolls = 1 << 22;       // some seconds: a bound that a sound run never meets
-
-__device__ __forceinline__ uint32_t word(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return u >= kCut ? 0x7fc00000u : u;  // two NaN patterns are taken
-}
-
-__device__ __forceinline__ float apply(uint32_t A, float U, float h) { return A == kCut ? U : fmaf(__uint_as_float(A), h, U); }
-
-// The chain's words of one sequence and tile of channels: [nblk][CH] maps, [nblk][CH] states.
-template <int CH>
-struct Chain {
-    uint64_t *map;
-    uint32_t *state;
-
-    __device__ __forceinline__ Chain(const ScanParams &p, long column, long columns) {
-        char *ws = static_cast<char *>(p.ws) + kChainHead;
-        map = reinterpret_cast<uint64_t *>(ws) + column * p.nblk * CH;
-        state = reinterpret_cast<uint32_t *>(ws + columns * p.nblk * CH * 8) + column * p.nblk * CH;
-    }
-    __device__ __forceinline__ void put_map(int at, int c, uint32_t A, float U) const {
-        __hip_atomic_store(map + (long)at * CH + c, (uint64_t)A << 32 | __float_as_uint(U), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ void put_state(int at, int c, float h) const {
-        __hip_atomic_store(state + (long)at * CH + c, word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    // The state behind block `at - 1` of channel c (at > 0; block 0 gives its state without a map).
-    __device__ __forceinline__ float enter(int at, int c) const {
-        for (int poll = 0; poll < kMaxPolls; ++poll) {
-            uint32_t h[kWindow];
-            uint64_t m[kWindow];
-#pragma unroll
-            for (int w = 0; w < kWindow; ++w) {
-                const int j = at - 1 - w;
-                h[w] = kNone;
-                m[w] = ~0ull;
-                if (j < 0) continue;
-                h[w] = __hip_atomic_load(state + (long)j * CH + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                m[w] = __hip_atomic_load(map + (long)j * CH + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-            // nearest block whose state is there for every channel, with every map after it
-            int from = -1;
-            bool maps = true;
-#pragma unroll
-            for (int w = 0; w < kWindow; ++w) {
-                if (from >= 0 || !maps) continue;
-                if (__all(h[w] != kNone)) from = w;
-                else maps = __all((uint32_t)(m[w] >> 32) != kNone);
-            }
-            if (from >= 0) {
-                float s = 0.f;
-#pragma unroll
-                for (int w = kWindow - 1; w >= 0; --w) {
-                    if (w == from) s = __uint_as_float(h[w]);
-                    if (w < from) s = apply((uint32_t)(m[w] >> 32), __uint_as_float((uint32_t)m[w]), s);
-                }
-                return s;
-            }
-            __builtin_amdgcn_s_sleep(1);
-        }
-        return __uint_as_float(0x7fc00000u);
-    }
-};
-
-template <int W, int CH>
-struct Shared {
-    float A[W][CH], U[W][CH];  // a wave's composed map, per channel
-    int cut[W];                // it holds a border of sequences
-    float in[W][CH];           // the state that enters a wave's strands
-};
-
-// Composes the strands of a wave: (A, U) is the lane's own map, afterwards that of the
-// wave's strands up to and with its own.  The wave's map goes to shared memory.  REV: the
-// strands are taken from the last to the first.  A strand with a border of sequences (`cut`)
-// lets nothing of what enters it through: a flag and not A = 0, which would turn an infinity
-// of one sequence into a NaN of the next.
-template <int V, bool REV, bool PACKED, class S>
-__device__ __forceinline__ void compose(S &sh, float (&A)[V], float (&U)[V], bool &cut) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
-    const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
-#pragma unroll
-    for (int s = 1; s < kWS; s <<= 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float a = REV ? __shfl_down(A[v], s * kLR) : __shfl_up(A[v], s * kLR);
-            const float u = REV ? __shfl_down(U[v], s * kLR) : __shfl_up(U[v], s * kLR);
-            if (strand >= s && !(PACKED && cut)) {
-                U[v] = fmaf(A[v], u, U[v]);
-                A[v] *= a;
-            }
-        }
-        if (PACKED) {
-            const int c = REV ? __shfl_down((int)cut, s * kLR) : __shfl_up((int)cut, s * kLR);
-            if (strand >= s) cut = cut || c;
-        }
-    }
-    if (strand == kWS - 1) {
-        if (PACKED) sh.cut[wave] = cut;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            sh.A[wave][cl + v] = A[v];
-            sh.U[wave][cl + v] = U[v];
-        }
-    }
-}
-
-// One lane per channel: the composed map of the workgroup's waves, in the order of the strands.
-template <bool REV, bool PACKED, class S>
-__device__ __forceinline__ void block_map(const S &sh, int waves, int c, uint32_t &A, float &U) {
-    float a = 1.f, u = 0.f;
-    bool cut = false;
-    for (int i = 0; i < waves; ++i) {
-        const int w = REV ? waves - 1 - i : i;
-        if (PACKED && sh.cut[w]) {
-            cut = true;
-            u = sh.U[w][c];
-        } else {
-            u = fmaf(sh.A[w][c], u, sh.U[w][c]);
-            a *= sh.A[w][c];
-        }
-    }
-    A = cut ? kCut : word(a);
-    U = u;
-}
-
-// One lane per channel: the state that enters each wave when h enters the block.
-template <bool REV, bool PACKED, class S>
-__device__ __forceinline__ void wave_states(S &sh, int waves, int c, float h) {
-    for (int i = 0; i < waves; ++i) {
-        const int w = REV ? waves - 1 - i : i;
-        sh.in[w][c] = h;
-        h = PACKED && sh.cut[w] ? sh.U[w][c] : fmaf(sh.A[w][c], h, sh.U[w][c]);
-    }
-}
-
-// The state that enters the lane's strand.
-template <int V, bool REV, bool PACKED, class S>
-__device__ __forceinline__ void strand_states(const S &sh, const float (&A)[V], const float (&U)[V], bool cut, float (&h)[V]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
-    const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
-    const int before = PACKED ? (REV ? __shfl_down((int)cut, kLR) : __shfl_up((int)cut, kLR)) : 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float c = sh.in[wave][cl + v];
-        const float a = REV ? __shfl_down(A[v], kLR) : __shfl_up(A[v], kLR);
-        const float u = REV ? __shfl_down(U[v], kLR) : __shfl_up(U[v], kLR);
-        h[v] = strand ? (PACKED && before ? u : fmaf(a, c, u)) : c;
-    }
-}
-
-// This workgroup's place: blocks in the order of the recurrence, all channels of one block
-// before the next (neighbours read neighbouring memory, and a block's predecessors began long
-// before it).
-__device__ __forceinline__ unsigned place(const ScanParams &p, int &ticket) {
-    if (p.nblk == 1) return blockIdx.x;
-    if (threadIdx.x == 0) ticket = (int)(atomicAdd(static_cast<uint32_t *>(p.ws), 1u) + 1u);  // starts at kNone
-    __syncthreads();
-    return (unsigned)ticket;
-}
-
-template <bool IOB, bool GB, int F, bool PACKED>
-__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(ScanParams p) {
-    typedef Shape<IOB, GB> Sh;
-    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH;
-    __shared__ Shared<Sh::waves, CH> sh;
-    __shared__ int ticket;
-    const int waves = blockDim.x >> 6;
-    const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
-    const unsigned column = id % columns, k = id / columns, b = column / tiles, tile = column % tiles;
-    const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
-    const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const long t0 = (long)k * kBlk + strand * L, row = (long)b * p.T + t0;
-    Marks<PACKED, L> m;
-    m.find(p, t0);
-    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
-    Pack<IOB, V> x[L];
-    Pack<GB, V> al[L], be[F == kGiven ? L : 1];
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (m.in >> j & 1) {
-            x[j].load(p.x, (row + j) * p.ldx + ch, n);
-            al[j].load(p.alpha, (row + j) * p.lda + ch, n);
-            if (F == kGiven) be[F == kGiven ? j : 0].load(p.beta, (row + j) * p.ldb + ch, n);
-        }
-    }
-    if (PACKED && p.ST && k == 0) {  // empty sequences end as they begin
-        for (int i = strand; i < p.nseq; i += waves * kWS) {
-            if (p.off[i + 1] > p.off[i]) continue;
-            float c[V];
-            load_state<V>(p.S0 ? p.S0 + (int64_t)i * p.D + ch : nullptr, n, c);
-            store_state<V>(p.ST + (int64_t)i * p.D + ch, n, c);
-        }
-    }
-    float a[L][V], u[L][V], A[V], U[V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = 1.f;
-        U[v] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (!(m.in >> j & 1)) continue;
-        gates<F, GB, V>(p.log_gate, al[j], be[F == kGiven ? j : 0], a[j], u[j]);
-        const bool first = PACKED && (m.first >> j & 1);
-        if (first) load_state<V>(state(p.S0, j), n, U);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            u[j][v] *= x[j].get(v);
-            U[v] = fmaf(a[j][v], U[v], u[j][v]);
-            A[v] = first ? 0.f : A[v] * a[j][v];
-        }
-    }
-    bool cut = m.first != 0;
-    compose<V, false, PACKED>(sh, A, U, cut);
-    __syncthreads();
-    if (threadIdx.x < CH) {
-        const int c = threadIdx.x, cc = tile * CH + c;
-        const Chain<CH> chain(p, column, columns);
-        uint32_t ba;
-        float bu, in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f;
-        block_map<false, PACKED>(sh, waves, c, ba, bu);
-        if (k > 0) {
-            if (k < p.nblk - 1) chain.put_map(k, c, ba, bu);
-            in = chain.enter(k, c);
-        }
-        const float out = apply(ba, bu, in);
-        if (k < p.nblk - 1) chain.put_state(k, c, out);
-        wave_states<false, PACKED>(sh, waves, c, in);
-        if (p.ckpt && cc < p.D) p.ckpt[((int64_t)b * p.nblk + k) * p.D + cc] = out;
-    }
-    __syncthreads();
-    strand_states<V, false, PACKED>(sh, A, U, cut, h);
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (!(m.in >> j & 1)) continue;
-        if (PACKED && (m.first >> j & 1)) load_state<V>(state(p.S0, j), n, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], u[j][v]);
-#pragma unroll
-        for (int v = 0; v < V; v += 2) x[j].set2(v, h[v], h[v + 1]);
-        x[j].store(p.y, (row + j) * p.D + ch, n);
-        if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[j] * p.D + ch, n, h);
-    }
-    if (!PACKED && p.ST && k == p.nblk - 1 && strand == waves * kWS - 1)
-        store_state<V>(p.ST + (int64_t)b * p.D + ch, n, h);
-}
-
-template <bool IOB, bool GB, int F, bool PACKED>
-__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(ScanParams p) {
-    typedef Shape<IOB, GB> Sh;
-    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH;
-    __shared__ Shared<Sh::waves, CH> sh, sg;
-    __shared__ int ticket;
-    const int waves = blockDim.x >> 6;
-    const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
-    const unsigned column = id % columns, step = id / columns, k = p.nblk - 1 - step;  // from the last block to the first
-    const unsigned b = column / tiles, tile = column % tiles;
-    const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
-    const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const long t0 = (long)k * kBlk + strand * L, row = (long)b * p.T + t0;
-    Marks<PACKED, L> m;
-    m.find(p, t0);
-    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
-    Pack<IOB, V> x[L], dy[L];
-    Pack<GB, V> al[L], be[F == kGiven ? L : 1];
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (m.in >> j & 1) {
-            x[j].load(p.x, (row + j) * p.ldx + ch, n);
-            dy[j].load(p.dy, (row + j) * p.D + ch, n);
-            al[j].load(p.alpha, (row + j) * p.lda + ch, n);
-            if (F == kGiven) be[F == kGiven ? j : 0].load(p.beta, (row + j) * p.ldb + ch, n);
-        }
-    }
-    if (PACKED && p.dS0 && k == 0) {
-        for (int i = strand; i < p.nseq; i += waves * kWS) {
-            if (p.off[i + 1] > p.off[i]) continue;
-            float c[V];
-            load_state<V>(p.dST ? p.dST + (int64_t)i * p.D + ch : nullptr, n, c);
-            store_state<V>(p.dS0 + (int64_t)i * p.D + ch, n, c);
-        }
-    }
-    float a[L][V], bb[L][V], A[V], U[V], GA[V], GU[V], h[V], G[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = GA[v] = 1.f;
-        U[v] = GU[v] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (!(m.in >> j & 1)) continue;
-        gates<F, GB, V>(p.log_gate, al[j], be[F == kGiven ? j : 0], a[j], bb[j]);
-        const bool first = PACKED && (m.first >> j & 1);
-        if (first) load_state<V>(state(p.S0, j), n, U);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            U[v] = fmaf(a[j][v], U[v], bb[j][v] * x[j].get(v));
-            A[v] = first ? 0.f : A[v] * a[j][v];
-        }
-    }
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j) {
-        if (!(m.in >> j & 1)) continue;
-        const bool last = PACKED && (m.last >> j & 1);
-        if (last) load_state<V>(state(p.dST, j), n, GU);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            GU[v] = a[j][v] * (dy[j].get(v) + GU[v]);
-            GA[v] = last ? 0.f : GA[v] * a[j][v];
-        }
-    }
-    bool cut = m.first != 0, gcut = m.last != 0;
-    compose<V, false, PACKED>(sh, A, U, cut);
-    compose<V, true, PACKED>(sg, GA, GU, gcut);
-    __syncthreads();
-    {
-        // one wave joins the chain of gradients while another one takes the kept state into the block
-        const int c = threadIdx.x & 63, cc = tile * CH + c, wave = threadIdx.x >> 6;
-        if (wave == 0 && c < CH) {
-            const Chain<CH> chain(p, column, columns);
-            uint32_t ba;
-            float bu, in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f;
-            block_map<true, PACKED>(sg, waves, c, ba, bu);
-            if (step > 0) {
-                if (step < p.nblk - 1) chain.put_map(step, c, ba, bu);
-                in = chain.enter(step, c);
-            }
-            if (step < p.nblk - 1) chain.put_state(step, c, apply(ba, bu, in));
-            wave_states<true, PACKED>(sg, waves, c, in);
-        }
-        if (wave == (waves > 1 ? 1 : 0) && c < CH) {
-            float in = 0.f;
-            if (cc < p.D) {
-                if (k > 0) in = p.ckpt[((int64_t)b * p.nblk + k - 1) * p.D + cc];
-                else if (!PACKED && p.S0) in = p.S0[(int64_t)b * p.D + cc];
-            }
-            wave_states<false, PACKED>(sh, waves, c, in);
-        }
-    }
-    __syncthreads();
-    strand_states<V, false, PACKED>(sh, A, U, cut, h);
-    strand_states<V, true, PACKED>(sg, GA, GU, gcut, G);
-    // two channels at a time: the states before each token, then the gradients from the last token back
-#pragma unroll
-    for (int v = 0; v < V; v += 2) {
-        float before[2][L];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float s = h[v + e];
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                if (!(m.in >> j & 1)) continue;
-                if (PACKED && (m.first >> j & 1)) s = p.S0 && v + e < n ? state(p.S0, j)[v + e] : 0.f;
-                before[e][j] = s;
-                s = fmaf(a[j][v + e], s, bb[j][v + e] * x[j].get(v + e));
-            }
-        }
-#pragma unroll
-        for (int j = L - 1; j >= 0; --j) {
-            if (!(m.in >> j & 1)) continue;
-            float dx[2], da[2], db[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (PACKED && (m.last >> j & 1)) G[v + e] = p.dST && v + e < n ? state(p.dST, j)[v + e] : 0.f;
-                const float g = dy[j].get(v + e) + G[v + e], xv = x[j].get(v + e);
-                dx[e] = bb[j][v + e] * g;
-                db[e] = g * xv;
-                da[e] = g * (F == kCoupled ? before[e][j] - xv : before[e][j]);
-                G[v + e] = a[j][v + e] * g;
-                if (p.log_gate) da[e] *= a[j][v + e];
-                if (PACKED && p.dS0 && (m.first >> j & 1) && v + e < n)
-                    p.dS0[(int64_t)m.seq[j] * p.D + ch + v + e] = G[v + e];
-            }
-            dy[j].set2(v, dx[0], dx[1]);
-            al[j].set2(v, da[0], da[1]);
-            if (F == kGiven) be[F == kGiven ? j : 0].set2(v, db[0], db[1]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (!(m.in >> j & 1)) continue;
-        dy[j].store(p.dx, (row + j) * p.D + ch, n);
-        al[j].store(p.dalpha, (row + j) * p.D + ch, n);
-        if (F == kGiven) be[F == kGiven ? j : 0].store(p.dbeta, (row + j) * p.D + ch, n);
-    }
-    if (!PACKED && strand == 0 && k == 0 && p.dS0) store_state<V>(p.dS0 + (int64_t)b * p.D + ch, n, G);
-}
-
-// Every word of the chain to kNone (a kernel, so that a captured graph replays it).
-__global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
-    const long i = (long)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) ws[i] = (u32x4){kNone, kNone, kNone, kNone};
-}
-
 // One token for every batch row: the state is read and written in place.
-template <bool IOB, bool GB, int F>
+template <bool IOB, bool GB, int F, bool LOG>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
     constexpr int V = Shape<IOB, GB>::V;
     const unsigned groups = (p.D + V - 1) / V;
@@ -628,17 +16,29 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
     Pack<GB, V> al, be;
     float *S = p.ST + b * p.D + ch;
     float a[V], u[V], h[V];
-    x.load(p.x, b * p.ldx + ch, n);
-    al.load(p.alpha, b * p.lda + ch, n);
-    if (F == kGiven) be.load(p.beta, b * p.ldb + ch, n);
+    const char *px = static_cast<const char *>(p.x) + (b * p.ldx + ch) * (IOB ? 2 : 4);
+    const char *pa = static_cast<const char *>(p.alpha) + (b * p.lda + ch) * (GB ? 2 : 4);
+    const char *pb = static_cast<const char *>(p.beta) + (b * p.ldb + ch) * (GB ? 2 : 4);
+    char *py = static_cast<char *>(p.y) + (b * p.D + ch) * (IOB ? 2 : 4);
+    const bool whole = n == V;
+    if (whole) {
+        x.load(px);
+        al.load(pa);
+        if (F == kGiven) be.load(pb);
+    } else {
+        x.load(px, n);
+        al.load(pa, n);
+        if (F == kGiven) be.load(pb, n);
+    }
     load_state<V>(S, n, h);
-    gates<F, GB, V>(p.log_gate, al, be, a, u);
+    gates<F, LOG, GB, V>(al, be, a, u);
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], h[v], u[v] * x.get(v));
 #pragma unroll
     for (int v = 0; v < V; v += 2) x.set2(v, h[v], h[v + 1]);
     store_state<V>(S, n, h);
-    x.store(p.y, b * p.D + ch, n);
+    if (whole) x.store(py);
+    else x.store(py, n);
 }
 
 // ST = S0 (or 0) of a call without tokens
@@ -647,88 +47,24 @@ __global__ void __launch_bounds__(256) scan_copy_kernel(const float *src, float 
     if (i < n) dst[i] = src ? src[i] : 0.f;
 }
 
-enum Kind { kFwd, kBwd, kStep };
-
-template <Kind K, bool IOB, bool GB, int F, bool PACKED>
-const void *kernel() {
-    if constexpr (K == kFwd) return reinterpret_cast<const void *>(&scan_fwd_kernel<IOB, GB, F, PACKED>);
-    if constexpr (K == kBwd) return reinterpret_cast<const void *>(&scan_bwd_kernel<IOB, GB, F, PACKED>);
-    return reinterpret_cast<const void *>(&scan_step_kernel<IOB, GB, F>);
-}
-
-// The kernel of a call, with its Shape's numbers.
-struct Pick {
-    const void *fn;
-    int V, L, CH;
+struct Step {
+    template <bool IOB, bool GB, int F, bool LOG, bool>
+    static const void *get() { return reinterpret_cast<const void *>(&scan_step_kernel<IOB, GB, F, LOG>); }
 };
 
-template <Kind K, bool IOB, bool GB, int F>
-Pick pick_packed(const ScanParams &p) {
-    typedef Shape<IOB, GB> Sh;
-    return {p.off ? kernel<K, IOB, GB, F, true>() : kernel<K, IOB, GB, F, false>(), Sh::V, Sh::L, Sh::CH};
-}
+}  // namespace
 
-template <Kind K, bool IOB, bool GB>
-Pick pick_factor(const ScanParams &p) {
-    if (p.beta) return pick_packed<K, IOB, GB, kGiven>(p);
-    return p.coupled ? pick_packed<K, IOB, GB, kCoupled>(p) : pick_packed<K, IOB, GB, kOne>(p);
-}
+size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p); }
 
-template <Kind K>
-Pick pick(const ScanParams &p) {
-    if (p.io_bf16) return p.gate_bf16 ? pick_factor<K, true, true>(p) : pick_factor<K, true, false>(p);
-    return p.gate_bf16 ? pick_factor<K, false, true>(p) : pick_factor<K, false, false>(p);
-}
-
-hipError_t copy_states(const float *src, float *dst, long n, hipStream_t s) {
+hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s) {
     if (!dst || n == 0 || src == dst) return hipSuccess;
     void *args[] = {&src, &dst, &n};
     return hipLaunchKernel(reinterpret_cast<const void *>(&scan_copy_kernel), dim3((unsigned)((n + 255) / 256)), dim3(256),
                            args, 0, s);
 }
 
-// Bytes of the chain's words: a map and a state per block, sequence and channel of whole tiles.
-long chain_bytes(const ScanParams &p, int ch) {
-    if (p.nblk <= 1) return 0;
-    const long columns = (long)p.B * ((p.D + ch - 1) / ch);
-    return kChainHead + (columns * p.nblk * ch * 12 + 15) / 16 * 16;
-}
-
-template <Kind K>
-hipError_t launch(const ScanParams &p, hipStream_t s) {
-    const Pick k = pick<K>(p);
-    const int strands = ((p.T < kBlk ? p.T : kBlk) + k.L - 1) / k.L, waves = (strands + kWS - 1) / kWS;
-    const long blocks = (long)p.B * ((p.D + k.CH - 1) / k.CH) * p.nblk;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    if (p.nblk > 1) {
-        u32x4 *ws = static_cast<u32x4 *>(p.ws);
-        long n = chain_bytes(p, k.CH) / 16;
-        void *args[] = {&ws, &n};
-        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&scan_fill_kernel), dim3((unsigned)((n + 255) / 256)),
-                                             dim3(256), args, 0, s);
-        if (e != hipSuccess) return e;
-    }
-    ScanParams q = p;
-    void *args[] = {&q};
-    return hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(64 * waves), args, 0, s);
-}
-
-}  // namespace
-
-size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p, pick<kFwd>(p).CH); }
-
-hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s) {
-    if (p.T == 0) return copy_states(p.S0, p.ST, (long)(p.off ? p.nseq : p.B) * p.D, s);
-    return launch<kFwd>(p, s);
-}
-
-hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t s) {
-    if (p.T == 0) return copy_states(p.dST, p.dS0, (long)(p.off ? p.nseq : p.B) * p.D, s);
-    return launch<kBwd>(p, s);
-}
-
 hipError_t launch_scan_step(const ScanParams &p, hipStream_t s) {
-    const Pick k = pick<kStep>(p);
+    const Pick k = pick<Step>(p);
     const long threads = (long)p.B * ((p.D + k.V - 1) / k.V);
     if ((threads + 255) / 256 > 0x7fffffffL) return hipErrorInvalidValue;
     ScanParams q = p;

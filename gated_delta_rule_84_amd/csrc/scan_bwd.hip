@@ -1,0 +1,155 @@
+// scan_bwd.hip -- gated linear recurrence: the backward pass (see scan_impl.hpp).
+#include "scan_impl.hpp"
+
+namespace gdr {
+namespace {
+
+template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
+__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(ScanParams p) {
+    typedef Shape<IOB, GB> Sh;
+    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH, LB = F == kGiven ? L : 1;
+    __shared__ Shared<Sh::waves, CH> sh, sg;
+    __shared__ int ticket;
+    const int waves = blockDim.x >> 6;
+    const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
+    const unsigned column = id % columns, step = id / columns, k = p.nblk - 1 - step;  // from the last block to the first
+    const unsigned b = column / tiles, tile = column % tiles;
+    const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
+    const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
+    const bool whole = (tile + 1) * CH <= (unsigned)p.D;
+    const int t0 = k * kBlk + strand * L, tb = min(t0, p.T - 1), last = p.T - 1 - tb;
+    const int64_t row = (int64_t)b * p.T + tb;
+    Pack<IOB, V> x[L], dy[L];
+    Pack<GB, V> al[L], be[LB];
+    Rows<IOB, V, L>(p.x, row, p.ldx, ch).load(x, last, whole, n);
+    Rows<GB, V, L>(p.alpha, row, p.lda, ch).load(al, last, whole, n);
+    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, p.ldb, ch).load(be, last, whole, n);
+    Rows<IOB, V, L>(p.dy, row, p.D, ch).load(dy, last, whole, n);
+    Marks<PACKED, L> m;
+    m.find(p, t0);
+    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
+    if (PACKED && p.dS0 && k == 0) {
+        for (int i = strand; i < p.nseq; i += waves * kWS) {
+            if (p.off[i + 1] > p.off[i]) continue;
+            float c[V];
+            load_state<V>(p.dST ? p.dST + (int64_t)i * p.D + ch : nullptr, n, c);
+            store_state<V>(p.dS0 + (int64_t)i * p.D + ch, n, c);
+        }
+    }
+    if (PACKED || (k + 1) * kBlk > (unsigned)p.T) {
+        leave_out<LOG>(m.in, x, al, be);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (!(m.in >> j & 1)) dy[j].clear();
+    }
+    float a[L][V], bb[L][V], A[V], U[V], GA[V], GU[V], h[V], G[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        A[v] = GA[v] = 1.f;
+        U[v] = GU[v] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        gates<F, LOG, GB, V>(al[j], be[j % LB], a[j], bb[j]);
+        const bool first = PACKED && (m.first >> j & 1);
+        if (first) load_state<V>(state(p.S0, j), n, U);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            U[v] = fmaf(a[j][v], U[v], bb[j][v] * x[j].get(v));
+            A[v] = first ? 0.f : A[v] * a[j][v];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = L - 1; j >= 0; --j) {
+        const bool end = PACKED && (m.last >> j & 1);
+        if (end) load_state<V>(state(p.dST, j), n, GU);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            GU[v] = a[j][v] * (dy[j].get(v) + GU[v]);
+            GA[v] = end ? 0.f : GA[v] * a[j][v];
+        }
+    }
+    bool cut = m.first != 0, gcut = m.last != 0;
+    compose<V, false, PACKED>(sh, A, U, cut);
+    compose<V, true, PACKED>(sg, GA, GU, gcut);
+    __syncthreads();
+    {
+        // one wave joins the chain of gradients while another one takes the kept state into the block
+        const int c = threadIdx.x & 63, cc = tile * CH + c, wave = threadIdx.x >> 6;
+        if (wave == 0 && c < CH) {
+            const Chain<CH> chain(p, column, columns);
+            uint32_t ba;
+            float bu, in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f;
+            block_map<true, PACKED>(sg, waves, c, ba, bu);
+            if (step > 0) {
+                if (step < p.nblk - 1) chain.put_map(step, c, ba, bu);
+                in = chain.enter(step, c);
+            }
+            if (step < p.nblk - 1) chain.put_state(step, c, apply(ba, bu, in));
+            wave_states<true, PACKED>(sg, waves, c, in);
+        }
+        if (wave == (waves > 1 ? 1 : 0) && c < CH) {
+            float in = 0.f;
+            if (cc < p.D) {
+                if (k > 0) in = p.ckpt[((int64_t)b * p.nblk + k - 1) * p.D + cc];
+                else if (!PACKED && p.S0) in = p.S0[(int64_t)b * p.D + cc];
+            }
+            wave_states<false, PACKED>(sh, waves, c, in);
+        }
+    }
+    __syncthreads();
+    strand_states<V, false, PACKED>(sh, A, U, cut, h);
+    strand_states<V, true, PACKED>(sg, GA, GU, gcut, G);
+    // two channels at a time: the states before each token, then the gradients from the last token back
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+        float before[2][L];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float s = h[v + e];
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                if (PACKED && (m.first >> j & 1)) s = p.S0 && v + e < n ? state(p.S0, j)[v + e] : 0.f;
+                before[e][j] = s;
+                s = fmaf(a[j][v + e], s, bb[j][v + e] * x[j].get(v + e));
+            }
+        }
+#pragma unroll
+        for (int j = L - 1; j >= 0; --j) {
+            float dx[2], da[2], db[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (PACKED && (m.last >> j & 1)) G[v + e] = p.dST && v + e < n ? state(p.dST, j)[v + e] : 0.f;
+                const float g = dy[j].get(v + e) + G[v + e], xv = x[j].get(v + e);
+                dx[e] = bb[j][v + e] * g;
+                db[e] = g * xv;
+                G[v + e] = a[j][v + e] * g;
+                da[e] = (LOG ? G[v + e] : g) * (F == kCoupled ? before[e][j] - xv : before[e][j]);
+                if (PACKED && p.dS0 && (m.first >> j & 1) && v + e < n)
+                    p.dS0[(int64_t)m.seq[j] * p.D + ch + v + e] = G[v + e];
+            }
+            dy[j].set2(v, dx[0], dx[1]);
+            al[j].set2(v, da[0], da[1]);
+            if (F == kGiven) be[j % LB].set2(v, db[0], db[1]);
+        }
+    }
+    Rows<IOB, V, L>(p.dx, row, p.D, ch).store(dy, m.in, whole, n);
+    Rows<GB, V, L>(p.dalpha, row, p.D, ch).store(al, m.in, whole, n);
+    if constexpr (F == kGiven) Rows<GB, V, LB>(p.dbeta, row, p.D, ch).store(be, m.in, whole, n);
+    if (!PACKED && strand == 0 && k == 0 && p.dS0) store_state<V>(p.dS0 + (int64_t)b * p.D + ch, n, G);
+}
+
+struct Bwd {
+    template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
+    static const void *get() { return reinterpret_cast<const void *>(&scan_bwd_kernel<IOB, GB, F, LOG, PACKED>); }
+};
+
+}  // namespace
+
+hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t s) {
+    if (p.T == 0) return launch_scan_copy(p.dST, p.dS0, (long)(p.off ? p.nseq : p.B) * p.D, s);
+    return launch_blocks<Bwd>(p, s);
+}
+
+}  // namespace gdr

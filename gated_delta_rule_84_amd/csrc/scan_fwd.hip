@@ -1,0 +1,104 @@
+// scan_fwd.hip -- gated linear recurrence: the forward pass (see scan_impl.hpp).
+#include "scan_impl.hpp"
+
+namespace gdr {
+namespace {
+
+template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
+__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(ScanParams p) {
+    typedef Shape<IOB, GB> Sh;
+    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH, LB = F == kGiven ? L : 1;
+    __shared__ Shared<Sh::waves, CH> sh;
+    __shared__ int ticket;
+    const int waves = blockDim.x >> 6;
+    const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
+    const unsigned column = id % columns, k = id / columns, b = column / tiles, tile = column % tiles;
+    const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
+    const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
+    const bool whole = (tile + 1) * CH <= (unsigned)p.D;  // every lane's channels are there
+    const int t0 = k * kBlk + strand * L, tb = min(t0, p.T - 1), last = p.T - 1 - tb;
+    const int64_t row = (int64_t)b * p.T + tb;
+    Pack<IOB, V> x[L];
+    Pack<GB, V> al[L], be[LB];
+    Rows<IOB, V, L>(p.x, row, p.ldx, ch).load(x, last, whole, n);
+    Rows<GB, V, L>(p.alpha, row, p.lda, ch).load(al, last, whole, n);
+    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, p.ldb, ch).load(be, last, whole, n);
+    Marks<PACKED, L> m;
+    m.find(p, t0);
+    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
+    if (PACKED && p.ST && k == 0) {  // empty sequences end as they begin
+        for (int i = strand; i < p.nseq; i += waves * kWS) {
+            if (p.off[i + 1] > p.off[i]) continue;
+            float c[V];
+            load_state<V>(p.S0 ? p.S0 + (int64_t)i * p.D + ch : nullptr, n, c);
+            store_state<V>(p.ST + (int64_t)i * p.D + ch, n, c);
+        }
+    }
+    if (PACKED || (k + 1) * kBlk > (unsigned)p.T) leave_out<LOG>(m.in, x, al, be);
+    float a[L][V], u[L][V], A[V], U[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        A[v] = 1.f;
+        U[v] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        gates<F, LOG, GB, V>(al[j], be[j % LB], a[j], u[j]);
+        const bool first = PACKED && (m.first >> j & 1);
+        if (first) load_state<V>(state(p.S0, j), n, U);
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[j][v] *= x[j].get(v);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            U[v] = fmaf(a[j][v], U[v], u[j][v]);
+            A[v] = first ? 0.f : A[v] * a[j][v];
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a token at a time, or the exponentials of all are in flight at once
+    }
+    bool cut = m.first != 0;
+    compose<V, false, PACKED>(sh, A, U, cut);
+    __syncthreads();
+    if (threadIdx.x < CH) {
+        const int c = threadIdx.x, cc = tile * CH + c;
+        const Chain<CH> chain(p, column, columns);
+        uint32_t ba;
+        float bu, in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f;
+        block_map<false, PACKED>(sh, waves, c, ba, bu);
+        if (k > 0) {
+            if (k < p.nblk - 1) chain.put_map(k, c, ba, bu);
+            in = chain.enter(k, c);
+        }
+        const float out = apply(ba, bu, in);
+        if (k < p.nblk - 1) chain.put_state(k, c, out);
+        wave_states<false, PACKED>(sh, waves, c, in);
+        if (p.ckpt && cc < p.D) p.ckpt[((int64_t)b * p.nblk + k) * p.D + cc] = out;
+    }
+    __syncthreads();
+    strand_states<V, false, PACKED>(sh, A, U, cut, h);
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        if (PACKED && (m.first >> j & 1)) load_state<V>(state(p.S0, j), n, h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], u[j][v]);
+#pragma unroll
+        for (int v = 0; v < V; v += 2) x[j].set2(v, h[v], h[v + 1]);
+        if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[j] * p.D + ch, n, h);
+    }
+    Rows<IOB, V, L>(p.y, row, p.D, ch).store(x, m.in, whole, n);
+    if (!PACKED && p.ST && k == p.nblk - 1 && strand == waves * kWS - 1)
+        store_state<V>(p.ST + (int64_t)b * p.D + ch, n, h);
+}
+
+struct Fwd {
+    template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
+    static const void *get() { return reinterpret_cast<const void *>(&scan_fwd_kernel<IOB, GB, F, LOG, PACKED>); }
+};
+
+}  // namespace
+
+hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s) {
+    if (p.T == 0) return launch_scan_copy(p.S0, p.ST, (long)(p.off ? p.nseq : p.B) * p.D, s);
+    return launch_blocks<Fwd>(p, s);
+}
+
+}  // namespace gdr

@@ -1,0 +1,515 @@
+// scan_impl.hpp -- gated linear recurrence per channel (include/gdr.h: gdr_scan_fwd, gdr_scan_bwd,
+// gdr_scan_step): the mathematics and what its kernels share.  scan_fwd.hip and scan_bwd.hip hold the
+// passes over long sequences, scan.hip the single-token step.
+//
+//     h_t = a_t h_{t-1} + b_t x_t,   y_t = h_t        (per channel, state in fp32)
+//
+// A token is the affine map h -> a h + u with u = b x; maps compose associatively,
+// (A2, U2) o (A1, U1) = (A2 A1, A2 U1 + U2), so a block of tokens is reduced in parallel.
+// The backward pass is the same recurrence run from the end.  With G_t the gradient that
+// token t hands to t - 1,
+//     g_t = dy_t + G_{t+1},  G_t = a_t g_t        (G_{T+1} = dS_T, dS_0 = G_1)
+//     dx = b g,  dbeta = g x,  da = g h_{t-1}  (- g x where b = 1 - a)
+// and h_{t-1} is formed again inside each block from the state that the forward pass kept
+// at the block's border, so no state of a token is stored or read.
+//
+// Layout: a workgroup takes a block of 256 tokens x CH channels.  8 lanes hold a row of the
+// block (V channels each: 16-byte loads, 128-byte rows of bf16) and a lane holds 8 tokens
+// one after the other (a strand), all of its inputs in registers between the reduction and
+// the second pass, so every input is read once.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr.h"
+#include "gdr_device.hpp"
+#include "gdr_internal.hpp"
+#include "gdr_mfma.hpp"
+
+namespace gdr {
+namespace {
+
+constexpr int kBlk = GDR_SCAN_BLOCK;  // tokens per block
+constexpr int kLR = 8;                // lanes per row
+constexpr int kWS = 64 / kLR;         // strands per wave
+constexpr int kChainHead = 256;       // bytes before the chain's words: the counter of blocks
+
+// How the input factor b is given.
+enum Factor { kOne = 0, kGiven = 1, kCoupled = 2 };
+
+// Channels per lane, tokens per strand and lanes per workgroup for a pair of types.
+template <bool IOB, bool GB>
+struct Shape {
+    static constexpr int V = IOB && GB ? 8 : 4;
+    static constexpr int L = 32 / V;
+    static constexpr int threads = kBlk / L * kLR;
+    static constexpr int waves = threads / 64;
+    static constexpr int CH = kLR * V;  // channels per workgroup
+};
+
+typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
+
+// V elements of one token, packed as they are stored.
+template <bool BF, int V>
+struct Pack {
+    static constexpr int N = BF ? V / 2 : V;
+    uint32_t w[N];
+
+    __device__ __forceinline__ float get(int v) const {
+        if constexpr (BF) return (v & 1) ? __uint_as_float(w[v / 2] & 0xffff0000u) : __uint_as_float(w[v / 2] << 16);
+        return __uint_as_float(w[v]);
+    }
+    // members v and v + 1 (v even)
+    __device__ __forceinline__ void set2(int v, float a, float b) {
+        if constexpr (BF) {
+            w[v / 2] = pk_bf16(a, b);
+        } else {
+            w[v] = __float_as_uint(a);
+            w[v + 1] = __float_as_uint(b);
+        }
+    }
+    __device__ __forceinline__ void load(const char *p) {
+        if constexpr (N == 2) {
+            const w2 a = *reinterpret_cast<const w2 *>(p);
+            w[0] = a[0];
+            w[1] = a[1];
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+                const w4 a = *reinterpret_cast<const w4 *>(p + 4 * k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[k + i] = a[i];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char *p) const {
+        if constexpr (N == 2) {
+            w2 a;
+            a[0] = w[0];
+            a[1] = w[1];
+            *reinterpret_cast<w2 *>(p) = a;
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+                w4 a;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = w[k + i];
+                *reinterpret_cast<w4 *>(p + 4 * k) = a;
+            }
+        }
+    }
+    // the first n of the V elements alone
+    __device__ __forceinline__ void load(const char *p, int n) {
+        clear();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (v >= n) continue;
+            if constexpr (BF)
+                w[v / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[v] << (16 * (v & 1));
+            else
+                w[v] = reinterpret_cast<const uint32_t *>(p)[v];
+        }
+    }
+    __device__ __forceinline__ void store(char *p, int n) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (v >= n) continue;
+            if constexpr (BF)
+                reinterpret_cast<uint16_t *>(p)[v] = (uint16_t)(w[v / 2] >> (16 * (v & 1)));
+            else
+                reinterpret_cast<uint32_t *>(p)[v] = w[v];
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = 0;
+    }
+    __device__ __forceinline__ void ones() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = BF ? 0x3f803f80u : 0x3f800000u;
+    }
+};
+
+// n of V floats; a NULL address holds zeros
+template <int V>
+__device__ __forceinline__ void load_state(const float *p, int n, float (&f)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = 0.f;
+    if (!p) return;
+    if (n == V) {
+        Pack<false, V> w;
+        w.load(reinterpret_cast<const char *>(p));
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = w.get(v);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < n) f[v] = p[v];
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_state(float *p, int n, const float (&f)[V]) {
+    if (n == V) {
+        Pack<false, V> w;
+#pragma unroll
+        for (int v = 0; v < V; v += 2) w.set2(v, f[v], f[v + 1]);
+        w.store(reinterpret_cast<char *>(p));
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < n) p[v] = f[v];
+    }
+}
+
+// exp(x) and 1 - exp(x), both to about 2 units in the last place, for x in -88 .. 88 (below, 0 and 1;
+// above, as at 88).  With n = rint(x / ln 2) and r = x - n ln 2 (ln 2 in two parts), exp(x) = s + s q
+// and exp(x) - 1 = (s - 1) + s q for s = 2^n and q = exp(r) - 1, a polynomial on |r| <= 0.35 whose
+// first term left out is r^8 / 8! < 2^-26 r.  For x near 0, where 1 - exp(x) would cancel, s = 1 and
+// the result is q itself.  n = -127, the least, makes the bit pattern of s that of 0.
+__device__ __forceinline__ void exp_both(float x, float &a, float &b) {
+    const float y = __builtin_amdgcn_fmed3f(x, -88.f, 88.f);
+    const float n = rintf(y * 1.44269504f);
+    float r = fmaf(n, -0.693145752f, y);
+    r = fmaf(n, -1.42860677e-6f, r);
+    float q = fmaf(r, 1.f / 5040, 1.f / 720);
+    q = fmaf(r, q, 1.f / 120);
+    q = fmaf(r, q, 1.f / 24);
+    q = fmaf(r, q, 1.f / 6);
+    q = fmaf(r, q, 0.5f);
+    q = fmaf(r * r, q, r);
+    const float s = __uint_as_float(((uint32_t)(int)n << 23) + 0x3f800000u);
+    a = x == x ? fmaf(s, q, s) : x;
+    b = x == x ? fmaf(-s, q, 1.f - s) : x;
+}
+
+// Decays and input factors of a lane's channels of one token (b is 1 for kOne).
+template <int F, bool LOG, bool GB, int V>
+__device__ __forceinline__ void gates(const Pack<GB, V> &al, const Pack<GB, V> &be, float (&a)[V], float (&b)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        a[v] = al.get(v);
+        b[v] = 1.f - a[v];
+        if (LOG) exp_both(al.get(v), a[v], b[v]);
+        b[v] = F == kGiven ? be.get(v) : (F == kCoupled ? b[v] : 1.f);
+    }
+}
+
+// Tokens of a strand that are in no sequence become ones that change nothing: a = 1, b x = 0.
+template <bool LOG, class X, class G, int L, int LB>
+__device__ __forceinline__ void leave_out(unsigned in, X (&x)[L], G (&al)[L], G (&be)[LB]) {
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        if (in >> j & 1) continue;
+        x[j].clear();
+        be[j % LB].clear();
+        if (LOG) al[j].clear();
+        else al[j].ones();
+    }
+}
+
+// The rows of a lane's strand in one tensor: `ld` elements between tokens, `last` the last token
+// that the memory holds after the strand's first.  Rows past it are read at it (and left out later).
+template <bool BF, int V, int L>
+struct Rows {
+    const char *p;
+    int64_t step;
+    __device__ __forceinline__ Rows(const void *base, int64_t row, int64_t ld, int ch)
+        : p(static_cast<const char *>(base) + (row * ld + ch) * (BF ? 2 : 4)), step(ld * (BF ? 2 : 4)) {}
+    __device__ __forceinline__ void load(Pack<BF, V> (&x)[L], int last, bool whole, int n) const {
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) x[j].load(p + min(j, last) * step);
+        } else {
+#pragma unroll
+            for (int j = 0; j < L; ++j) x[j].load(p + min(j, last) * step, n);
+        }
+    }
+    __device__ __forceinline__ void store(const Pack<BF, V> (&x)[L], unsigned in, bool whole, int n) const {
+        char *q = const_cast<char *>(p);
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                if (in >> j & 1) x[j].store(q + j * step);
+        } else {
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                if (in >> j & 1) x[j].store(q + j * step, n);
+        }
+    }
+};
+
+// The tokens t0 .. t0 + L - 1 of a strand: bit j of `in` where the token belongs to a sequence,
+// of `first` / `last` where it opens / closes one; seq[j] its sequence.  Offsets are read
+// with sequence numbers clamped to 0 .. nseq, whatever they hold.
+template <bool PACKED, int L>
+struct Marks {
+    unsigned in = 0, first = 0, last = 0;
+    int seq[L];
+
+    __device__ __forceinline__ void find(const ScanParams &p, int t0) {
+        if constexpr (PACKED) {
+            int lo = 0, hi = p.nseq;  // first sequence that ends after t0
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (p.off[mid + 1] <= t0) lo = mid + 1;
+                else hi = mid;
+            }
+            int i = lo;
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const int t = t0 + j;
+                while (i < p.nseq && p.off[i + 1] <= t) ++i;
+                const bool ok = i < p.nseq && t < p.T && p.off[i] <= t;
+                seq[j] = ok ? i : 0;
+                in |= (unsigned)ok << j;
+                first |= (unsigned)(ok && p.off[i] == t) << j;
+                last |= (unsigned)(ok && p.off[i + 1] == t + 1) << j;
+            }
+        } else {
+            const int n = p.T - t0;
+            in = n >= L ? (1u << L) - 1 : (n > 0 ? (1u << n) - 1 : 0);
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The chain of blocks.  Every block publishes its composed map as soon as it has it and the
+// state behind it once that is known; a block takes the state that enters it from the nearest
+// block before it whose state is there and applies the maps in between, in the order of the
+// blocks.  That is the arithmetic of a walk from block to block whatever was ready first, so
+// the results do not depend on timing.  Words are stored and loaded whole with relaxed atomics
+// that all eight L2 caches see; a word is there once it is no longer kNone, which no value
+// is stored as, so no order between words matters.  Blocks are numbered by a counter when
+// they begin: every block before a waiting one is running or done, so each wait ends.
+constexpr uint32_t kNone = 0xffffffffu;  // what launch_fill leaves
+constexpr uint32_t kCut = 0xfffffffeu;   // in a map's factor: nothing of what enters gets through
+constexpr int kWindow = 8;               // blocks looked back over at a time
+constexpr int kMaxPolls = 1 << 22;       // some seconds: a bound that a sound run never meets
+
+__device__ __forceinline__ uint32_t word(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u >= kCut ? 0x7fc00000u : u;  // two NaN patterns are taken
+}
+
+__device__ __forceinline__ float apply(uint32_t A, float U, float h) { return A == kCut ? U : fmaf(__uint_as_float(A), h, U); }
+
+// The chain's words of one sequence and tile of channels: [nblk][CH] maps, [nblk][CH] states.
+template <int CH>
+struct Chain {
+    uint64_t *map;
+    uint32_t *state;
+
+    __device__ __forceinline__ Chain(const ScanParams &p, long column, long columns) {
+        char *ws = static_cast<char *>(p.ws) + kChainHead;
+        map = reinterpret_cast<uint64_t *>(ws) + column * p.nblk * CH;
+        state = reinterpret_cast<uint32_t *>(ws + columns * p.nblk * CH * 8) + column * p.nblk * CH;
+    }
+    __device__ __forceinline__ void put_map(int at, int c, uint32_t A, float U) const {
+        __hip_atomic_store(map + (long)at * CH + c, (uint64_t)A << 32 | __float_as_uint(U), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ void put_state(int at, int c, float h) const {
+        __hip_atomic_store(state + (long)at * CH + c, word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // The state behind block `at - 1` of channel c (at > 0; block 0 gives its state without a map).
+    __device__ __forceinline__ float enter(int at, int c) const {
+        for (int poll = 0; poll < kMaxPolls; ++poll) {
+            uint32_t h[kWindow];
+            uint64_t m[kWindow];
+#pragma unroll
+            for (int w = 0; w < kWindow; ++w) {
+                const int j = at - 1 - w;
+                h[w] = kNone;
+                m[w] = ~0ull;
+                if (j < 0) continue;
+                h[w] = __hip_atomic_load(state + (long)j * CH + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                m[w] = __hip_atomic_load(map + (long)j * CH + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            // nearest block whose state is there for every channel, with every map after it
+            int from = -1;
+            bool maps = true;
+#pragma unroll
+            for (int w = 0; w < kWindow; ++w) {
+                if (from >= 0 || !maps) continue;
+                if (__all(h[w] != kNone)) from = w;
+                else maps = __all((uint32_t)(m[w] >> 32) != kNone);
+            }
+            if (from >= 0) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = kWindow - 1; w >= 0; --w) {
+                    if (w == from) s = __uint_as_float(h[w]);
+                    if (w < from) s = apply((uint32_t)(m[w] >> 32), __uint_as_float((uint32_t)m[w]), s);
+                }
+                return s;
+            }
+            __builtin_amdgcn_s_sleep(1);
+        }
+        return __uint_as_float(0x7fc00000u);
+    }
+};
+
+template <int W, int CH>
+struct Shared {
+    float A[W][CH], U[W][CH];  // a wave's composed map, per channel
+    int cut[W];                // it holds a border of sequences
+    float in[W][CH];           // the state that enters a wave's strands
+};
+
+// Composes the strands of a wave: (A, U) is the lane's own map, afterwards that of the
+// wave's strands up to and with its own.  The wave's map goes to shared memory.  REV: the
+// strands are taken from the last to the first.  A strand with a border of sequences (`cut`)
+// lets nothing of what enters it through: a flag and not A = 0, which would turn an infinity
+// of one sequence into a NaN of the next.
+template <int V, bool REV, bool PACKED, class S>
+__device__ __forceinline__ void compose(S &sh, float (&A)[V], float (&U)[V], bool &cut) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
+    const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
+#pragma unroll
+    for (int s = 1; s < kWS; s <<= 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float a = REV ? __shfl_down(A[v], s * kLR) : __shfl_up(A[v], s * kLR);
+            const float u = REV ? __shfl_down(U[v], s * kLR) : __shfl_up(U[v], s * kLR);
+            if (strand >= s && !(PACKED && cut)) {
+                U[v] = fmaf(A[v], u, U[v]);
+                A[v] *= a;
+            }
+        }
+        if (PACKED) {
+            const int c = REV ? __shfl_down((int)cut, s * kLR) : __shfl_up((int)cut, s * kLR);
+            if (strand >= s) cut = cut || c;
+        }
+    }
+    if (strand == kWS - 1) {
+        if (PACKED) sh.cut[wave] = cut;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            sh.A[wave][cl + v] = A[v];
+            sh.U[wave][cl + v] = U[v];
+        }
+    }
+}
+
+// One lane per channel: the composed map of the workgroup's waves, in the order of the strands.
+template <bool REV, bool PACKED, class S>
+__device__ __forceinline__ void block_map(const S &sh, int waves, int c, uint32_t &A, float &U) {
+    float a = 1.f, u = 0.f;
+    bool cut = false;
+    for (int i = 0; i < waves; ++i) {
+        const int w = REV ? waves - 1 - i : i;
+        if (PACKED && sh.cut[w]) {
+            cut = true;
+            u = sh.U[w][c];
+        } else {
+            u = fmaf(sh.A[w][c], u, sh.U[w][c]);
+            a *= sh.A[w][c];
+        }
+    }
+    A = cut ? kCut : word(a);
+    U = u;
+}
+
+// One lane per channel: the state that enters each wave when h enters the block.
+template <bool REV, bool PACKED, class S>
+__device__ __forceinline__ void wave_states(S &sh, int waves, int c, float h) {
+    for (int i = 0; i < waves; ++i) {
+        const int w = REV ? waves - 1 - i : i;
+        sh.in[w][c] = h;
+        h = PACKED && sh.cut[w] ? sh.U[w][c] : fmaf(sh.A[w][c], h, sh.U[w][c]);
+    }
+}
+
+// The state that enters the lane's strand.
+template <int V, bool REV, bool PACKED, class S>
+__device__ __forceinline__ void strand_states(const S &sh, const float (&A)[V], const float (&U)[V], bool cut, float (&h)[V]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
+    const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
+    const int before = PACKED ? (REV ? __shfl_down((int)cut, kLR) : __shfl_up((int)cut, kLR)) : 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float c = sh.in[wave][cl + v];
+        const float a = REV ? __shfl_down(A[v], kLR) : __shfl_up(A[v], kLR);
+        const float u = REV ? __shfl_down(U[v], kLR) : __shfl_up(U[v], kLR);
+        h[v] = strand ? (PACKED && before ? u : fmaf(a, c, u)) : c;
+    }
+}
+
+// This workgroup's place: blocks in the order of the recurrence, all channels of one block
+// before the next (neighbours read neighbouring memory, and a block's predecessors began long
+// before it).
+__device__ __forceinline__ unsigned place(const ScanParams &p, int &ticket) {
+    if (p.nblk == 1) return blockIdx.x;
+    if (threadIdx.x == 0) ticket = (int)(atomicAdd(static_cast<uint32_t *>(p.ws), 1u) + 1u);  // starts at kNone
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(ticket);  // one value for the wave, held as one
+}
+
+// The kernel of a call, with its Shape's numbers.
+struct Pick {
+    const void *fn;
+    int V, L, CH;
+};
+
+// K::get<IOB, GB, F, LOG, PACKED>() is a kernel.
+template <class K, bool IOB, bool GB, int F>
+Pick pick_rest(const ScanParams &p) {
+    typedef Shape<IOB, GB> Sh;
+    const void *fn = p.log_gate ? (p.off ? K::template get<IOB, GB, F, true, true>() : K::template get<IOB, GB, F, true, false>())
+                                : (p.off ? K::template get<IOB, GB, F, false, true>() : K::template get<IOB, GB, F, false, false>());
+    return {fn, Sh::V, Sh::L, Sh::CH};
+}
+
+template <class K, bool IOB, bool GB>
+Pick pick_factor(const ScanParams &p) {
+    if (p.beta) return pick_rest<K, IOB, GB, kGiven>(p);
+    return p.coupled ? pick_rest<K, IOB, GB, kCoupled>(p) : pick_rest<K, IOB, GB, kOne>(p);
+}
+
+template <class K>
+Pick pick(const ScanParams &p) {
+    if (p.io_bf16) return p.gate_bf16 ? pick_factor<K, true, true>(p) : pick_factor<K, true, false>(p);
+    return p.gate_bf16 ? pick_factor<K, false, true>(p) : pick_factor<K, false, false>(p);
+}
+
+// Channels of a workgroup, whatever the rest of the call is.
+inline int tile_channels(const ScanParams &p) {
+    return p.io_bf16 && p.gate_bf16 ? Shape<true, true>::CH : Shape<false, false>::CH;
+}
+
+// Bytes of the chain's words: a map and a state per block, sequence and channel of whole tiles.
+inline long chain_bytes(const ScanParams &p) {
+    if (p.nblk <= 1) return 0;
+    const long ch = tile_channels(p), columns = (long)p.B * ((p.D + ch - 1) / ch);
+    return kChainHead + (columns * p.nblk * ch * 12 + 15) / 16 * 16;
+}
+
+// Every word of the chain to kNone (a kernel, so that a captured graph replays it).
+__global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) ws[i] = (u32x4){kNone, kNone, kNone, kNone};
+}
+
+// Clears the chain's words and launches the blocks.
+template <class K>
+hipError_t launch_blocks(const ScanParams &p, hipStream_t s) {
+    const Pick k = pick<K>(p);
+    const int strands = ((p.T < kBlk ? p.T : kBlk) + k.L - 1) / k.L, waves = (strands + kWS - 1) / kWS;
+    const long blocks = (long)p.B * ((p.D + k.CH - 1) / k.CH) * p.nblk;
+    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    if (p.nblk > 1) {
+        u32x4 *ws = static_cast<u32x4 *>(p.ws);
+        long n = chain_bytes(p) / 16;
+        void *args[] = {&ws, &n};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&scan_fill_kernel), dim3((unsigned)((n + 255) / 256)),
+                                             dim3(256), args, 0, s);
+        if (e != hipSuccess) return e;
+    }
+    ScanParams q = p;
+    void *args[] = {&q};
+    return hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(64 * waves), args, 0, s);
+}
+
+}  // namespace
+}  // namespace gdr
