@@ -622,8 +622,8 @@ int check_scan_desc(const gdr_desc *d) {
     if (d->flags & ~(GDR_FLAG_LOG_GATE | GDR_FLAG_COUPLED)) return GDR_EINVAL;
     if (d->dv < 1) return GDR_EINVAL;
     if (d->alpha_mode != GDR_ALPHA_CHANNEL) return GDR_EUNSUPPORTED;
-    // channels in 31 bits; tokens and blocks of channels too
-    if ((long long)d->H * d->dv > 0x3fffffffLL || (long long)d->B * d->T > 0x3fffffffLL) return GDR_EUNSUPPORTED;
+    if ((long long)d->H * d->dv > kMaxRow || (long long)d->B * d->T > 0x3fffffffLL) return GDR_EUNSUPPORTED;
+    if ((int64_t)d->B * d->H * d->dv * 4 > kMaxStates) return GDR_EUNSUPPORTED;
     return GDR_OK;
 }
 
@@ -645,6 +645,7 @@ int scan_inputs(ScanParams &p, long long rows, const void *x, int64_t ldx, const
                 int64_t ldb, Span (&in)[3]) {
     const size_t es = p.io_bf16 ? 2 : 4, gs = p.gate_bf16 ? 2 : 4;
     if (!stride_ok(ldx, rows, p.D) || !stride_ok(lda, rows, p.D) || !stride_ok(ldb, rows, p.D)) return GDR_EINVAL;
+    if (ldx > kMaxRow || lda > kMaxRow || ldb > kMaxRow) return GDR_EUNSUPPORTED;
     if (p.coupled && beta) return GDR_EINVAL;
     if (rows > 0 && p.D > 0 && (!x || !alpha)) return GDR_EINVAL;
     if (!aligned_to(x, es) || !aligned_to(alpha, gs) || !aligned_to(beta, gs)) return GDR_EINVAL;
@@ -664,6 +665,7 @@ int scan_sequences(ScanParams &p, const int32_t *seq_off, int32_t n_seq) {
     if (!seq_off) return n_seq == 0 ? GDR_OK : GDR_EINVAL;
     if (n_seq < 0 || !aligned_to(seq_off, 4)) return GDR_EINVAL;
     if (p.B != 1) return GDR_EINVAL;
+    if ((int64_t)n_seq * p.D * 4 > kMaxStates) return GDR_EUNSUPPORTED;
     p.off = seq_off;
     p.nseq = n_seq;
     return GDR_OK;

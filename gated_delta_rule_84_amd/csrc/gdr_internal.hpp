@@ -91,6 +91,10 @@ struct QkParams {
     int lanes, rows, blocks_q, blocks_k;  // set by the launcher
 };
 
+// Most elements between tokens of a gated linear recurrence (and channels of one), so that a block
+// of 256 tokens spans at most 2^30 bytes, and most bytes of the states of packed sequences.
+constexpr int64_t kMaxRow = 1 << 20, kMaxStates = 1 << 30;
+
 // Parameters of one gated linear recurrence call (forward, backward or single step).
 struct ScanParams {
     int B, T, D;  // D channels per token

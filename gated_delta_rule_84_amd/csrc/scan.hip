@@ -4,6 +4,56 @@
 namespace gdr {
 namespace {
 
+// Words at an element-aligned address (the hardware takes a global access of a dword or more at
+// any byte address); n of the V elements, one by one where that is not all of them.
+typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool BF, int V>
+__device__ __forceinline__ void load_at(Pack<BF, V> &x, const void *base, int64_t at, int n) {
+    constexpr int N = Pack<BF, V>::N;
+    const char *p = static_cast<const char *>(base) + at * x.es;
+    if (n < V) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) x.w[k] = 0;
+        for (int v = 0; v < n; ++v) {
+            const uint32_t e = BF ? reinterpret_cast<const uint16_t *>(p)[v] : reinterpret_cast<const uint32_t *>(p)[v];
+#pragma unroll
+            for (int k = 0; k < N; ++k) x.w[k] |= k == (BF ? v / 2 : v) ? (BF && (v & 1) ? e << 16 : e) : 0;
+        }
+    } else if constexpr (N == 2) {
+        const w2 a = *reinterpret_cast<const w2 *>(p);
+        x.w[0] = a[0];
+        x.w[1] = a[1];
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            const w4 a = *reinterpret_cast<const w4 *>(p + 4 * k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.w[k + i] = a[i];
+        }
+    }
+}
+
+template <bool BF, int V>
+__device__ __forceinline__ void store_at(const Pack<BF, V> &x, void *base, int64_t at, int n) {
+    constexpr int N = Pack<BF, V>::N;
+    char *p = static_cast<char *>(base) + at * x.es;
+    if (n < V) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (v >= n) continue;
+            if constexpr (BF) reinterpret_cast<uint16_t *>(p)[v] = (uint16_t)(x.w[v / 2] >> (16 * (v & 1)));
+            else reinterpret_cast<uint32_t *>(p)[v] = x.w[v];
+        }
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<w2 *>(p) = (w2){x.w[0], x.w[1]};
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) *reinterpret_cast<w4 *>(p + 4 * k) = (w4){x.w[k], x.w[k + 1], x.w[k + 2], x.w[k + 3]};
+    }
+}
+
 // One token for every batch row: the state is read and written in place.
 template <bool IOB, bool GB, int F, bool LOG>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
@@ -14,31 +64,22 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
     if (b >= p.B) return;
     Pack<IOB, V> x;
     Pack<GB, V> al, be;
-    float *S = p.ST + b * p.D + ch;
+    Pack<false, V> S;
     float a[V], u[V], h[V];
-    const char *px = static_cast<const char *>(p.x) + (b * p.ldx + ch) * (IOB ? 2 : 4);
-    const char *pa = static_cast<const char *>(p.alpha) + (b * p.lda + ch) * (GB ? 2 : 4);
-    const char *pb = static_cast<const char *>(p.beta) + (b * p.ldb + ch) * (GB ? 2 : 4);
-    char *py = static_cast<char *>(p.y) + (b * p.D + ch) * (IOB ? 2 : 4);
-    const bool whole = n == V;
-    if (whole) {
-        x.load(px);
-        al.load(pa);
-        if (F == kGiven) be.load(pb);
-    } else {
-        x.load(px, n);
-        al.load(pa, n);
-        if (F == kGiven) be.load(pb, n);
-    }
-    load_state<V>(S, n, h);
+    load_at(x, p.x, b * p.ldx + ch, n);
+    load_at(al, p.alpha, b * p.lda + ch, n);
+    if (F == kGiven) load_at(be, p.beta, b * p.ldb + ch, n);
+    load_at(S, p.ST, b * p.D + ch, n);
     gates<F, LOG, GB, V>(al, be, a, u);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], h[v], u[v] * x.get(v));
+    for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], S.get(v), u[v] * x.get(v));
 #pragma unroll
-    for (int v = 0; v < V; v += 2) x.set2(v, h[v], h[v + 1]);
-    store_state<V>(S, n, h);
-    if (whole) x.store(py);
-    else x.store(py, n);
+    for (int v = 0; v < V; v += 2) {
+        S.set2(v, h[v], h[v + 1]);
+        x.set2(v, h[v], h[v + 1]);
+    }
+    store_at(S, p.ST, b * p.D + ch, n);
+    store_at(x, p.y, b * p.D + ch, n);
 }
 
 // ST = S0 (or 0) of a call without tokens

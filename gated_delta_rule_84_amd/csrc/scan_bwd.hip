@@ -17,30 +17,32 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
     const bool whole = (tile + 1) * CH <= (unsigned)p.D;
-    const int t0 = k * kBlk + strand * L, tb = min(t0, p.T - 1), last = p.T - 1 - tb;
-    const int64_t row = (int64_t)b * p.T + tb;
+    const int local = strand * L, t0 = k * kBlk + local;
+    const int rows = min(kBlk, p.T - (int)k * kBlk);  // of this block
+    const int64_t row = (int64_t)b * p.T + k * kBlk;  // its first
+    const unsigned there = rows >= local + L ? (1u << L) - 1 : rows > local ? (1u << (rows - local)) - 1 : 0;
     Pack<IOB, V> x[L], dy[L];
     Pack<GB, V> al[L], be[LB];
-    Rows<IOB, V, L>(p.x, row, p.ldx, ch).load(x, last, whole, n);
-    Rows<GB, V, L>(p.alpha, row, p.lda, ch).load(al, last, whole, n);
-    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, p.ldb, ch).load(be, last, whole, n);
-    Rows<IOB, V, L>(p.dy, row, p.D, ch).load(dy, last, whole, n);
+    Rows<IOB, V, L>(p.x, row, rows, p.ldx, p.D, local, ch).load(x, whole, n);
+    Rows<GB, V, L>(p.alpha, row, rows, p.lda, p.D, local, ch).load(al, whole, n);
+    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, rows, p.ldb, p.D, local, ch).load(be, whole, n);
+    Rows<IOB, V, L>(p.dy, row, rows, p.D, p.D, local, ch).load(dy, whole, n);
     Marks<PACKED, L> m;
-    m.find(p, t0);
-    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
+    m.find(p, t0, there);
+    const States S0(p.S0, PACKED ? p.nseq : p.B, p.D, ch), dST(p.dST, PACKED ? p.nseq : p.B, p.D, ch), dS0(p.dS0, PACKED ? p.nseq : p.B, p.D, ch);
     if (PACKED && p.dS0 && k == 0) {
         for (int i = strand; i < p.nseq; i += waves * kWS) {
             if (p.off[i + 1] > p.off[i]) continue;
             float c[V];
-            load_state<V>(p.dST ? p.dST + (int64_t)i * p.D + ch : nullptr, n, c);
-            store_state<V>(p.dS0 + (int64_t)i * p.D + ch, n, c);
+            dST.load(i, c);
+            dS0.store(i, n, c);
         }
     }
-    if (PACKED || (k + 1) * kBlk > (unsigned)p.T) {
+    if (PACKED || rows < kBlk) {
         leave_out<LOG>(m.in, x, al, be);
 #pragma unroll
         for (int j = 0; j < L; ++j)
-            if (!(m.in >> j & 1)) dy[j].clear();
+            dy[j].choose(m.in >> j & 1, 0);
     }
     float a[L][V], bb[L][V], A[V], U[V], GA[V], GU[V], h[V], G[V];
 #pragma unroll
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
     for (int j = 0; j < L; ++j) {
         gates<F, LOG, GB, V>(al[j], be[j % LB], a[j], bb[j]);
         const bool first = PACKED && (m.first >> j & 1);
-        if (first) load_state<V>(state(p.S0, j), n, U);
+        if (first) S0.load(m.seq[j], U);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             U[v] = fmaf(a[j][v], U[v], bb[j][v] * x[j].get(v));
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
         const bool end = PACKED && (m.last >> j & 1);
-        if (end) load_state<V>(state(p.dST, j), n, GU);
+        if (end) dST.load(m.seq[j], GU);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             GU[v] = a[j][v] * (dy[j].get(v) + GU[v]);
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
             float s = h[v + e];
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                if (PACKED && (m.first >> j & 1)) s = p.S0 && v + e < n ? state(p.S0, j)[v + e] : 0.f;
+                if (PACKED && (m.first >> j & 1)) s = S0.load1(m.seq[j], v + e);
                 before[e][j] = s;
                 s = fmaf(a[j][v + e], s, bb[j][v + e] * x[j].get(v + e));
             }
@@ -120,24 +122,23 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
             float dx[2], da[2], db[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if (PACKED && (m.last >> j & 1)) G[v + e] = p.dST && v + e < n ? state(p.dST, j)[v + e] : 0.f;
+                if (PACKED && (m.last >> j & 1)) G[v + e] = dST.load1(m.seq[j], v + e);
                 const float g = dy[j].get(v + e) + G[v + e], xv = x[j].get(v + e);
                 dx[e] = bb[j][v + e] * g;
                 db[e] = g * xv;
                 G[v + e] = a[j][v + e] * g;
                 da[e] = (LOG ? G[v + e] : g) * (F == kCoupled ? before[e][j] - xv : before[e][j]);
-                if (PACKED && p.dS0 && (m.first >> j & 1) && v + e < n)
-                    p.dS0[(int64_t)m.seq[j] * p.D + ch + v + e] = G[v + e];
+                if (PACKED && (m.first >> j & 1)) dS0.store1(m.seq[j], v + e, n, G[v + e]);
             }
             dy[j].set2(v, dx[0], dx[1]);
             al[j].set2(v, da[0], da[1]);
             if (F == kGiven) be[j % LB].set2(v, db[0], db[1]);
         }
     }
-    Rows<IOB, V, L>(p.dx, row, p.D, ch).store(dy, m.in, whole, n);
-    Rows<GB, V, L>(p.dalpha, row, p.D, ch).store(al, m.in, whole, n);
-    if constexpr (F == kGiven) Rows<GB, V, LB>(p.dbeta, row, p.D, ch).store(be, m.in, whole, n);
-    if (!PACKED && strand == 0 && k == 0 && p.dS0) store_state<V>(p.dS0 + (int64_t)b * p.D + ch, n, G);
+    Rows<IOB, V, L>(p.dx, row, rows, p.D, p.D, local, ch).store(dy, m.in, whole, n);
+    Rows<GB, V, L>(p.dalpha, row, rows, p.D, p.D, local, ch).store(al, m.in, whole, n);
+    if constexpr (F == kGiven) Rows<GB, V, LB>(p.dbeta, row, rows, p.D, p.D, local, ch).store(be, m.in, whole, n);
+    if (!PACKED && strand == 0 && k == 0) dS0.store(b, n, G);
 }
 
 struct Bwd {

@@ -16,25 +16,27 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
     const bool whole = (tile + 1) * CH <= (unsigned)p.D;  // every lane's channels are there
-    const int t0 = k * kBlk + strand * L, tb = min(t0, p.T - 1), last = p.T - 1 - tb;
-    const int64_t row = (int64_t)b * p.T + tb;
+    const int local = strand * L, t0 = k * kBlk + local;
+    const int rows = min(kBlk, p.T - (int)k * kBlk);  // of this block
+    const int64_t row = (int64_t)b * p.T + k * kBlk;  // its first
+    const unsigned there = rows >= local + L ? (1u << L) - 1 : rows > local ? (1u << (rows - local)) - 1 : 0;
     Pack<IOB, V> x[L];
     Pack<GB, V> al[L], be[LB];
-    Rows<IOB, V, L>(p.x, row, p.ldx, ch).load(x, last, whole, n);
-    Rows<GB, V, L>(p.alpha, row, p.lda, ch).load(al, last, whole, n);
-    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, p.ldb, ch).load(be, last, whole, n);
+    Rows<IOB, V, L>(p.x, row, rows, p.ldx, p.D, local, ch).load(x, whole, n);
+    Rows<GB, V, L>(p.alpha, row, rows, p.lda, p.D, local, ch).load(al, whole, n);
+    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, rows, p.ldb, p.D, local, ch).load(be, whole, n);
     Marks<PACKED, L> m;
-    m.find(p, t0);
-    auto state = [&](const float *base, int j) { return base ? base + (int64_t)m.seq[j] * p.D + ch : nullptr; };
+    m.find(p, t0, there);
+    const States S0(p.S0, PACKED ? p.nseq : p.B, p.D, ch), ST(p.ST, PACKED ? p.nseq : p.B, p.D, ch);
     if (PACKED && p.ST && k == 0) {  // empty sequences end as they begin
         for (int i = strand; i < p.nseq; i += waves * kWS) {
             if (p.off[i + 1] > p.off[i]) continue;
             float c[V];
-            load_state<V>(p.S0 ? p.S0 + (int64_t)i * p.D + ch : nullptr, n, c);
-            store_state<V>(p.ST + (int64_t)i * p.D + ch, n, c);
+            S0.load(i, c);
+            ST.store(i, n, c);
         }
     }
-    if (PACKED || (k + 1) * kBlk > (unsigned)p.T) leave_out<LOG>(m.in, x, al, be);
+    if (PACKED || rows < kBlk) leave_out<LOG>(m.in, x, al, be);
     float a[L][V], u[L][V], A[V], U[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -45,7 +47,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
     for (int j = 0; j < L; ++j) {
         gates<F, LOG, GB, V>(al[j], be[j % LB], a[j], u[j]);
         const bool first = PACKED && (m.first >> j & 1);
-        if (first) load_state<V>(state(p.S0, j), n, U);
+        if (first) S0.load(m.seq[j], U);
 #pragma unroll
         for (int v = 0; v < V; ++v) u[j][v] *= x[j].get(v);
 #pragma unroll
@@ -77,16 +79,15 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
     strand_states<V, false, PACKED>(sh, A, U, cut, h);
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        if (PACKED && (m.first >> j & 1)) load_state<V>(state(p.S0, j), n, h);
+        if (PACKED && (m.first >> j & 1)) S0.load(m.seq[j], h);
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], u[j][v]);
 #pragma unroll
         for (int v = 0; v < V; v += 2) x[j].set2(v, h[v], h[v + 1]);
-        if (PACKED && p.ST && (m.last >> j & 1)) store_state<V>(p.ST + (int64_t)m.seq[j] * p.D + ch, n, h);
+        if (PACKED && (m.last >> j & 1)) ST.store(m.seq[j], n, h);
     }
-    Rows<IOB, V, L>(p.y, row, p.D, ch).store(x, m.in, whole, n);
-    if (!PACKED && p.ST && k == p.nblk - 1 && strand == waves * kWS - 1)
-        store_state<V>(p.ST + (int64_t)b * p.D + ch, n, h);
+    Rows<IOB, V, L>(p.y, row, rows, p.D, p.D, local, ch).store(x, m.in, whole, n);
+    if (!PACKED && k == p.nblk - 1 && strand == waves * kWS - 1) ST.store(b, n, h);
 }
 
 struct Fwd {

@@ -48,13 +48,19 @@ struct Shape {
     static constexpr int CH = kLR * V;  // channels per workgroup
 };
 
-typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
-typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
+// A range of memory that the hardware checks: loads past its end give 0, stores past it do nothing.
+typedef __amdgpu_buffer_rsrc_t Buf;
+
+__device__ __forceinline__ Buf buf(const void *base, int64_t at, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(static_cast<char *>(const_cast<void *>(base)) + at, 0, base ? (int)bytes : 0, 0x00020000);
+}
+
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every range: they hold at most 2^30 bytes
 
 // V elements of one token, packed as they are stored.
 template <bool BF, int V>
 struct Pack {
-    static constexpr int N = BF ? V / 2 : V;
+    static constexpr int N = BF ? V / 2 : V, es = BF ? 2 : 4;
     uint32_t w[N];
 
     __device__ __forceinline__ float get(int v) const {
@@ -70,98 +76,86 @@ struct Pack {
             w[v + 1] = __float_as_uint(b);
         }
     }
-    __device__ __forceinline__ void load(const char *p) {
+    // V elements at byte `at`
+    __device__ __forceinline__ void load(Buf r, uint32_t at) {
         if constexpr (N == 2) {
-            const w2 a = *reinterpret_cast<const w2 *>(p);
+            const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
             w[0] = a[0];
             w[1] = a[1];
         } else {
 #pragma unroll
             for (int k = 0; k < N; k += 4) {
-                const w4 a = *reinterpret_cast<const w4 *>(p + 4 * k);
+                const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(r, at + 4 * k, 0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[k + i] = a[i];
             }
         }
     }
-    __device__ __forceinline__ void store(char *p) const {
+    __device__ __forceinline__ void store(Buf r, uint32_t at) const {
         if constexpr (N == 2) {
-            w2 a;
-            a[0] = w[0];
-            a[1] = w[1];
-            *reinterpret_cast<w2 *>(p) = a;
+            __builtin_amdgcn_raw_buffer_store_b64((u32x2){w[0], w[1]}, r, at, 0, 0);
         } else {
 #pragma unroll
-            for (int k = 0; k < N; k += 4) {
-                w4 a;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = w[k + i];
-                *reinterpret_cast<w4 *>(p + 4 * k) = a;
-            }
+            for (int k = 0; k < N; k += 4)
+                __builtin_amdgcn_raw_buffer_store_b128((u32x4){w[k], w[k + 1], w[k + 2], w[k + 3]}, r, at + 4 * k, 0, 0);
         }
     }
     // the first n of the V elements alone
-    __device__ __forceinline__ void load(const char *p, int n) {
-        clear();
+    __device__ __forceinline__ void load(Buf r, uint32_t at, int n) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (v >= n) continue;
-            if constexpr (BF)
-                w[v / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[v] << (16 * (v & 1));
-            else
-                w[v] = reinterpret_cast<const uint32_t *>(p)[v];
+            const uint32_t o = v < n ? at + v * es : kNowhere;
+            if constexpr (BF) {
+                const uint32_t h = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0);
+                w[v / 2] = v & 1 ? w[v / 2] | h << 16 : h;
+            } else {
+                w[v] = __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
+            }
         }
     }
-    __device__ __forceinline__ void store(char *p, int n) const {
+    __device__ __forceinline__ void store(Buf r, uint32_t at, int n) const {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (v >= n) continue;
+            const uint32_t o = v < n ? at + v * es : kNowhere;
             if constexpr (BF)
-                reinterpret_cast<uint16_t *>(p)[v] = (uint16_t)(w[v / 2] >> (16 * (v & 1)));
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[v / 2] >> (16 * (v & 1))), r, o, 0, 0);
             else
-                reinterpret_cast<uint32_t *>(p)[v] = w[v];
+                __builtin_amdgcn_raw_buffer_store_b32(w[v], r, o, 0, 0);
         }
     }
-    __device__ __forceinline__ void clear() {
+    // its words where `keep`, else `other`
+    __device__ __forceinline__ void choose(bool keep, uint32_t other) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = 0;
-    }
-    __device__ __forceinline__ void ones() {
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = BF ? 0x3f803f80u : 0x3f800000u;
+        for (int k = 0; k < N; ++k) w[k] = keep ? w[k] : other;
     }
 };
 
-// n of V floats; a NULL address holds zeros
-template <int V>
-__device__ __forceinline__ void load_state(const float *p, int n, float (&f)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = 0.f;
-    if (!p) return;
-    if (n == V) {
+// The fp32 states of all sequences, [n, D]: row i, the lane's channels.  Channels past the row's end
+// read what follows it (or 0) and are never stored.
+struct States {
+    Buf r;
+    uint32_t row, ch;
+    __device__ __forceinline__ States(const float *base, int n, int D, int ch0)
+        : r(buf(base, 0, (uint32_t)n * (uint32_t)D * 4)), row((uint32_t)D * 4), ch((uint32_t)ch0 * 4) {}
+    template <int V>
+    __device__ __forceinline__ void load(int i, float (&f)[V]) const {
         Pack<false, V> w;
-        w.load(reinterpret_cast<const char *>(p));
+        w.load(r, i * row + ch);
 #pragma unroll
         for (int v = 0; v < V; ++v) f[v] = w.get(v);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (v < n) f[v] = p[v];
     }
-}
-template <int V>
-__device__ __forceinline__ void store_state(float *p, int n, const float (&f)[V]) {
-    if (n == V) {
-        Pack<false, V> w;
-#pragma unroll
-        for (int v = 0; v < V; v += 2) w.set2(v, f[v], f[v + 1]);
-        w.store(reinterpret_cast<char *>(p));
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (v < n) p[v] = f[v];
+    __device__ __forceinline__ float load1(int i, int v) const {
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, i * row + ch + 4 * v, 0, 0));
     }
-}
+    __device__ __forceinline__ void store1(int i, int v, int n, float f) const {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), r, v < n ? i * row + ch + 4 * v : kNowhere, 0, 0);
+    }
+    template <int V>
+    __device__ __forceinline__ void store(int i, int n, const float (&f)[V]) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) store1(i, v, n, f[v]);
+    }
+};
 
 // exp(x) and 1 - exp(x), both to about 2 units in the last place, for x in -88 .. 88 (below, 0 and 1;
 // above, as at 88).  With n = rint(x / ln 2) and r = x - n ln 2 (ln 2 in two parts), exp(x) = s + s q
@@ -197,45 +191,44 @@ __device__ __forceinline__ void gates(const Pack<GB, V> &al, const Pack<GB, V> &
 }
 
 // Tokens of a strand that are in no sequence become ones that change nothing: a = 1, b x = 0.
-template <bool LOG, class X, class G, int L, int LB>
-__device__ __forceinline__ void leave_out(unsigned in, X (&x)[L], G (&al)[L], G (&be)[LB]) {
+template <bool LOG, bool IOB, bool GB, int V, int L, int LB>
+__device__ __forceinline__ void leave_out(unsigned in, Pack<IOB, V> (&x)[L], Pack<GB, V> (&al)[L], Pack<GB, V> (&be)[LB]) {
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        if (in >> j & 1) continue;
-        x[j].clear();
-        be[j % LB].clear();
-        if (LOG) al[j].clear();
-        else al[j].ones();
+        const bool keep = in >> j & 1;
+        x[j].choose(keep, 0);
+        be[j % LB].choose(keep, 0);
+        al[j].choose(keep, LOG ? 0 : (GB ? 0x3f803f80u : 0x3f800000u));
     }
 }
 
-// The rows of a lane's strand in one tensor: `ld` elements between tokens, `last` the last token
-// that the memory holds after the strand's first.  Rows past it are read at it (and left out later).
+// The rows of a block of one tensor: from the block's first row to the end of the last one that is
+// there, so rows past T are past the range.  `at` is the byte offset of the lane's first row.
 template <bool BF, int V, int L>
 struct Rows {
-    const char *p;
-    int64_t step;
-    __device__ __forceinline__ Rows(const void *base, int64_t row, int64_t ld, int ch)
-        : p(static_cast<const char *>(base) + (row * ld + ch) * (BF ? 2 : 4)), step(ld * (BF ? 2 : 4)) {}
-    __device__ __forceinline__ void load(Pack<BF, V> (&x)[L], int last, bool whole, int n) const {
+    static constexpr int es = BF ? 2 : 4;
+    Buf r;
+    uint32_t at, step;
+    __device__ __forceinline__ Rows(const void *t, int64_t row, int rows, int64_t ld, int D, int local, int ch)
+        : r(buf(t, row * ld * es, ((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)D) * es)),
+          at(((uint32_t)local * (uint32_t)ld + (uint32_t)ch) * es), step((uint32_t)ld * es) {}
+    // `whole`: all V channels of every lane are in the row, else n of them
+    __device__ __forceinline__ void load(Pack<BF, V> (&x)[L], bool whole, int n) const {
         if (whole) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) x[j].load(p + min(j, last) * step);
+            for (int j = 0; j < L; ++j) x[j].load(r, at + j * step);
         } else {
 #pragma unroll
-            for (int j = 0; j < L; ++j) x[j].load(p + min(j, last) * step, n);
+            for (int j = 0; j < L; ++j) x[j].load(r, at + j * step, n);
         }
     }
     __device__ __forceinline__ void store(const Pack<BF, V> (&x)[L], unsigned in, bool whole, int n) const {
-        char *q = const_cast<char *>(p);
         if (whole) {
 #pragma unroll
-            for (int j = 0; j < L; ++j)
-                if (in >> j & 1) x[j].store(q + j * step);
+            for (int j = 0; j < L; ++j) x[j].store(r, in >> j & 1 ? at + j * step : kNowhere);
         } else {
 #pragma unroll
-            for (int j = 0; j < L; ++j)
-                if (in >> j & 1) x[j].store(q + j * step, n);
+            for (int j = 0; j < L; ++j) x[j].store(r, at + j * step, in >> j & 1 ? n : 0);
         }
     }
 };
@@ -248,7 +241,7 @@ struct Marks {
     unsigned in = 0, first = 0, last = 0;
     int seq[L];
 
-    __device__ __forceinline__ void find(const ScanParams &p, int t0) {
+    __device__ __forceinline__ void find(const ScanParams &p, int t0, unsigned there) {
         if constexpr (PACKED) {
             int lo = 0, hi = p.nseq;  // first sequence that ends after t0
             while (lo < hi) {
@@ -261,15 +254,14 @@ struct Marks {
             for (int j = 0; j < L; ++j) {
                 const int t = t0 + j;
                 while (i < p.nseq && p.off[i + 1] <= t) ++i;
-                const bool ok = i < p.nseq && t < p.T && p.off[i] <= t;
+                const bool ok = i < p.nseq && (there >> j & 1) && p.off[i] <= t;
                 seq[j] = ok ? i : 0;
                 in |= (unsigned)ok << j;
                 first |= (unsigned)(ok && p.off[i] == t) << j;
                 last |= (unsigned)(ok && p.off[i + 1] == t + 1) << j;
             }
         } else {
-            const int n = p.T - t0;
-            in = n >= L ? (1u << L) - 1 : (n > 0 ? (1u << n) - 1 : 0);
+            in = there;
         }
     }
 };
@@ -285,7 +277,7 @@ struct Marks {
 // they begin: every block before a waiting one is running or done, so each wait ends.
 constexpr uint32_t kNone = 0xffffffffu;  // what launch_fill leaves
 constexpr uint32_t kCut = 0xfffffffeu;   // in a map's factor: nothing of what enters gets through
-constexpr int kWindow = 8;               // blocks looked back over at a time
+constexpr int kWindow = 4;               // blocks looked back over at a time
 constexpr int kMaxPolls = 1 << 22;       // some seconds: a bound that a sound run never meets
 
 __device__ __forceinline__ uint32_t word(float f) {
@@ -438,12 +430,12 @@ __device__ __forceinline__ void strand_states(const S &sh, const float (&A)[V], 
 
 // This workgroup's place: blocks in the order of the recurrence, all channels of one block
 // before the next (neighbours read neighbouring memory, and a block's predecessors began long
-// before it).
+// before it).  Never past the last place, whatever the counter holds.
 __device__ __forceinline__ unsigned place(const ScanParams &p, int &ticket) {
     if (p.nblk == 1) return blockIdx.x;
     if (threadIdx.x == 0) ticket = (int)(atomicAdd(static_cast<uint32_t *>(p.ws), 1u) + 1u);  // starts at kNone
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(ticket);  // one value for the wave, held as one
+    return min((unsigned)__builtin_amdgcn_readfirstlane(ticket), gridDim.x - 1);  // one value for the wave, held as one
 }
 
 // The kernel of a call, with its Shape's numbers.

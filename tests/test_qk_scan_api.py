@@ -150,6 +150,7 @@ def test_scan_pointers(g):
     assert call(ldx=59) == g.GDR_EINVAL
     assert call(lda=-60) == g.GDR_EINVAL
     assert call(ldb=1 << 60) == g.GDR_EINVAL
+    assert call(ldx=(1 << 20) + 1) == g.GDR_EUNSUPPORTED
     assert call(x=FakePtr(x.addr + 1)) == g.GDR_EINVAL
     assert call(a=FakePtr(a.addr + 2)) == g.GDR_EINVAL                       # fp32 gates
     assert call(ST=FakePtr(ST.addr + 2)) == g.GDR_EINVAL
