@@ -7,8 +7,8 @@ namespace {
 template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
 __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(ScanParams p) {
     typedef Shape<IOB, GB> Sh;
-    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH, LB = F == kGiven ? L : 1;
-    __shared__ Shared<Sh::waves, CH> sh;
+    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH, kLR = Sh::LR, kWS = Sh::WS, LB = F == kGiven ? L : 1;
+    __shared__ Shared<Sh> sh;
     __shared__ int ticket;
     const int waves = blockDim.x >> 6;
     const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);

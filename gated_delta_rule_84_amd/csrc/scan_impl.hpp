@@ -31,21 +31,20 @@ namespace gdr {
 namespace {
 
 constexpr int kBlk = GDR_SCAN_BLOCK;  // tokens per block
-constexpr int kLR = 8;                // lanes per row
-constexpr int kWS = 64 / kLR;         // strands per wave
 constexpr int kChainHead = 256;       // bytes before the chain's words: the counter of blocks
 
 // How the input factor b is given.
 enum Factor { kOne = 0, kGiven = 1, kCoupled = 2 };
 
-// Channels per lane, tokens per strand and lanes per workgroup for a pair of types.
+// Channels per lane, tokens per strand, lanes per row and the rest for a pair of types.
 template <bool IOB, bool GB>
 struct Shape {
-    static constexpr int V = IOB && GB ? 8 : 4;
-    static constexpr int L = 32 / V;
-    static constexpr int threads = kBlk / L * kLR;
+    static constexpr int V = 4, L = 8;
+    static constexpr int LR = IOB || GB ? 16 : 8;
+    static constexpr int WS = 64 / LR;  // strands per wave
+    static constexpr int threads = kBlk / L * LR;
     static constexpr int waves = threads / 64;
-    static constexpr int CH = kLR * V;  // channels per workgroup
+    static constexpr int CH = LR * V;  // channels per workgroup
 };
 
 // A range of memory that the hardware checks: loads past its end give 0, stores past it do nothing.
@@ -342,8 +341,9 @@ struct Chain {
     }
 };
 
-template <int W, int CH>
+template <class Sh, int W = Sh::waves, int CH = Sh::CH>
 struct Shared {
+    static constexpr int LR = Sh::LR, WS = Sh::WS;
     float A[W][CH], U[W][CH];  // a wave's composed map, per channel
     int cut[W];                // it holds a border of sequences
     float in[W][CH];           // the state that enters a wave's strands
@@ -356,6 +356,7 @@ struct Shared {
 // of one sequence into a NaN of the next.
 template <int V, bool REV, bool PACKED, class S>
 __device__ __forceinline__ void compose(S &sh, float (&A)[V], float (&U)[V], bool &cut) {
+    constexpr int kLR = S::LR, kWS = S::WS;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
     const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
 #pragma unroll
@@ -416,6 +417,7 @@ __device__ __forceinline__ void wave_states(S &sh, int waves, int c, float h) {
 // The state that enters the lane's strand.
 template <int V, bool REV, bool PACKED, class S>
 __device__ __forceinline__ void strand_states(const S &sh, const float (&A)[V], const float (&U)[V], bool cut, float (&h)[V]) {
+    constexpr int kLR = S::LR, kWS = S::WS;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = (lane & (kLR - 1)) * V;
     const int strand = REV ? kWS - 1 - lane / kLR : lane / kLR;
     const int before = PACKED ? (REV ? __shfl_down((int)cut, kLR) : __shfl_up((int)cut, kLR)) : 0;
@@ -441,7 +443,7 @@ __device__ __forceinline__ unsigned place(const ScanParams &p, int &ticket) {
 // The kernel of a call, with its Shape's numbers.
 struct Pick {
     const void *fn;
-    int V, L, CH;
+    int V, L, WS, CH;
 };
 
 // K::get<IOB, GB, F, LOG, PACKED>() is a kernel.
@@ -450,7 +452,7 @@ Pick pick_rest(const ScanParams &p) {
     typedef Shape<IOB, GB> Sh;
     const void *fn = p.log_gate ? (p.off ? K::template get<IOB, GB, F, true, true>() : K::template get<IOB, GB, F, true, false>())
                                 : (p.off ? K::template get<IOB, GB, F, false, true>() : K::template get<IOB, GB, F, false, false>());
-    return {fn, Sh::V, Sh::L, Sh::CH};
+    return {fn, Sh::V, Sh::L, Sh::WS, Sh::CH};
 }
 
 template <class K, bool IOB, bool GB>
@@ -467,7 +469,7 @@ Pick pick(const ScanParams &p) {
 
 // Channels of a workgroup, whatever the rest of the call is.
 inline int tile_channels(const ScanParams &p) {
-    return p.io_bf16 && p.gate_bf16 ? Shape<true, true>::CH : Shape<false, false>::CH;
+    return p.io_bf16 || p.gate_bf16 ? Shape<true, true>::CH : Shape<false, false>::CH;
 }
 
 // Bytes of the chain's words: a map and a state per block, sequence and channel of whole tiles.
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
 template <class K>
 hipError_t launch_blocks(const ScanParams &p, hipStream_t s) {
     const Pick k = pick<K>(p);
-    const int strands = ((p.T < kBlk ? p.T : kBlk) + k.L - 1) / k.L, waves = (strands + kWS - 1) / kWS;
+    const int strands = ((p.T < kBlk ? p.T : kBlk) + k.L - 1) / k.L, waves = (strands + k.WS - 1) / k.WS;
     const long blocks = (long)p.B * ((p.D + k.CH - 1) / k.CH) * p.nblk;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
     if (p.nblk > 1) {
