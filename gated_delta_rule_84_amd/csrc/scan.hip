@@ -9,9 +9,9 @@ namespace {
 typedef uint32_t w2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t w4 __attribute__((ext_vector_type(4), aligned(2)));
 
-template <bool BF, int V>
-__device__ __forceinline__ void load_at(Pack<BF, V> &x, const void *base, int64_t at, int n) {
-    constexpr int N = Pack<BF, V>::N;
+template <bool BF>
+__device__ __forceinline__ void load_at(Pack<BF> &x, const void *base, int64_t at, int n) {
+    constexpr int N = Pack<BF>::N;
     const char *p = static_cast<const char *>(base) + at * x.es;
     if (n < V) {
 #pragma unroll
@@ -35,9 +35,9 @@ __device__ __forceinline__ void load_at(Pack<BF, V> &x, const void *base, int64_
     }
 }
 
-template <bool BF, int V>
-__device__ __forceinline__ void store_at(const Pack<BF, V> &x, void *base, int64_t at, int n) {
-    constexpr int N = Pack<BF, V>::N;
+template <bool BF>
+__device__ __forceinline__ void store_at(const Pack<BF> &x, void *base, int64_t at, int n) {
+    constexpr int N = Pack<BF>::N;
     char *p = static_cast<char *>(base) + at * x.es;
     if (n < V) {
 #pragma unroll
@@ -57,20 +57,19 @@ __device__ __forceinline__ void store_at(const Pack<BF, V> &x, void *base, int64
 // One token for every batch row: the state is read and written in place.
 template <bool IOB, bool GB, int F, bool LOG>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
-    constexpr int V = Shape<IOB, GB>::V;
     const unsigned groups = (p.D + V - 1) / V;
     const long i = (long)blockIdx.x * 256 + threadIdx.x, b = i / groups;
     const int ch = (int)(i - b * groups) * V, n = min(V, p.D - ch);
     if (b >= p.B) return;
-    Pack<IOB, V> x;
-    Pack<GB, V> al, be;
-    Pack<false, V> S;
+    Pack<IOB> x;
+    Pack<GB> al, be;
+    Pack<false> S;
     float a[V], u[V], h[V];
     load_at(x, p.x, b * p.ldx + ch, n);
     load_at(al, p.alpha, b * p.lda + ch, n);
     if (F == kGiven) load_at(be, p.beta, b * p.ldb + ch, n);
     load_at(S, p.ST, b * p.D + ch, n);
-    gates<F, LOG, GB, V>(al, be, a, u);
+    gates<F, LOG, GB>(al, be, a, u);
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[v], S.get(v), u[v] * x.get(v));
 #pragma unroll
@@ -105,12 +104,11 @@ hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s)
 }
 
 hipError_t launch_scan_step(const ScanParams &p, hipStream_t s) {
-    const Pick k = pick<Step>(p);
-    const long threads = (long)p.B * ((p.D + k.V - 1) / k.V);
+    const long threads = (long)p.B * ((p.D + V - 1) / V);
     if ((threads + 255) / 256 > 0x7fffffffL) return hipErrorInvalidValue;
     ScanParams q = p;
     void *args[] = {&q};
-    return hipLaunchKernel(k.fn, dim3((unsigned)((threads + 255) / 256)), dim3(256), args, 0, s);
+    return hipLaunchKernel(pick<Step>(p), dim3((unsigned)((threads + 255) / 256)), dim3(256), args, 0, s);
 }
 
 }  // namespace gdr

@@ -5,10 +5,9 @@ namespace gdr {
 namespace {
 
 template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
-__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(ScanParams p) {
-    typedef Shape<IOB, GB> Sh;
-    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH, kLR = Sh::LR, kWS = Sh::WS, LB = F == kGiven ? L : 1;
-    __shared__ Shared<Sh> sh, sg;
+__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
+    constexpr int LB = F == kGiven ? L : 1;
+    __shared__ Shared sh, sg;
     __shared__ int ticket;
     const int waves = blockDim.x >> 6;
     const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
@@ -21,13 +20,13 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
     const int rows = min(kBlk, p.T - (int)k * kBlk);  // of this block
     const int64_t row = (int64_t)b * p.T + k * kBlk;  // its first
     const unsigned there = rows >= local + L ? (1u << L) - 1 : rows > local ? (1u << (rows - local)) - 1 : 0;
-    Pack<IOB, V> x[L], dy[L];
-    Pack<GB, V> al[L], be[LB];
-    Rows<IOB, V, L>(p.x, row, rows, p.ldx, p.D, local, ch).load(x, whole, n);
-    Rows<GB, V, L>(p.alpha, row, rows, p.lda, p.D, local, ch).load(al, whole, n);
-    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, rows, p.ldb, p.D, local, ch).load(be, whole, n);
-    Rows<IOB, V, L>(p.dy, row, rows, p.D, p.D, local, ch).load(dy, whole, n);
-    Marks<PACKED, L> m;
+    Pack<IOB> x[L], dy[L];
+    Pack<GB> al[L], be[LB];
+    Rows<IOB>(p.x, row, rows, p.ldx, p.D, local, ch).load(x, whole, n);
+    Rows<GB>(p.alpha, row, rows, p.lda, p.D, local, ch).load(al, whole, n);
+    if constexpr (F == kGiven) Rows<GB>(p.beta, row, rows, p.ldb, p.D, local, ch).load(be, whole, n);
+    Rows<IOB>(p.dy, row, rows, p.D, p.D, local, ch).load(dy, whole, n);
+    Marks<PACKED> m;
     m.find(p, t0, there);
     const States S0(p.S0, PACKED ? p.nseq : p.B, p.D, ch), dST(p.dST, PACKED ? p.nseq : p.B, p.D, ch), dS0(p.dS0, PACKED ? p.nseq : p.B, p.D, ch);
     if (PACKED && p.dS0 && k == 0) {
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
     }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        gates<F, LOG, GB, V>(al[j], be[j % LB], a[j], bb[j]);
+        gates<F, LOG, GB>(al[j], be[j % LB], a[j], bb[j]);
         const bool first = PACKED && (m.first >> j & 1);
         if (first) S0.load(m.seq[j], U);
 #pragma unroll
@@ -73,25 +72,19 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
         }
     }
     bool cut = m.first != 0, gcut = m.last != 0;
-    compose<V, false, PACKED>(sh, A, U, cut);
-    compose<V, true, PACKED>(sg, GA, GU, gcut);
+    compose<false, PACKED>(sh, A, U, cut);
+    compose<true, PACKED>(sg, GA, GU, gcut);
     __syncthreads();
     {
         // one wave joins the chain of gradients while another one takes the kept state into the block
         const int c = threadIdx.x & 63, cc = tile * CH + c, wave = threadIdx.x >> 6;
-        if (wave == 0 && c < CH) {
-            const Chain<CH> chain(p, column, columns);
-            uint32_t ba;
-            float bu, in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f;
-            block_map<true, PACKED>(sg, waves, c, ba, bu);
-            if (step > 0) {
-                if (step < p.nblk - 1) chain.put_map(step, c, ba, bu);
-                in = chain.enter(step, c);
-            }
-            if (step < p.nblk - 1) chain.put_state(step, c, apply(ba, bu, in));
+        if (wave == 0) {
+            const Map own = block_map<true, PACKED>(sg, waves, c);
+            float in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f, out;
+            if (p.nblk > 1) in = Chain(p, column, c).join(step, own, in, out);
             wave_states<true, PACKED>(sg, waves, c, in);
         }
-        if (wave == (waves > 1 ? 1 : 0) && c < CH) {
+        if (wave == (waves > 1 ? 1 : 0)) {
             float in = 0.f;
             if (cc < p.D) {
                 if (k > 0) in = p.ckpt[((int64_t)b * p.nblk + k - 1) * p.D + cc];
@@ -101,8 +94,8 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
         }
     }
     __syncthreads();
-    strand_states<V, false, PACKED>(sh, A, U, cut, h);
-    strand_states<V, true, PACKED>(sg, GA, GU, gcut, G);
+    strand_states<false, PACKED>(sh, A, U, cut, h);
+    strand_states<true, PACKED>(sg, GA, GU, gcut, G);
     // two channels at a time: the states before each token, then the gradients from the last token back
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
@@ -135,9 +128,9 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_bwd_kernel(Sca
             if (F == kGiven) be[j % LB].set2(v, db[0], db[1]);
         }
     }
-    Rows<IOB, V, L>(p.dx, row, rows, p.D, p.D, local, ch).store(dy, m.in, whole, n);
-    Rows<GB, V, L>(p.dalpha, row, rows, p.D, p.D, local, ch).store(al, m.in, whole, n);
-    if constexpr (F == kGiven) Rows<GB, V, LB>(p.dbeta, row, rows, p.D, p.D, local, ch).store(be, m.in, whole, n);
+    Rows<IOB>(p.dx, row, rows, p.D, p.D, local, ch).store(dy, m.in, whole, n);
+    Rows<GB>(p.dalpha, row, rows, p.D, p.D, local, ch).store(al, m.in, whole, n);
+    if constexpr (F == kGiven) Rows<GB>(p.dbeta, row, rows, p.D, p.D, local, ch).store(be, m.in, whole, n);
     if (!PACKED && strand == 0 && k == 0) dS0.store(b, n, G);
 }
 

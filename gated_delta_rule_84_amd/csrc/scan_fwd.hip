@@ -5,10 +5,9 @@ namespace gdr {
 namespace {
 
 template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
-__global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(ScanParams p) {
-    typedef Shape<IOB, GB> Sh;
-    constexpr int V = Sh::V, L = Sh::L, CH = Sh::CH, kLR = Sh::LR, kWS = Sh::WS, LB = F == kGiven ? L : 1;
-    __shared__ Shared<Sh> sh;
+__global__ void __launch_bounds__(kThreads, 4) scan_fwd_kernel(ScanParams p) {
+    constexpr int LB = F == kGiven ? L : 1;
+    __shared__ Shared sh;
     __shared__ int ticket;
     const int waves = blockDim.x >> 6;
     const unsigned tiles = (p.D + CH - 1) / CH, columns = p.B * tiles, id = place(p, ticket);
@@ -20,12 +19,12 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
     const int rows = min(kBlk, p.T - (int)k * kBlk);  // of this block
     const int64_t row = (int64_t)b * p.T + k * kBlk;  // its first
     const unsigned there = rows >= local + L ? (1u << L) - 1 : rows > local ? (1u << (rows - local)) - 1 : 0;
-    Pack<IOB, V> x[L];
-    Pack<GB, V> al[L], be[LB];
-    Rows<IOB, V, L>(p.x, row, rows, p.ldx, p.D, local, ch).load(x, whole, n);
-    Rows<GB, V, L>(p.alpha, row, rows, p.lda, p.D, local, ch).load(al, whole, n);
-    if constexpr (F == kGiven) Rows<GB, V, LB>(p.beta, row, rows, p.ldb, p.D, local, ch).load(be, whole, n);
-    Marks<PACKED, L> m;
+    Pack<IOB> x[L];
+    Pack<GB> al[L], be[LB];
+    Rows<IOB>(p.x, row, rows, p.ldx, p.D, local, ch).load(x, whole, n);
+    Rows<GB>(p.alpha, row, rows, p.lda, p.D, local, ch).load(al, whole, n);
+    if constexpr (F == kGiven) Rows<GB>(p.beta, row, rows, p.ldb, p.D, local, ch).load(be, whole, n);
+    Marks<PACKED> m;
     m.find(p, t0, there);
     const States S0(p.S0, PACKED ? p.nseq : p.B, p.D, ch), ST(p.ST, PACKED ? p.nseq : p.B, p.D, ch);
     if (PACKED && p.ST && k == 0) {  // empty sequences end as they begin
@@ -45,7 +44,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
     }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        gates<F, LOG, GB, V>(al[j], be[j % LB], a[j], u[j]);
+        gates<F, LOG, GB>(al[j], be[j % LB], a[j], u[j]);
         const bool first = PACKED && (m.first >> j & 1);
         if (first) S0.load(m.seq[j], U);
 #pragma unroll
@@ -58,25 +57,18 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
         __builtin_amdgcn_sched_barrier(0);  // a token at a time, or the exponentials of all are in flight at once
     }
     bool cut = m.first != 0;
-    compose<V, false, PACKED>(sh, A, U, cut);
+    compose<false, PACKED>(sh, A, U, cut);
     __syncthreads();
     if (threadIdx.x < CH) {
         const int c = threadIdx.x, cc = tile * CH + c;
-        const Chain<CH> chain(p, column, columns);
-        uint32_t ba;
-        float bu, in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f;
-        block_map<false, PACKED>(sh, waves, c, ba, bu);
-        if (k > 0) {
-            if (k < p.nblk - 1) chain.put_map(k, c, ba, bu);
-            in = chain.enter(k, c);
-        }
-        const float out = apply(ba, bu, in);
-        if (k < p.nblk - 1) chain.put_state(k, c, out);
+        const Map own = block_map<false, PACKED>(sh, waves, c);
+        float in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f, out = own.apply(in);
+        if (p.nblk > 1) in = Chain(p, column, c).join(k, own, in, out);
         wave_states<false, PACKED>(sh, waves, c, in);
         if (p.ckpt && cc < p.D) p.ckpt[((int64_t)b * p.nblk + k) * p.D + cc] = out;
     }
     __syncthreads();
-    strand_states<V, false, PACKED>(sh, A, U, cut, h);
+    strand_states<false, PACKED>(sh, A, U, cut, h);
 #pragma unroll
     for (int j = 0; j < L; ++j) {
         if (PACKED && (m.first >> j & 1)) S0.load(m.seq[j], h);
@@ -86,7 +78,7 @@ __global__ void __launch_bounds__((Shape<IOB, GB>::threads)) scan_fwd_kernel(Sca
         for (int v = 0; v < V; v += 2) x[j].set2(v, h[v], h[v + 1]);
         if (PACKED && (m.last >> j & 1)) ST.store(m.seq[j], n, h);
     }
-    Rows<IOB, V, L>(p.y, row, rows, p.D, p.D, local, ch).store(x, m.in, whole, n);
+    Rows<IOB>(p.y, row, rows, p.D, p.D, local, ch).store(x, m.in, whole, n);
     if (!PACKED && k == p.nblk - 1 && strand == waves * kWS - 1) ST.store(b, n, h);
 }
 
