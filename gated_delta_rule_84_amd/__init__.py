@@ -474,15 +474,16 @@ def gdr_scan_workspace_size(desc: Desc) -> int:
     return int(_lib.gdr_scan_workspace_size(ctypes.byref(desc)))
 
 
-def _check_scan(desc: Desc, rows: int, n_seq, specs) -> None:  # n_seq: None where the rows are not packed
-    io, gt = _io(desc)
-    if io is None or min(desc.B, desc.T, desc.H, desc.dv, int(n_seq or 0)) < 0:
-        return  # the library rejects the descriptor itself
-    D = desc.H * desc.dv
-    blocks = (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK
-    kind = {"io": (rows * D, io), "gate": (rows * D, gt), "state": ((desc.B if n_seq is None else int(n_seq)) * D, torch.float32),
-            "ckpt": (desc.B * blocks * D, torch.float32), "seq_off": (int(n_seq or 0) + 1, torch.int32)}
-    _check_all([(name, t) + kind[what] for name, what, t in specs])
+def _scan_kinds(desc: Desc, rows: int, n_seq):
+    """(count, dtype) of the streams, gates, states, ckpt and offsets; n_seq None where the rows are not packed.
+    None for a descriptor that the library rejects."""
+    io, gt = _TORCH_DTYPE.get(desc.io_dtype), _TORCH_DTYPE.get(desc.gate_dtype)
+    B, T, H, dv, n = desc.B, desc.T, desc.H, desc.dv, 0 if n_seq is None else int(n_seq)
+    if io is None or gt is None or min(B, T, H, dv, n) < 0:
+        return None
+    D, f32 = H * dv, torch.float32
+    return ((rows * D, io), (rows * D, gt), ((B if n_seq is None else n) * D, f32),
+            (B * ((T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK) * D, f32), (n + 1, torch.int32))
 
 
 def _scan_rows(desc: Desc, x, ldx, alpha, lda, beta, ldb):
@@ -492,9 +493,11 @@ def _scan_rows(desc: Desc, x, ldx, alpha, lda, beta, ldb):
 
 def gdr_scan_fwd(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, seq_off, n_seq: int, S0, y, ST, ckpt, workspace,
                  workspace_bytes: int, stream=None) -> int:
-    _check_scan(desc, desc.B * desc.T, n_seq if seq_off is not None else None, [
-        ("x", "io", x), ("alpha", "gate", alpha), ("beta", "gate", beta), ("y", "io", y), ("S0", "state", S0),
-        ("ST", "state", ST), ("ckpt", "ckpt", ckpt), ("seq_off", "seq_off", seq_off)])
+    kinds = _scan_kinds(desc, desc.B * desc.T, None if seq_off is None else n_seq)
+    if kinds is not None:
+        io, gate, state, blocks, offsets = kinds
+        _check_all((("x", x) + io, ("alpha", alpha) + gate, ("beta", beta) + gate, ("y", y) + io, ("S0", S0) + state,
+                    ("ST", ST) + state, ("ckpt", ckpt) + blocks, ("seq_off", seq_off) + offsets))
     _check_workspace(workspace, workspace_bytes)
     return int(_lib.gdr_scan_fwd(ctypes.byref(desc), *_scan_rows(desc, x, ldx, alpha, lda, beta, ldb), _ptr(seq_off),
                                  int(n_seq), _ptr(S0), _ptr(y), _ptr(ST), _ptr(ckpt), _ptr(workspace), int(workspace_bytes),
@@ -503,10 +506,12 @@ def gdr_scan_fwd(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, seq_o
 
 def gdr_scan_bwd(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, seq_off, n_seq: int, S0, ckpt, dy, dST, dx,
                  dalpha, dbeta, dS0, workspace, workspace_bytes: int, stream=None) -> int:
-    _check_scan(desc, desc.B * desc.T, n_seq if seq_off is not None else None, [
-        ("x", "io", x), ("alpha", "gate", alpha), ("beta", "gate", beta), ("dy", "io", dy), ("dx", "io", dx),
-        ("dalpha", "gate", dalpha), ("dbeta", "gate", dbeta), ("S0", "state", S0), ("dST", "state", dST),
-        ("dS0", "state", dS0), ("ckpt", "ckpt", ckpt), ("seq_off", "seq_off", seq_off)])
+    kinds = _scan_kinds(desc, desc.B * desc.T, None if seq_off is None else n_seq)
+    if kinds is not None:
+        io, gate, state, blocks, offsets = kinds
+        _check_all((("x", x) + io, ("alpha", alpha) + gate, ("beta", beta) + gate, ("dy", dy) + io, ("dx", dx) + io,
+                    ("dalpha", dalpha) + gate, ("dbeta", dbeta) + gate, ("S0", S0) + state, ("dST", dST) + state,
+                    ("dS0", dS0) + state, ("ckpt", ckpt) + blocks, ("seq_off", seq_off) + offsets))
     _check_workspace(workspace, workspace_bytes)
     return int(_lib.gdr_scan_bwd(ctypes.byref(desc), *_scan_rows(desc, x, ldx, alpha, lda, beta, ldb), _ptr(seq_off),
                                  int(n_seq), _ptr(S0), _ptr(ckpt), _ptr(dy), _ptr(dST), _ptr(dx), _ptr(dalpha), _ptr(dbeta),
@@ -514,8 +519,10 @@ def gdr_scan_bwd(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, seq_o
 
 
 def gdr_scan_step(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, S, y, stream=None) -> int:
-    _check_scan(desc, desc.B, None, [("x", "io", x), ("alpha", "gate", alpha), ("beta", "gate", beta), ("y", "io", y),
-                                  ("S", "state", S)])
+    kinds = _scan_kinds(desc, desc.B, None)
+    if kinds is not None:
+        io, gate, state = kinds[:3]
+        _check_all((("x", x) + io, ("alpha", alpha) + gate, ("beta", beta) + gate, ("y", y) + io, ("S", S) + state))
     return int(_lib.gdr_scan_step(ctypes.byref(desc), *_scan_rows(desc, x, ldx, alpha, lda, beta, ldb), _ptr(S), _ptr(y),
                                   _stream(stream)))
 
@@ -718,17 +725,17 @@ def _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale) -> Q
         raise ValueError(f"norm must be None, 'none', 'l2' or 'rms', got {norm!r}")
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3] or q.dtype != k.dtype:
+    qs, ks = tuple(q.shape), tuple(k.shape)
+    if len(qs) != 4 or len(ks) != 4 or qs[:2] != ks[:2] or qs[3] != ks[3] or q.dtype != k.dtype:
         raise ValueError(f"expected q [B, T, Hq, d] and k [B, T, Hk, d] of one type, got {tuple(q.shape)} {q.dtype} and "
                          f"{tuple(k.shape)} {k.dtype}")
     if wq is not None and wk is not None and wq.dtype != wk.dtype:
         raise ValueError(f"wq and wk must have one type, got {wq.dtype} and {wk.dtype}")
-    B, T, Hq, d = q.shape
-    Hk = k.shape[2]
+    (B, T, Hq, d), Hk = qs, ks[2]
     w = wq if wq is not None else wk
     return QkDesc(B, T, Hq, Hk, d, _dtype_code(q), GDR_F32 if w is None else _dtype_code(w), _NORMS[norm], _LAYOUTS[layout],
                   0 if inv_freq is None else 2 * inv_freq.numel(), eps, q_scale, rot_scale,
-                  _row_stride("q", q, Hq * d) if q.numel() else 0, _row_stride("k", k, Hk * d) if k.numel() else 0)
+                  0 if q.is_contiguous() else _row_stride("q", q, Hq * d), 0 if k.is_contiguous() else _row_stride("k", k, Hk * d))
 
 
 def qk_prep(q, k, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv_freq=None, layout="half", rot_scale=1.0,
@@ -753,7 +760,7 @@ def qk_prep_bwd(q, k, dq_out, dk_out, *, norm="rms", wq=None, wk=None, eps=1e-6,
     Returns (dq, dk, dwq, dwk): dense gradients in q's type, weight gradients [d] in fp32 or None."""
     desc = _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale)
     dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
-    dwq, dwk = (None if w is None else torch.empty(desc.d, dtype=torch.float32, device=q.device) for w in (wq, wk))
+    dwq, dwk = (None if w is None else w.new_empty(w.shape, dtype=torch.float32) for w in (wq, wk))
     if dwq is not None or dwk is not None:
         workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device)
     rc = gdr_qk_prep_bwd(desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
@@ -773,18 +780,19 @@ def _room(workspace, need: int, device):
 
 
 def _scan_desc(x, alpha, log_gate, coupled, step=False) -> Desc:
-    if x.dim() != (3 if step else 4) or alpha.shape != x.shape:
+    shape = tuple(x.shape)
+    if len(shape) != (3 if step else 4) or tuple(alpha.shape) != shape:
         raise ValueError(f"expected x and alpha [B, {'' if step else 'T, '}H, dv], got {tuple(x.shape)} and {tuple(alpha.shape)}")
-    H, dv = x.shape[-2:]
+    H, dv = shape[-2:]
     flags = (GDR_FLAG_LOG_GATE if log_gate else 0) | (GDR_FLAG_COUPLED if coupled else 0)
-    return Desc(x.shape[0], 1 if step else x.shape[1], H, 1, dv, 64, _dtype_code(x), _dtype_code(alpha), GDR_ALPHA_CHANNEL, 0,
+    return Desc(shape[0], 1 if step else shape[1], H, 1, dv, 64, _dtype_code(x), _dtype_code(alpha), GDR_ALPHA_CHANNEL, 0,
                 flags)
 
 
 def _strides(desc: Desc, x, alpha, beta):
     D = desc.H * desc.dv
-    return tuple(0 if t is None or not t.numel() else _row_stride(n, t, D) for n, t in
-                 (("x", x), ("alpha", alpha), ("beta", beta)))
+    return (0 if x.is_contiguous() else _row_stride("x", x, D), 0 if alpha.is_contiguous() else _row_stride("alpha", alpha, D),
+            0 if beta is None or beta.is_contiguous() else _row_stride("beta", beta, D))
 
 
 def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq_offsets=None, want_state=True,
@@ -799,8 +807,8 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
     n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
     H, dv, dev = desc.H, desc.dv, x.device
     y = x.new_empty(x.shape)
-    ST = torch.empty((desc.B if seq_offsets is None else n_seq, H, dv), dtype=torch.float32, device=dev) if want_state else None
-    ckpt = (torch.empty((desc.B, (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK, H, dv), dtype=torch.float32, device=dev)
+    ST = x.new_empty((desc.B if seq_offsets is None else n_seq, H, dv), dtype=torch.float32) if want_state else None
+    ckpt = (x.new_empty((desc.B, (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK, H, dv), dtype=torch.float32)
             if want_ckpt else None)
     workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
@@ -820,7 +828,7 @@ def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0
     dev = x.device
     dx, dalpha = x.new_empty(x.shape), alpha.new_empty(x.shape)
     dbeta = None if beta is None else alpha.new_empty(x.shape)
-    dS0 = torch.empty((desc.B if seq_offsets is None else n_seq, desc.H, desc.dv), dtype=torch.float32, device=dev)
+    dS0 = x.new_empty((desc.B if seq_offsets is None else n_seq, desc.H, desc.dv), dtype=torch.float32)
     workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
     rc = gdr_scan_bwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, ckpt, dy, dST, dx, dalpha, dbeta, dS0,
