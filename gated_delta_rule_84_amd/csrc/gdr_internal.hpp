@@ -120,6 +120,7 @@ struct ScanParams {
 size_t qk_prep_bwd_workspace(const QkParams &p);
 hipError_t launch_qk_prep(const QkParams &p, bool bwd, hipStream_t s);
 size_t scan_workspace(const ScanParams &p);
+long scan_blocks(const ScanParams &p);  // workgroups of a pass
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t s);
 hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s);  // src NULL: zeros

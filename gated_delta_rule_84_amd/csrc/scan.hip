@@ -96,6 +96,8 @@ struct Step {
 
 size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p); }
 
+long scan_blocks(const ScanParams &p) { return columns_of(p) * p.nblk; }
+
 hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s) {
     if (!dst || n == 0 || src == dst) return hipSuccess;
     void *args[] = {&src, &dst, &n};

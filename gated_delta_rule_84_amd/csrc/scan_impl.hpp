@@ -519,8 +519,7 @@ __global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
 template <class K>
 hipError_t launch_blocks(const ScanParams &p, hipStream_t s) {
     const int strands = ((p.T < kBlk ? p.T : kBlk) + L - 1) / L, waves = (strands + kWS - 1) / kWS;
-    const long blocks = columns_of(p) * p.nblk;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    const long blocks = columns_of(p) * p.nblk;  // fits 31 bits: the host has checked
     if (p.nblk > 1) {
         u32x4 *ws = static_cast<u32x4 *>(p.ws);
         long n = chain_bytes(p) / 16;

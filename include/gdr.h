@@ -456,7 +456,7 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *   seq_off    NULL, or [n_seq + 1] int32 on the device with B == 1: sequence i is the rows
  *              seq_off[i] .. seq_off[i + 1] - 1 of the T packed ones.  The offsets must not
  *              decrease and lie in 0 .. T; a sequence may be empty; rows before the first
- *              and behind the last one are neither read nor written.  Offsets that break
+ *              and behind the last one are left as they were, and what they hold does not matter.  Offsets that break
  *              this give undefined values in y and the states, and no access outside the
  *              tensors.  n_seq is 0 with a NULL seq_off.
  *   S0, ST     [B, H, dv] fp32 ([n_seq, H, dv] when packed): state before and after each
@@ -471,6 +471,7 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *              serves one call at a time: calls, or graphs, that may run at the same time
  *              need one each.
  * Pointers need their element's alignment only.  Outputs overlap no input and no other output.
+ * Results are deterministic.
  */
 #define GDR_SCAN_BLOCK 256
 size_t gdr_scan_workspace_size(const gdr_desc *desc);

@@ -110,6 +110,8 @@ CASES = [
     (2, 1100, 2, 36, "bf16", "f32", "log", "coupled", False),
     (1, 6000, 1, 9, "f32", "f32", "log", "one", True),
     (40, 520, 1, 5, "bf16", "bf16", "log", "beta", False),
+    (1, 2049, 1, 66, "bf16", "f32", "value", "one", False),                # a token more than a group of blocks
+    (2, 4096, 1, 3, "f32", "bf16", "log", "coupled", True),
 ]
 
 
@@ -137,6 +139,8 @@ PACKED = [
         reason="ended with a memory fault in a form of the row accesses that has been replaced since; the cause was not "
                "found, so the case stays off the GPU (the kernels' accesses for it were checked on the CPU)")),
     (1500, [0, 0, 0, 0], 12, "bf16", "f32", "log", "beta"),                # nothing but empty sequences
+    (5000, [5, 300, 300, 4700, 4990], 66, "bf16", "f32", "log", "coupled"),  # groups of blocks with and without a border
+    (4700, [2100, 2110, 4650], 20, "bf16", "bf16", "value", "one"),
 ]
 
 
