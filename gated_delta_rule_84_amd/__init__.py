@@ -762,7 +762,7 @@ def qk_prep_bwd(q, k, dq_out, dk_out, *, norm="rms", wq=None, wk=None, eps=1e-6,
     dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
     dwq, dwk = (None if w is None else w.new_empty(w.shape, dtype=torch.float32) for w in (wq, wk))
     if dwq is not None or dwk is not None:
-        workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device)
+        workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device, stream)
     rc = gdr_qk_prep_bwd(desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                          _nbytes(workspace), stream)
     if rc != GDR_OK:
@@ -774,9 +774,17 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _room(workspace, need: int, device):
-    """`workspace` where it holds `need` bytes, else a new one (None for 0)."""
-    return torch.empty(need, dtype=torch.uint8, device=device) if need and _nbytes(workspace) < need else workspace
+def _room(workspace, need: int, device, stream):
+    """`workspace` where it holds `need` bytes, else a new one (None for 0), whose memory is not given to other work
+    before what `stream` does with it is done."""
+    if not need or _nbytes(workspace) >= need:
+        return workspace
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        workspace.record_stream(stream)
+    return workspace
 
 
 def _scan_desc(x, alpha, log_gate, coupled, step=False) -> Desc:
@@ -810,7 +818,7 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
     ST = x.new_empty((desc.B if seq_offsets is None else n_seq, H, dv), dtype=torch.float32) if want_state else None
     ckpt = (x.new_empty((desc.B, (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK, H, dv), dtype=torch.float32)
             if want_ckpt else None)
-    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
+    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev, stream)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
     rc = gdr_scan_fwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, y, ST, ckpt, workspace, _nbytes(workspace),
                       stream)
@@ -829,7 +837,7 @@ def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0
     dx, dalpha = x.new_empty(x.shape), alpha.new_empty(x.shape)
     dbeta = None if beta is None else alpha.new_empty(x.shape)
     dS0 = x.new_empty((desc.B if seq_offsets is None else n_seq, desc.H, desc.dv), dtype=torch.float32)
-    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
+    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev, stream)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
     rc = gdr_scan_bwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, ckpt, dy, dST, dx, dalpha, dbeta, dS0,
                       workspace, _nbytes(workspace), stream)

@@ -304,6 +304,25 @@ def test_deterministic_captured_and_side_by_side():
         x.copy_(torch.randn(x.shape, device="cuda"))
 
 
+def test_workspace_of_a_call_on_another_stream():
+    """The workspace that a wrapper makes for a call on a side stream is not handed to the current stream's
+    allocations while the call runs."""
+    torch, g = gpu()
+    x, alpha, how, dy, dST = _inputs(torch, 33, 1, 20000, 1, 64, "f32", "f32", "value", "one")
+    want = g.scan_fwd(x, alpha, **how)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        for _ in range(5):
+            side.wait_stream(torch.cuda.current_stream())
+            got = g.scan_fwd(x, alpha, stream=handle, **how)
+            desc = g._scan_desc(x, alpha, False, False)
+            for _ in range(4):  # what would take the workspace's place
+                torch.zeros(g.gdr_scan_workspace_size(desc), dtype=torch.uint8, device="cuda")
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_offsets_past_32_bits():
     """2.6 billion elements: the last rows, behind a reset, equal a call on them alone."""
     torch, g = gpu()
