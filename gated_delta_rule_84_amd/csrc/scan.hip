@@ -94,7 +94,8 @@ struct Step {
 
 }  // namespace
 
-size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p); }
+// of either direction: the smallest groups need most
+size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p, kGroupPacked); }
 
 long scan_blocks(const ScanParams &p) { return columns_of(p) * p.nblk; }
 

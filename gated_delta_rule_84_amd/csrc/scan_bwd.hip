@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
         if (wave == 0) {
             const Map own = block_map<true, PACKED>(sg, waves, c);
             float in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f, out;
-            if (p.nblk > 1) in = Chain(p, column, c).join(step, own, in, out);
+            if (p.nblk > 1) in = Chain<kGroupBwd>(p, column, c).join(step, own, in, out);
             wave_states<true, PACKED>(sg, waves, c, in);
         }
         if (wave == (waves > 1 ? 1 : 0)) {
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
 }
 
 struct Bwd {
+    static int group(const ScanParams &) { return kGroupBwd; }
     template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
     static const void *get() { return reinterpret_cast<const void *>(&scan_bwd_kernel<IOB, GB, F, LOG, PACKED>); }
 };

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_fwd_kernel(ScanParams p) {
         const int c = threadIdx.x, cc = tile * CH + c;
         const Map own = block_map<false, PACKED>(sh, waves, c);
         float in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f, out = own.apply(in);
-        if (p.nblk > 1) in = Chain(p, column, c).join(k, own, in, out);
+        if (p.nblk > 1) in = Chain<PACKED ? kGroupPacked : kGroupFwd>(p, column, c).join(k, own, in, out);
         wave_states<false, PACKED>(sh, waves, c, in);
         if (p.ckpt && cc < p.D) p.ckpt[((int64_t)b * p.nblk + k) * p.D + cc] = out;
     }
@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_fwd_kernel(ScanParams p) {
 }
 
 struct Fwd {
+    static int group(const ScanParams &p) { return p.off ? kGroupPacked : kGroupFwd; }
     template <bool IOB, bool GB, int F, bool LOG, bool PACKED>
     static const void *get() { return reinterpret_cast<const void *>(&scan_fwd_kernel<IOB, GB, F, LOG, PACKED>); }
 };

@@ -264,18 +264,23 @@ struct Marks {
 
 // ---------------------------------------------------------------------------
 // The chain of blocks.  Every block publishes its composed map as soon as it has it.  The last block
-// of each group of kGroup composes the group's map from them and publishes that, and the state behind
+// of each group composes the group's map from them and publishes that, and the state behind
 // the group once it is known.  A block takes the state behind the nearest group before it whose state
 // is there, applies the maps of the groups in between and then those of its own group's blocks.  What
 // is applied to what does not depend on which words were there first, so neither do the results.
-// Groups shorten the wait where few channels leave only the chain (16,384 tokens of 512 bf16 channels:
-// 27.4 us without, 21.5 us with them).  Words are stored and loaded whole with relaxed atomics that all eight L2 caches see; a word
-// is there once it is no longer kNone, which no value is stored as, so no order between words matters.
+// Groups shorten the wait where few channels leave only the chain.  Forward, bf16, log gates, in groups
+// of 4 / 6 / 8 blocks: 65,536 tokens of 128 channels 36.6 / 31.2 / 28.7 us, 400,000 of 40 channels
+// 142 / 106 / 89 us, and no difference where the data is what counts.  The backward kernel loses 3 %
+// of its rate on 65,536 x 2,032 with groups of 8 (371 against 358 us), nothing with 6, and the packed
+// forward kernel, whose registers are all in use, spills with more than 4.
+// Words are stored and loaded whole with relaxed atomics that all eight L2 caches see; a word is there
+// once it is no longer kNone, which no value is stored as, so no order between words matters.
 // Blocks are numbered by a counter when they begin: every block before a waiting one is running or
 // done, so each wait ends.
 constexpr uint32_t kNone = 0xffffffffu;  // what scan_fill_kernel leaves
 constexpr uint32_t kCut = 0xfffffffeu;   // in a map's factor: nothing of what enters gets through
-constexpr int kGroup = 4;                // blocks per group
+constexpr int kGroupFwd = 8, kGroupPacked = 4, kGroupBwd = 6;  // blocks per group (kGroupPacked: forward with offsets)
+static_assert(kGroupPacked <= kGroupFwd && kGroupPacked <= kGroupBwd, "scan_workspace takes the smallest");
 constexpr int kWindow = 2;               // groups looked back over at a time
 constexpr int kMaxPolls = 1 << 22;       // some seconds: a bound that a sound run never meets
 
@@ -304,9 +309,10 @@ __device__ __forceinline__ uint64_t look(const uint64_t *p) { return __hip_atomi
 __device__ __forceinline__ uint32_t look(const uint32_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // Words of a chain, for one channel: a map per block, a map and a state per group.
-__host__ __device__ constexpr int groups_of(int nblk) { return (nblk + kGroup - 1) / kGroup; }
-__host__ __device__ constexpr long chain_words(int nblk) { return 2l * nblk + 3l * groups_of(nblk); }
+__host__ __device__ constexpr int groups_of(int nblk, int group) { return (nblk + group - 1) / group; }
+__host__ __device__ constexpr long chain_words(int nblk, int group) { return 2l * nblk + 3l * groups_of(nblk, group); }
 
+template <int GROUP>
 struct Chain {
     uint64_t *map, *gmap;
     uint32_t *gstate;
@@ -314,10 +320,10 @@ struct Chain {
 
     // the words of one column (sequence and tile of channels), the lane's channel c
     __device__ __forceinline__ Chain(const ScanParams &p, unsigned column, int c) : nblk(p.nblk) {
-        char *ws = static_cast<char *>(p.ws) + kChainHead + column * (chain_words(nblk) * CH * 4);
+        char *ws = static_cast<char *>(p.ws) + kChainHead + column * (chain_words(nblk, GROUP) * CH * 4);
         map = reinterpret_cast<uint64_t *>(ws) + c;
         gmap = map + (long)nblk * CH;
-        gstate = reinterpret_cast<uint32_t *>(ws + 8l * (nblk + groups_of(nblk)) * CH) + c;
+        gstate = reinterpret_cast<uint32_t *>(ws + 8l * (nblk + groups_of(nblk, GROUP)) * CH) + c;
     }
     // The state behind group g - 1 (g > 0; group 0 gives its state without a map).
     __device__ __forceinline__ float group_enters(int g) const {
@@ -358,23 +364,23 @@ struct Chain {
     // Joins block k, whose map is `own`, `start` being the state before block 0: the state that
     // enters the block, and in `out` the one behind it.
     __device__ __forceinline__ float join(int k, const Map &own, float start, float &out) const {
-        const int g = k / kGroup, r = k % kGroup;
-        const bool closes = r == kGroup - 1 && k < nblk - 1;  // the last group's state enters nothing
-        if (r < kGroup - 1 && k < nblk - 1) put(map + (long)k * CH, own.bits());
-        uint64_t m[kGroup - 1];  // of the group's blocks before this one
+        const int g = k / GROUP, r = k % GROUP;
+        const bool closes = r == GROUP - 1 && k < nblk - 1;  // the last group's state enters nothing
+        if (r < GROUP - 1 && k < nblk - 1) put(map + (long)k * CH, own.bits());
+        uint64_t m[GROUP - 1];  // of the group's blocks before this one
         bool there = false;
         for (int poll = 0; !there && poll < kMaxPolls; ++poll) {
             there = true;
 #pragma unroll
-            for (int i = 0; i < kGroup - 1; ++i) m[i] = i < r ? look(map + (long)(g * kGroup + i) * CH) : 0;
+            for (int i = 0; i < GROUP - 1; ++i) m[i] = i < r ? look(map + (long)(g * GROUP + i) * CH) : 0;
 #pragma unroll
-            for (int i = 0; i < kGroup - 1; ++i) there = there && __all((uint32_t)(m[i] >> 32) != kNone);
+            for (int i = 0; i < GROUP - 1; ++i) there = there && __all((uint32_t)(m[i] >> 32) != kNone);
         }
         Map all = {0, 0.f};
         if (closes) {
             all = Map::of(m[0]);
 #pragma unroll
-            for (int i = 1; i < kGroup - 1; ++i) all = all.then(Map::of(m[i]));
+            for (int i = 1; i < GROUP - 1; ++i) all = all.then(Map::of(m[i]));
             all = all.then(own);
             if (g > 0) put(gmap + (long)g * CH, all.bits());
         }
@@ -382,7 +388,7 @@ struct Chain {
         const float behind = all.apply(h);
         if (closes) put(gstate + (long)g * CH, word(behind));
 #pragma unroll
-        for (int i = 0; i < kGroup - 1; ++i)
+        for (int i = 0; i < GROUP - 1; ++i)
             if (i < r) h = Map::of(m[i]).apply(h);
         if (!there) h = __uint_as_float(0x7fc00000u);
         out = closes ? behind : own.apply(h);
@@ -505,8 +511,8 @@ const void *pick(const ScanParams &p) {
 
 // Columns of a call (sequences times tiles of channels) and the bytes of their chains.
 inline long columns_of(const ScanParams &p) { return (long)p.B * ((p.D + CH - 1) / CH); }
-inline long chain_bytes(const ScanParams &p) {
-    return p.nblk <= 1 ? 0 : kChainHead + columns_of(p) * chain_words(p.nblk) * CH * 4;
+inline long chain_bytes(const ScanParams &p, int group) {
+    return p.nblk <= 1 ? 0 : kChainHead + columns_of(p) * chain_words(p.nblk, group) * CH * 4;
 }
 
 // Every word of the chain to kNone (a kernel, so that a captured graph replays it).
@@ -522,7 +528,7 @@ hipError_t launch_blocks(const ScanParams &p, hipStream_t s) {
     const long blocks = columns_of(p) * p.nblk;  // fits 31 bits: the host has checked
     if (p.nblk > 1) {
         u32x4 *ws = static_cast<u32x4 *>(p.ws);
-        long n = chain_bytes(p) / 16;
+        long n = chain_bytes(p, K::group(p)) / 16;
         void *args[] = {&ws, &n};
         const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&scan_fill_kernel), dim3((unsigned)((n + 255) / 256)),
                                              dim3(256), args, 0, s);
