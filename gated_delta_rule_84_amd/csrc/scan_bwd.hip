@@ -15,7 +15,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
     const unsigned b = column / tiles, tile = column % tiles;
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const bool whole = (tile + 1) * CH <= (unsigned)p.D;
+    const bool whole = (tile + 1) * CH <= (unsigned)p.D || p.D % V == 0;
     const int local = strand * L, t0 = k * kBlk + local;
     const int rows = min(kBlk, p.T - (int)k * kBlk);  // of this block
     const int64_t row = (int64_t)b * p.T + k * kBlk;  // its first

@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_fwd_kernel(ScanParams p) {
     const unsigned column = id % columns, k = id / columns, b = column / tiles, tile = column % tiles;
     const int lr = threadIdx.x & (kLR - 1), strand = threadIdx.x / kLR;
     const int ch = (tile * kLR + lr) * V, n = max(0, min(V, p.D - ch));
-    const bool whole = (tile + 1) * CH <= (unsigned)p.D;  // every lane's channels are there
+    const bool whole = (tile + 1) * CH <= (unsigned)p.D || p.D % V == 0;  // no lane's channels end inside
     const int local = strand * L, t0 = k * kBlk + local;
     const int rows = min(kBlk, p.T - (int)k * kBlk);  // of this block
     const int64_t row = (int64_t)b * p.T + k * kBlk;  // its first

@@ -199,7 +199,7 @@ __device__ __forceinline__ void leave_out(unsigned in, Pack<IOB> (&x)[L], Pack<G
 }
 
 // The rows of a block of one tensor: from the block's first row to the end of the last one that is
-// there, so rows past T are past the range.  `at` is the byte offset of the lane's first row.
+// there, so rows past T are past the range, and so is a lane whose channels are past D.
 template <bool BF>
 struct Rows {
     static constexpr int es = BF ? 2 : 4;
@@ -207,8 +207,9 @@ struct Rows {
     uint32_t at, step;
     __device__ __forceinline__ Rows(const void *t, int64_t row, int rows, int64_t ld, int D, int local, int ch)
         : r(buf(t, row * ld * es, ((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)D) * es)),
-          at(((uint32_t)local * (uint32_t)ld + (uint32_t)ch) * es), step((uint32_t)ld * es) {}
-    // `whole`: all V channels of every lane are in the row, else n of them
+          at(ch < D ? ((uint32_t)local * (uint32_t)ld + (uint32_t)ch) * es : kNowhere), step((uint32_t)ld * es) {}
+    // `whole`: each lane has all of its V channels in the row or none, else n of them (element by element:
+    // 8 x 1,000 tokens of 1,020 bf16 channels, forward 25.0 us so and 21.4 us whole)
     __device__ __forceinline__ void load(Pack<BF> (&x)[L], bool whole, int n) const {
         if (whole) {
 #pragma unroll
