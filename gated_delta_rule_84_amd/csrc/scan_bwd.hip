@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
         const int c = threadIdx.x & 63, cc = tile * CH + c, wave = threadIdx.x >> 6;
         if (wave == 0) {
             const Map own = block_map<true, PACKED>(sg, waves, c);
-            float in = !PACKED && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f, out;
+            float in = !PACKED && step == 0 && p.dST && cc < p.D ? p.dST[(int64_t)b * p.D + cc] : 0.f, out;
             if (p.nblk > 1) in = Chain<kGroupBwd>(p, column, c).join(step, own, in, out);
             wave_states<true, PACKED>(sg, waves, c, in);
         }

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_fwd_kernel(ScanParams p) {
     if (threadIdx.x < CH) {
         const int c = threadIdx.x, cc = tile * CH + c;
         const Map own = block_map<false, PACKED>(sh, waves, c);
-        float in = !PACKED && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f, out = own.apply(in);
+        float in = !PACKED && k == 0 && p.S0 && cc < p.D ? p.S0[(int64_t)b * p.D + cc] : 0.f, out = own.apply(in);
         if (p.nblk > 1) in = Chain<PACKED ? kGroupPacked : kGroupFwd>(p, column, c).join(k, own, in, out);
         wave_states<false, PACKED>(sh, waves, c, in);
         if (p.ckpt && cc < p.D) p.ckpt[((int64_t)b * p.nblk + k) * p.D + cc] = out;

@@ -362,9 +362,12 @@ struct Chain {
         }
         return __uint_as_float(0x7fc00000u);
     }
-    // Joins block k, whose map is `own`, `start` being the state before block 0: the state that
-    // enters the block, and in `out` the one behind it.
-    __device__ __forceinline__ float join(int k, const Map &own, float start, float &out) const {
+    // Joins block k, whose map is `own`, `start` being the state before block 0 (read for k = 0 only):
+    // the state that enters the block, and in `out` the one behind it.  Block 0 publishes the state behind
+    // it as a map that lets nothing through, so no other block reads S0, which the last block's ST may be:
+    // that block begins to store once it has block 0's word, and block 0 has it only from S0.
+    __device__ __forceinline__ float join(int k, const Map &block, float start, float &out) const {
+        const Map own = k == 0 ? Map{kCut, block.apply(start)} : block;
         const int g = k / GROUP, r = k % GROUP;
         const bool closes = r == GROUP - 1 && k < nblk - 1;  // the last group's state enters nothing
         if (r < GROUP - 1 && k < nblk - 1) put(map + (long)k * CH, own.bits());

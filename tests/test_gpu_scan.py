@@ -268,6 +268,22 @@ def test_resume_in_place_and_empty():
     assert g.scan_fwd(x[:1], alpha[:1], seq_offsets=off)[1].shape == (0, 2, 10)
 
 
+@pytest.mark.parametrize("B,T,H,dv", [(1, 257, 1, 4), (3, 1800, 1, 130), (1, 9000, 2, 33), (64, 520, 1, 64)])
+def test_resume_in_place_over_many_blocks(B, T, H, dv):
+    """ST over S0: the block that writes it is the last, and no block may read S0 after that."""
+    torch, g = gpu()
+    log(f"[scan in place] {B} {T} {H} {dv}")
+    x, alpha, how, _, _ = _inputs(torch, 33, B, T, H, dv, "bf16", "f32", "log", "coupled")
+    y, ST, _ = g.scan_fwd(x, alpha, **how)
+    desc = g._scan_desc(x, alpha, True, True)
+    need = g.gdr_scan_workspace_size(desc)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        S, o = how["S0"].clone(), torch.empty_like(x)
+        assert g.gdr_scan_fwd(desc, x, 0, alpha, 0, None, 0, None, 0, S, o, S, None, ws, need) == g.GDR_OK
+        assert torch.equal(o, y) and torch.equal(S, ST)
+
+
 def test_deterministic_captured_and_side_by_side():
     """The same bits every time: eager, replayed from a graph with other calls between the replays, and on two
     streams at once with a workspace each."""
