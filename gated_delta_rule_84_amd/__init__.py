@@ -706,8 +706,8 @@ def rope_inv_freq(rot_dim, *, base=10000.0, scaling=None, factor=1.0, original_l
     if scaling == "linear":
         f = f / factor
     elif scaling == "yarn":
-        if original_len is None or not original_len > 0 or not fast > slow > 0:
-            raise ValueError("yarn needs original_len > 0 and fast > slow > 0")
+        if original_len is None or not original_len > 0 or not fast > slow > 0 or not base > 1:
+            raise ValueError("yarn needs original_len > 0, fast > slow > 0 and base > 1")
         # the (real) channel index whose frequency turns n times over original_len
         at = lambda n: rot_dim * math.log(original_len / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
         lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot_dim - 1)

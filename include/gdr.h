@@ -383,7 +383,9 @@ int gdr_dmem_fwd(const gdr_desc *desc, int32_t J, const void *q, const void *k, 
  *     (e, o) -> rot_scale (cos e - sin o, sin e + cos o)
  * with e, o the channels (i, i + rot_dim / 2) for GDR_ROT_HALF and (2i, 2i + 1) for
  * GDR_ROT_INTERLEAVED; the channels from rot_dim on are not rotated.  Angles are formed
- * and reduced in 64 bits, so far positions lose nothing.  Frequencies scaled for long
+ * and reduced in 64 bits, so far positions lose nothing.  The sum of squares is formed in
+ * fp32: rows whose sum passes its range give 0, and with eps = 0 rows smaller than about
+ * 1e-18 lose digits (below 1e-23 all of them: 0).  Frequencies scaled for long
  * contexts are the caller's inv_freq and rot_scale.
  */
 typedef enum gdr_norm { GDR_NORM_NONE = 0, GDR_NORM_L2 = 1, GDR_NORM_RMS = 2 } gdr_norm;
@@ -444,7 +446,10 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *     h_t = a_t h_{t-1} + b_t x_t,   y_t = h_t
  *
  * with a = alpha, or exp(alpha) with GDR_FLAG_LOG_GATE, and b = beta where given, 1 - a
- * with GDR_FLAG_COUPLED, else 1.  The sum runs in fp32 whatever the types.
+ * with GDR_FLAG_COUPLED, else 1.  The sum runs in fp32 whatever the types.  Tokens are
+ * joined by their decays' products over stretches of them: where such a product passes
+ * fp32's range (decays above 1), and behind an infinity or NaN, the channel's state up to
+ * the end of its sequence may be NaN where token by token it would be finite or infinite.
  *
  *   desc       B, T, H, dv >= 1 (any), io_dtype (x, y, dy, dx), gate_dtype (alpha, beta and
  *              their gradients), alpha_mode GDR_ALPHA_CHANNEL (else GDR_EUNSUPPORTED),
@@ -457,7 +462,7 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *              seq_off[i] .. seq_off[i + 1] - 1 of the T packed ones.  The offsets must not
  *              decrease and lie in 0 .. T; a sequence may be empty; rows before the first
  *              and behind the last one are left as they were, and what they hold does not matter.  Offsets that break
- *              this give undefined values in y and the states, and no access outside the
+ *              this give undefined values in y, ckpt, the states and the gradients, and no access outside the
  *              tensors.  n_seq is 0 with a NULL seq_off.
  *   S0, ST     [B, H, dv] fp32 ([n_seq, H, dv] when packed): state before and after each
  *              sequence; S0 NULL means zero, ST NULL not written.  ST == S0 is allowed

@@ -6,7 +6,7 @@ about 10 u; cosine and sine are within 4 u of an angle reduced in 64 bits; each 
 rotated pair adds the errors of 5 products and a sum.  40 u of the row's largest normalised
 value, rotated (a factor sqrt 2), covers it; the backward pass has twice the chain, and a sum
 over the row.  A weight gradient's sum runs over at most 8 rows per item and item loop, 6
-steps over a wave, 4 waves, and 1024 / 16 + 16 workgroups."""
+steps over a wave, 4 waves, and up to 768 / 64 + 6 sums of workgroups."""
 import numpy as np
 import pytest
 

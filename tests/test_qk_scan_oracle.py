@@ -120,6 +120,7 @@ def test_rope_inv_freq():
     np.testing.assert_allclose(scale, 0.1 * math.log(8) + 1)
     assert g.rope_inv_freq(0, device="cpu")[0].numel() == 0
     for bad in (dict(rot_dim=3), dict(rot_dim=-2), dict(rot_dim=8, base=0), dict(rot_dim=8, factor=0.5),
-                dict(rot_dim=8, scaling="other"), dict(rot_dim=8, scaling="yarn", factor=2)):
+                dict(rot_dim=8, scaling="other"), dict(rot_dim=8, scaling="yarn", factor=2),
+                dict(rot_dim=8, scaling="yarn", factor=2, original_len=64, base=1.0)):
         with pytest.raises(ValueError):
             g.rope_inv_freq(**bad, device="cpu")
