@@ -11,11 +11,17 @@
 //
 // Bound by HBM (forward 2 and backward 3 passes over the heads, under 10 operations per
 // byte), so the layout serves the loads.  Rotated channels are held as pairs: a lane owns
-// VP consecutive pairs of a row, read as 16-byte vectors from the two places where the
-// pairs' members lie, so the rotation needs no exchange between lanes; P = 2^k lanes hold
-// a row and only the norm's sum crosses lanes (log2 P xor shuffles).  A group of P lanes
-// works on up to `rows` heads of one token, so that the token's cosines and sines, held in
-// registers, are formed once for them.
+// VP = 4 consecutive pairs of a row, read from the two places where the pairs' members lie
+// (8 bytes each of bf16, 16 of fp32; interleaved members in one access of twice that), so the
+// rotation needs no exchange between lanes; P = 2^k lanes hold a row and only the norm's sum
+// crosses lanes (log2 P xor shuffles).  A group of P lanes works on up to 8 heads of one
+// token, each loaded while the one before it is worked on, and the workgroup forms the
+// cosines and sines of its tokens once, in shared memory (each lane its own pairs' before:
+// 5 us of 91 in the backward pass below).
+// 4 x 4,096 tokens of 16 + 16 bf16 heads of 128: forward 44 us (6.1 TB/s), backward 73 to 80 us
+// (5.0 to 5.5 TB/s); 65,536 tokens of 32 + 8 forward 255 us (5.3 TB/s); fp32 4.8 and 7.1 TB/s.
+// 8 tokens of 16 + 16 take 4.5 us, which is a launch and one trip to memory.  Half rotations of
+// rot_dim / 2 not a multiple of 4 take each member by itself and reach 1.9 to 3.2 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -160,32 +166,33 @@ struct Row {
     }
 };
 
+// The weights of a lane's pairs, stored as bf16 (WB) or fp32.
+template <bool WB, int VP, int LAY>
+__device__ __forceinline__ void weights(const void *w, int pair0, int half, float (&we)[VP], float (&wo)[VP]) {
+    Row<WB, VP, LAY> at;
+    Held<WB, VP, LAY> h;
+    at.place(pair0, half);
+    at.load(w, 0, h);
+    at.unpack(h, we, wo);
+}
+
 // sum over the P lanes of a row (P a power of two)
 __device__ __forceinline__ float row_sum(float x, int P) {
     for (int s = 1; s < P; s <<= 1) x += __shfl_xor(x, s);
     return x;
 }
 
-// Cosine and sine of pos * f for the lane's pairs, times rot_scale; pairs past the rotated
-// part get 1 and 0.  The angle is formed and reduced to a fraction of a turn in 64 bits: at
-// position 10^6 its 32-bit product would be off by 0.06.
-template <int VP>
-__device__ __forceinline__ void angles(const QkParams &p, long token, int i0, float (&c)[VP], float (&s)[VP]) {
-    const int half = p.rot / 2;
-    const double pos = p.pos ? (double)p.pos[token] : (double)(token % p.T);
-#pragma unroll
-    for (int j = 0; j < VP; ++j) {
-        c[j] = 1.f;
-        s[j] = 0.f;
-        if (i0 + j < half) {
-            double turn = pos * p.inv_freq[i0 + j] * 0.15915494309189535;
-            turn -= rint(turn);
-            float sn, cs;
-            sincospif(2.f * (float)turn, &sn, &cs);
-            c[j] = cs * p.rot_scale;
-            s[j] = sn * p.rot_scale;
-        }
-    }
+// Cosine and sine of pos * f_i, times rot_scale; pairs past the rotated part get 1 and 0.  The
+// angle is formed and reduced to a fraction of a turn in 64 bits: at position 10^6 its 32-bit
+// product would be off by 0.06.
+__device__ __forceinline__ float2 angle(const QkParams &p, unsigned token, int i) {
+    if (2 * i >= p.rot) return make_float2(1.f, 0.f);
+    const int pos = p.pos ? p.pos[token] : (int)(token % (unsigned)p.T);
+    double turn = (double)pos * p.inv_freq[i] * 0.15915494309189535;
+    turn -= rint(turn);
+    float sn, cs;
+    sincospif(2.f * (float)turn, &sn, &cs);
+    return make_float2(cs * p.rot_scale, sn * p.rot_scale);
 }
 
 // r of one row from its sum of squares (already over the P lanes)
@@ -197,6 +204,7 @@ __device__ __forceinline__ float inverse_norm(const QkParams &p, float ss) {
 
 template <bool BF, int VP, int LAY, bool BWD>
 __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
+    __shared__ float2 turns[kThreads * VP];
     const bool isk = blockIdx.x >= (unsigned)p.blocks_q;
     const QkTensor &X = isk ? p.k : p.q;
     const long block = isk ? (long)blockIdx.x - p.blocks_q : blockIdx.x;
@@ -210,23 +218,40 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
     float we[VP], wo[VP], ae[VP], ao[VP];
 #pragma unroll
     for (int j = 0; j < VP; ++j) {
-        we[j] = X.w ? ld_elem(X.w, at.channel(j, 0), p.w_bf16) : 1.f;
-        wo[j] = X.w ? ld_elem(X.w, at.channel(j, 1), p.w_bf16) : 1.f;
+        we[j] = wo[j] = 1.f;
         ae[j] = ao[j] = 0.f;
     }
+    if (X.w && p.w_bf16) weights<true, VP, LAY>(X.w, holds ? i0 : 0, p.rot / 2, we, wo);
+    else if (X.w) weights<false, VP, LAY>(X.w, holds ? i0 : 0, p.rot / 2, we, wo);
+    const int pairs = P * VP, shift = __ffs(pairs) - 1;
     const long items = p.tokens * X.slices;
-    for (long item = block * groups + gl; item < items; item += nblocks * groups) {
-        const long token = item / X.slices;
-        const int h0 = (int)(item % X.slices) * p.rows, h1 = min(h0 + p.rows, X.H);
+    for (long first = block * groups; first < items; first += nblocks * groups) {
+        // the workgroup's items are slices of a few tokens that follow each other
+        const unsigned token0 = items >> 32 ? (unsigned)(first / X.slices) : (unsigned)first / (unsigned)X.slices;
+        const unsigned at0 = (unsigned)(first - (long)token0 * X.slices), mine = at0 + gl, step = mine / X.slices;
+        const int here = (int)min((long)groups, items - first);
+        const long token = token0 + step;
+        const int h0 = gl < here ? (int)(mine - step * X.slices) * p.rows : X.H, h1 = min(h0 + p.rows, X.H);
         // each row is loaded while the one before it is worked on, the first under the angles
         Held<BF, VP, LAY> next, gnext;
         auto fetch = [&](int h) __attribute__((always_inline)) {
             at.load(X.x, token * X.ld + (long)h * p.d, next);
             if constexpr (BWD) at.load(X.g, (token * X.H + h) * p.d, gnext);
         };
-        fetch(h0);
+        if (h0 < h1) fetch(h0);
+        const int used = ((at0 + here - 1) / X.slices + 1) << shift;  // angles of these tokens, at most kThreads * VP
         float c[VP], s[VP];
-        angles<VP>(p, token, holds ? i0 : p.d, c, s);
+        if (p.rot > 0) {
+            for (int i = threadIdx.x; i < used; i += kThreads) turns[i] = angle(p, token0 + (i >> shift), i & (pairs - 1));
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+            const float2 t = p.rot > 0 ? turns[gl < here ? ((int)step << shift) + i0 + j : 0] : make_float2(1.f, 0.f);
+            c[j] = t.x;
+            s[j] = t.y;
+        }
+        if (first + nblocks * groups < items) __syncthreads();  // before the next angles
         for (int h = h0; h < h1; ++h) {
             const long out = (token * X.H + h) * p.d;
             float e[VP], o[VP], ge[VP], go[VP];
@@ -297,7 +322,8 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
 }
 
 // The workgroups' sums of the weight gradients, always in the same order: 16 channels per
-// block, 4 lanes of 4 channels in 64 rows of threads.
+// block, 4 lanes of 4 channels in 64 rows of threads.  4.6 us for 2 x 768 sums of 128 channels
+// (0.8 MB, in cache: a launch and 12 dependent rows of loads per thread).
 __global__ void __launch_bounds__(256) qk_weight_kernel(QkParams p) {
     __shared__ f32x4 part[64][4];
     const bool isk = blockIdx.y != 0;
