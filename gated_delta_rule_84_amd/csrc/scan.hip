@@ -54,7 +54,9 @@ __device__ __forceinline__ void store_at(const Pack<BF> &x, void *base, int64_t 
     }
 }
 
-// One token for every batch row: the state is read and written in place.
+// One token for every batch row: the state is read and written in place.  512 rows of 2,048 bf16
+// channels with fp32 gates: 4.0 us for 16.8 MB, most of it in cache (4.2 TB/s; a launch alone takes
+// over 2 us).  Each lane has 4 channels of one row, so short calls still spread over the chip.
 template <bool IOB, bool GB, int F, bool LOG>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
     const unsigned groups = (p.D + V - 1) / V;

@@ -1,4 +1,10 @@
 // scan_fwd.hip -- gated linear recurrence: the forward pass (see scan_impl.hpp).
+//
+// Measured, with the fill of the chain: 4 x 4,096 tokens of 2,048 channels, log gates coupled:
+// bf16 48 us (4.1 TB/s), bf16 with fp32 gates 55 us (4.9), fp32 86 us (4.7); 65,536 of 2,032 bf16
+// 204 us (3.9) and fp32 294 us (5.4); 65,536 of 128 bf16 28 us, of which the chain is two thirds.
+// 128 registers (launch bounds of 4 waves per SIMD) keep two workgroups on a compute unit, so that
+// one loads while the other waits for the chain.
 #include "scan_impl.hpp"
 
 namespace gdr {
