@@ -277,9 +277,9 @@ struct Marks {
 // is applied to what does not depend on which words were there first, so neither do the results.
 // Groups shorten the wait where few channels leave only the chain.  Forward, bf16, log gates, in groups
 // of 4 / 6 / 8 blocks: 65,536 tokens of 128 channels 36.6 / 31.2 / 28.7 us, 400,000 of 40 channels
-// 142 / 106 / 89 us, and no difference where the data is what counts.  The backward kernel loses 3 %
-// of its rate on 65,536 x 2,032 with groups of 8 (371 against 358 us), nothing with 6, and the packed
-// forward kernel, whose registers are all in use, spills with more than 4.
+// 142 / 106 / 89 us, against 298 / 298 / 304 us for 65,536 of 4,096, where the data is what counts.
+// The backward kernel loses 3 % of its rate on 65,536 x 2,032 with groups of 8 (371 against 358 us),
+// nothing with 6, and the packed forward kernel, whose registers are all in use, spills with more than 4.
 // Words are stored and loaded whole with relaxed atomics that all eight L2 caches see; a word is there
 // once it is no longer kNone, which no value is stored as, so no order between words matters.
 // Blocks are numbered by a counter when they begin: every block before a waiting one is running or
@@ -379,12 +379,16 @@ struct Chain {
         if (r < GROUP - 1 && k < nblk - 1) put(map + (long)k * CH, own.bits());
         uint64_t m[GROUP - 1];  // of the group's blocks before this one
         bool there = false;
+#pragma unroll
+        for (int i = 0; i < GROUP - 1; ++i) m[i] = i < r ? look(map + (long)(g * GROUP + i) * CH) : 0;
         for (int poll = 0; !there && poll < kMaxPolls; ++poll) {
             there = true;
 #pragma unroll
-            for (int i = 0; i < GROUP - 1; ++i) m[i] = i < r ? look(map + (long)(g * GROUP + i) * CH) : 0;
-#pragma unroll
-            for (int i = 0; i < GROUP - 1; ++i) there = there && __all((uint32_t)(m[i] >> 32) != kNone);
+            for (int i = 0; i < GROUP - 1; ++i) {
+                if (__all((uint32_t)(m[i] >> 32) != kNone)) continue;  // only what is missing is looked for again
+                m[i] = look(map + (long)(g * GROUP + i) * CH);
+                there = false;
+            }
         }
         Map all = {0, 0.f};
         if (closes) {
