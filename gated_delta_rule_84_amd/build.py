@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libgdr.so")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["gdr_api.hip", "decode.hip", "chunk_valu.hip", "chunk_mfma.hip", "mc_readout.hip", "osdn_precond.hip", "sdm.hip", "dmem.hip",
-           "qk_prep.hip", "scan_fwd.hip", "scan_bwd.hip", "scan.hip"]
+           "mixer_api.hip", "qk_prep.hip", "scan_fwd.hip", "scan_bwd.hip", "scan.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

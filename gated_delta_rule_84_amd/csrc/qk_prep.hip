@@ -26,8 +26,8 @@
 #include <stdint.h>
 
 #include "gdr_device.hpp"
-#include "gdr_internal.hpp"
 #include "gdr_mfma.hpp"
+#include "mixer.hpp"
 
 namespace gdr {
 namespace {

@@ -30,8 +30,8 @@
 
 #include "gdr.h"
 #include "gdr_device.hpp"
-#include "gdr_internal.hpp"
 #include "gdr_mfma.hpp"
+#include "mixer.hpp"
 
 namespace gdr {
 namespace {
