@@ -59,6 +59,8 @@ CASES = [
     (2, 8, 2, 2, 24, "f32", None, "none", 6, "interleaved", 50, True),
     (1, 7, 3, 0, 64, "bf16", "f32", "rms", 32, "half", 50, False),      # queries alone
     (1, 2000, 10, 2, 16, "bf16", "f32", "rms", 16, "interleaved", 0, True),
+    (1, 1700, 16, 2, 128, "bf16", "f32", "rms", 64, "half", 5000, True),   # workgroups that come round again
+    (2, 450, 9, 3, 256, "f32", "bf16", "l2", 256, "interleaved", 0, False),
 ]
 
 

@@ -133,6 +133,7 @@ PACKED = [
     (30, [2, 2, 3, 11, 11, 12, 20, 29], 10, "bf16", "f32", "log", "coupled"),
     (1200, [0, 1, 8, 16, 511, 512, 513, 1024, 1024, 1100], 20, "f32", "bf16", "value", "beta"),
     (1100, [5, 600, 600, 1100], 70, "bf16", "bf16", "log", "one"),
+    (1300, [5, 600, 600, 1100, 1290], 76, "bf16", "f32", "value", "beta"),
     (700, list(range(3, 690, 3)), 16, "f32", "f32", "value", "coupled"),   # a sequence every three rows
     # blocks without any
     pytest.param((2600, [1030, 1040], 12, "f32", "f32", "log", "beta"), marks=pytest.mark.skip(
