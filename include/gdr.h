@@ -461,9 +461,10 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *   seq_off    NULL, or [n_seq + 1] int32 on the device with B == 1: sequence i is the rows
  *              seq_off[i] .. seq_off[i + 1] - 1 of the T packed ones.  The offsets must not
  *              decrease and lie in 0 .. T; a sequence may be empty; rows before the first
- *              and behind the last one are left as they were, and what they hold does not matter.  Offsets that break
- *              this give undefined values in y, ckpt, the states and the gradients, and no access outside the
- *              tensors.  n_seq is 0 with a NULL seq_off.
+ *              and behind the last one are left as they were, and what they hold does not
+ *              matter.  Offsets that break this give undefined values in y, ckpt, the states
+ *              and the gradients, and no access outside the tensors.  n_seq is 0 with a NULL
+ *              seq_off.
  *   S0, ST     [B, H, dv] fp32 ([n_seq, H, dv] when packed): state before and after each
  *              sequence; S0 NULL means zero, ST NULL not written.  ST == S0 is allowed
  *              (in-place resume) without seq_off; an empty sequence gives ST = S0.
