@@ -14,6 +14,7 @@ importing this package without it raises ImportError.  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -205,7 +206,11 @@ def _prefill_specs(desc: Desc, q, k, k_w, v, alpha, beta_k, beta_v, S0, o, ST) -
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:  # the current stream's handle without building a Stream object
         return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return ctypes.c_void_p(_handle(stream))
+
+
+def _handle(stream) -> int:
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # ---------------------------------------------------------------------------
@@ -539,6 +544,41 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
 
 
+def _tensors(values):
+    for t in values:
+        if isinstance(t, torch.Tensor):
+            if t.is_cuda:
+                yield t
+        elif isinstance(t, (tuple, list)):
+            yield from _tensors(t)
+
+
+def _on_its_stream(call):
+    """A wrapper called with a `stream` that is not torch's current one runs with it as the current one.  What
+    it allocates then comes from that stream's memory (a block of the current stream's may still be in use by
+    work pending there), and neither what it returns nor what it was given is handed to other work, once
+    dropped, before both streams are done with it.  Waiting for the inputs, and for the results, is the caller's."""
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None or not torch.cuda.is_initialized():  # without a device the call refuses its tensors
+            return call(*args, **kw)
+        handle = _handle(stream)
+        if handle == torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()):
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            out = call(*args, **dict(kw, stream=stream))
+        for t in _tensors((args, tuple(kw.values()))):
+            t.record_stream(stream)
+        for t in _tensors((out,)):
+            t.record_stream(here)
+        return out
+    return run
+
+
 def make_desc(q, v, alpha, beta_k, beta_v=None, *, chunk=64, decode=False, flags=0) -> Desc:
     """Descriptor from tensor shapes: prefill q [B, T, H, dk], decode q [B, H, dk]."""
     if decode:
@@ -738,6 +778,7 @@ def _qk_desc(q, k, norm, wq, wk, eps, inv_freq, layout, rot_scale, q_scale) -> Q
                   0 if q.is_contiguous() else _row_stride("q", q, Hq * d), 0 if k.is_contiguous() else _row_stride("k", k, Hk * d))
 
 
+@_on_its_stream
 def qk_prep(q, k, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv_freq=None, layout="half", rot_scale=1.0,
             q_scale=1.0, out=None, stream=None):
     """Norm of every head of q [B, T, Hq, d] and k [B, T, Hk, d] and the rotation by position, in one pass.
@@ -754,6 +795,7 @@ def qk_prep(q, k, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv
     return qo, ko
 
 
+@_on_its_stream
 def qk_prep_bwd(q, k, dq_out, dk_out, *, norm="rms", wq=None, wk=None, eps=1e-6, positions=None, inv_freq=None,
                 layout="half", rot_scale=1.0, q_scale=1.0, workspace=None, stream=None):
     """Backward pass of qk_prep, from its inputs and the (dense) gradients of its outputs.
@@ -762,7 +804,7 @@ def qk_prep_bwd(q, k, dq_out, dk_out, *, norm="rms", wq=None, wk=None, eps=1e-6,
     dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
     dwq, dwk = (None if w is None else w.new_empty(w.shape, dtype=torch.float32) for w in (wq, wk))
     if dwq is not None or dwk is not None:
-        workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device, stream)
+        workspace = _room(workspace, gdr_qk_prep_bwd_workspace_size(desc), q.device)
     rc = gdr_qk_prep_bwd(desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                          _nbytes(workspace), stream)
     if rc != GDR_OK:
@@ -774,17 +816,11 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _room(workspace, need: int, device, stream):
-    """`workspace` where it holds `need` bytes, else a new one (None for 0), whose memory is not given to other work
-    before what `stream` does with it is done."""
+def _room(workspace, need: int, device):
+    """`workspace` where it holds `need` bytes, else a new one (None for 0)."""
     if not need or _nbytes(workspace) >= need:
         return workspace
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-        workspace.record_stream(stream)
-    return workspace
+    return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def _scan_desc(x, alpha, log_gate, coupled, step=False) -> Desc:
@@ -803,6 +839,7 @@ def _strides(desc: Desc, x, alpha, beta):
             0 if beta is None or beta.is_contiguous() else _row_stride("beta", beta, D))
 
 
+@_on_its_stream
 def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq_offsets=None, want_state=True,
              want_ckpt=False, workspace=None, stream=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + b_t x_t over x [B, T, H, dv], y = h.
@@ -818,7 +855,7 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
     ST = x.new_empty((desc.B if seq_offsets is None else n_seq, H, dv), dtype=torch.float32) if want_state else None
     ckpt = (x.new_empty((desc.B, (desc.T + GDR_SCAN_BLOCK - 1) // GDR_SCAN_BLOCK, H, dv), dtype=torch.float32)
             if want_ckpt else None)
-    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev, stream)
+    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
     rc = gdr_scan_fwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, y, ST, ckpt, workspace, _nbytes(workspace),
                       stream)
@@ -827,6 +864,7 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
     return y, ST, ckpt
 
 
+@_on_its_stream
 def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0=None, dST=None, seq_offsets=None,
              workspace=None, stream=None):
     """Backward pass of scan_fwd with its inputs and its ckpt (None where T <= 256): gradients dy of y (dense) and
@@ -837,7 +875,7 @@ def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0
     dx, dalpha = x.new_empty(x.shape), alpha.new_empty(x.shape)
     dbeta = None if beta is None else alpha.new_empty(x.shape)
     dS0 = x.new_empty((desc.B if seq_offsets is None else n_seq, desc.H, desc.dv), dtype=torch.float32)
-    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev, stream)
+    workspace = _room(workspace, gdr_scan_workspace_size(desc), dev)
     ldx, lda, ldb = _strides(desc, x, alpha, beta)
     rc = gdr_scan_bwd(desc, x, ldx, alpha, lda, beta, ldb, seq_offsets, n_seq, S0, ckpt, dy, dST, dx, dalpha, dbeta, dS0,
                       workspace, _nbytes(workspace), stream)
@@ -846,6 +884,7 @@ def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0
     return dx, dalpha, dbeta, dS0
 
 
+@_on_its_stream
 def scan_step(S, x, alpha, *, beta=None, log_gate=False, coupled=False, out=None, stream=None):
     """One token of the recurrence for every sequence: x, alpha, beta [B, H, dv]; S [B, H, dv] fp32 is updated in
     place.  Returns y [B, H, dv]."""
