@@ -596,6 +596,7 @@ def make_desc(q, v, alpha, beta_k, beta_v=None, *, chunk=64, decode=False, flags
                 beta_mode=beta_mode, flags=flags)
 
 
+@_on_its_stream
 def chunk_fwd(q, k, v, alpha, beta_k, *, k_w=None, beta_v=None, S0=None, chunk=64, want_state=True,
               out=None, final_state=None, workspace=None, ctx=None, stream=None):
     """Prefill.  Returns (o [B, T, H, dv] in q's dtype, ST [B, H, dk, dv] fp32 or None).
@@ -618,6 +619,7 @@ def chunk_fwd(q, k, v, alpha, beta_k, *, k_w=None, beta_v=None, S0=None, chunk=6
     return o, ST
 
 
+@_on_its_stream
 def chunk_fwd_ckpt(q, k, v, alpha, beta_k, seg_len, *, k_w=None, beta_v=None, S0=None, chunk=64,
                    want_state=True, workspace=None, stream=None):
     """Prefill that also keeps the state after every complete segment of seg_len tokens.
@@ -638,6 +640,7 @@ def chunk_fwd_ckpt(q, k, v, alpha, beta_k, seg_len, *, k_w=None, beta_v=None, S0
     return o, ST, ckpt
 
 
+@_on_its_stream
 def mc_readout(q, ckpt, seg_len, *, gates=None, o_in=None, out=None, workspace=None, stream=None):
     """o_out[t] = o_in[t] + sum_{s < min(t // seg_len, N)} g[t, s] M_s^T q[t] (g = 1 without gates).
     q [B, T, H, 128] bf16, ckpt [B, H, N, 128, 128] fp32, gates [B, T, H, N] fp32 or None."""
@@ -656,6 +659,7 @@ def mc_readout(q, ckpt, seg_len, *, gates=None, o_in=None, out=None, workspace=N
     return o
 
 
+@_on_its_stream
 def osdn_precond(k, beta, eta, *, r=None, d0=None, workspace=None, ctx=None, stream=None):
     """OSDN phase 1.  k [B, T, H, dk] (bf16 or fp32), beta and r [B, T, H].
     Returns (k_w like k, dT [B, H, dk] fp32, qgeo [B, H] fp32)."""
@@ -675,6 +679,7 @@ def osdn_precond(k, beta, eta, *, r=None, d0=None, workspace=None, ctx=None, str
     return kw, dT, qg
 
 
+@_on_its_stream
 def sdm_fwd(M, ks, qs, v, alpha, beta, W, R, *, want_slots=False, workspace=None, ctx=None, stream=None):
     """Sparse Delta Memory over T tokens.  M [B, H, n * n, dv] fp32 is updated in place;
     ks, qs [B, T, H, 2, n] fp32; v [B, T, H, dv].  Returns o (and the selected write /
@@ -696,6 +701,7 @@ def sdm_fwd(M, ks, qs, v, alpha, beta, W, R, *, want_slots=False, workspace=None
     return (o, ws_[0], ws_[1]) if want_slots else o
 
 
+@_on_its_stream
 def dmem_fwd(M, q, k, v, lam, beta, *, seg_end=None, J=1, out=None, stream=None):
     """delta-mem context pass: M [B, H, r, r] fp32 is updated in place; q, k, v
     [B, T, H, r]; lam, beta [B, T, H]; seg_end [B, T] uint8 or None (one write per
@@ -710,6 +716,7 @@ def dmem_fwd(M, q, k, v, lam, beta, *, seg_end=None, J=1, out=None, stream=None)
     return o
 
 
+@_on_its_stream
 def decode_step(S, q, k, v, alpha, beta_k, *, k_w=None, beta_v=None, out=None, flags=0, stream=None):
     """One token for every (b, h); S [B, H, dk, dv] fp32 is updated in place.  Returns o [B, H, dv].
     `flags`: GDR_FLAG_READ_BEFORE_WRITE and / or GDR_FLAG_UNDECAYED_PREDICTION."""

@@ -18,7 +18,22 @@ def _calls(torch, g):
     q, k = r(1, 3000, 4, 64), r(1, 3000, 2, 64)
     ckpt = g.scan_fwd(x, gate, want_ckpt=True)[2]
     S = r(512, 2, 64)
+    bf, sig, unit = torch.bfloat16, torch.sigmoid, torch.nn.functional.normalize
+    heads = [unit(r(1, 1024, 2, 128), dim=-1).to(bf) for _ in range(3)]
+    alpha, beta = sig(r(1, 1024, 2) + 4), sig(r(1, 1024, 2))
+    states = g.chunk_fwd_ckpt(*heads, alpha, beta, 256)[2]
+    n, few = 32, [unit(r(64, 50, 2, 8), dim=-1) for _ in range(3)]
     return {
+        "chunk_fwd": (g.chunk_fwd, (*heads, alpha, beta)),
+        "chunk_fwd_ckpt": (lambda *t, **kw: g.chunk_fwd_ckpt(*t, 256, **kw), (*heads, alpha, beta)),
+        "mc_readout": (lambda q, c, **kw: (g.mc_readout(q, c, 256, **kw),), (heads[0], states)),
+        "osdn_precond": (lambda k, b, **kw: g.osdn_precond(k, b, 0.5, **kw), (heads[1], beta)),
+        "sdm_fwd": (lambda *t, **kw: g.sdm_fwd(*t, 8, 8, want_slots=True, **kw),
+                    (r(1, 2, n * n, 128), r(1, 1024, 2, 2, n), r(1, 1024, 2, 2, n), r(1, 1024, 2, 128).to(bf), alpha, beta)),
+        "dmem_fwd": (lambda *t, **kw: (g.dmem_fwd(*t, **kw),),
+                     (r(64, 2, 8, 8), *few, sig(r(64, 50, 2)), sig(r(64, 50, 2)))),
+        "decode_step": (lambda *t, **kw: (g.decode_step(*t, **kw),),
+                        (r(64, 2, 64, 64), *(unit(r(64, 2, 64), dim=-1) for _ in range(3)), sig(r(64, 2)), sig(r(64, 2)))),
         "scan_fwd": (lambda x, a, **kw: g.scan_fwd(x, a, want_ckpt=True, **kw), (x, gate)),
         "scan_bwd": (lambda x, a, dy, ck, d, **kw: g.scan_bwd(x, a, dy, ck, dST=d, **kw), (x, gate, dy, ckpt, dST)),
         "scan_step": (lambda S, x, a, **kw: (g.scan_step(S, x, a, **kw),), (S, r(512, 2, 64), torch.sigmoid(r(512, 2, 64)))),
@@ -28,7 +43,8 @@ def _calls(torch, g):
     }
 
 
-NAMES = ["scan_fwd", "scan_bwd", "scan_step", "qk_prep", "qk_prep_bwd"]
+NAMES = ["chunk_fwd", "chunk_fwd_ckpt", "mc_readout", "osdn_precond", "sdm_fwd", "dmem_fwd", "decode_step",
+         "scan_fwd", "scan_bwd", "scan_step", "qk_prep", "qk_prep_bwd"]
 
 
 def _busy(torch, stream):
