@@ -28,6 +28,7 @@ struct QkParams {
     int norm;         // 0 none, 1 L2, 2 RMS
     int half_layout;  // pairs (i, i + rot / 2) instead of (2 i, 2 i + 1)
     float kappa, eps, rot_scale;
+    float rot_sin;  // rot_scale, or its negative for turns the other way (set by the launcher)
     const int32_t *pos;  // [tokens] or NULL (the row's index in its sequence)
     const double *inv_freq;
     QkTensor q, k;

@@ -8,6 +8,7 @@
 // Backward, from g = d loss / d out:
 //     m = scale Rot_pos^T(g),  t = w (.) m,  dw = sum over rows r m (.) x
 //     dx = r t - kappa r^3 (t . x) x
+// and without a norm dx = m, which x does not enter: the forward pass of g, turned the other way.
 //
 // Bound by HBM (forward 2 and backward 3 passes over the heads, under 10 operations per
 // byte), so the layout serves the loads.  Rotated channels are held as pairs: a lane owns
@@ -182,7 +183,7 @@ __device__ __forceinline__ float row_sum(float x, int P) {
     return x;
 }
 
-// Cosine and sine of pos * f_i, times rot_scale; pairs past the rotated part get 1 and 0.  The
+// Cosine and sine of pos * f_i, times rot_scale and rot_sin; pairs past the rotated part get 1 and 0.  The
 // angle is formed and reduced to a fraction of a turn in 64 bits: at position 10^6 its 32-bit
 // product would be off by 0.06.
 __device__ __forceinline__ float2 angle(const QkParams &p, unsigned token, int i) {
@@ -192,7 +193,7 @@ __device__ __forceinline__ float2 angle(const QkParams &p, unsigned token, int i
     turn -= rint(turn);
     float sn, cs;
     sincospif(2.f * (float)turn, &sn, &cs);
-    return make_float2(cs * p.rot_scale, sn * p.rot_scale);
+    return make_float2(cs * p.rot_scale, sn * p.rot_sin);
 }
 
 // r of one row from its sum of squares (already over the P lanes)
@@ -394,6 +395,16 @@ size_t qk_prep_bwd_workspace(const QkParams &p0) {
 hipError_t launch_qk_prep(const QkParams &p0, bool bwd, hipStream_t s) {
     QkParams p = p0;
     int vp, lay;
+    p.rot_sin = p.rot_scale;
+    if (bwd && p.norm == 0) {
+        // without a norm dx = scale Rot^T(g): the gradient's forward pass with its turns the other way, and x is not read
+        for (QkTensor *X : {&p.q, &p.k}) {
+            X->x = X->g;
+            X->ld = (int64_t)X->H * p.d;
+        }
+        p.rot_sin = -p.rot_scale;
+        bwd = false;
+    }
     plan(p, bwd, vp, lay);
     const long blocks = (long)p.blocks_q + p.blocks_k;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;

@@ -424,7 +424,8 @@ int gdr_qk_prep_fwd(const gdr_qk_desc *desc, const void *q, const void *k, const
                     const int32_t *positions, const double *inv_freq, void *q_out, void *k_out, void *stream);
 
 /*
- * Its backward pass, from the inputs and the gradients of the outputs:
+ * Its backward pass, from the inputs (whose values do not enter with GDR_NORM_NONE) and the
+ * gradients of the outputs:
  *   dq_out, dk_out  dense, io_dtype: gradients of q_out, k_out
  *   dq, dk          dense, io_dtype: gradients of q, k; may be dq_out, dk_out themselves,
  *                   and overlap nothing else

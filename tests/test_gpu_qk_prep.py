@@ -120,6 +120,30 @@ def test_zero_rows_and_special_values():
         assert torch.equal(out[rows], want[rows]) and dq[rows].isfinite().all()
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rot", [0, 12, 64])
+def test_backward_without_a_norm_does_not_look_at_the_inputs(layout, rot):
+    """dx = scale Rot^T(g) whatever x holds: infinities, NaN, and rows whose sum of squares passes fp32's range."""
+    torch, g = gpu()
+    q, k, gq, gk, how = _case(torch, 12, 2, 37, 3, 2, 64, "f32", None, "none", rot, layout, 5000, True)
+    want = g.qk_prep_bwd(q, k, gq, gk, **how)
+    q, k = torch.randn_like(q) * 3e38, k.clone()
+    q[0, 1, 0], q[0, 2, 1, 5], k[1, 3] = float("nan"), float("inf"), float("-inf")
+    got = g.qk_prep_bwd(q, k, gq, gk, **how)
+    assert all(torch.equal(a, b) for a, b in zip(got[:2], want[:2])) and got[2] is None and got[3] is None
+    f = None if how["inv_freq"] is None else how["inv_freq"].cpu().numpy()
+    pos = how["positions"].cpu().numpy()
+    for i, (x, go, scale) in enumerate(((q, gq, 0.125), (k, gk, 1.0))):
+        g64 = to_np(go)
+        dx, _ = ref.backward(np.zeros_like(g64), g64, norm="none", pos=pos, inv_freq=f, layout=layout, rot_scale=1.25, scale=scale)
+        _check("d" + "qk"[i], got[i], dx, U, 40 * U * 1.25 * 1.5 * scale * np.abs(g64).max(-1, keepdims=True))
+    # each gradient written over, as with a norm
+    desc = g._qk_desc(q, k, "none", None, None, 1e-5, how["inv_freq"], layout, 1.25, 0.125)
+    oq, ok = gq.clone(), gk.clone()
+    assert g.gdr_qk_prep_bwd(desc, q, k, None, None, how["positions"], how["inv_freq"], oq, ok, oq, ok, None, None, None, 0) == g.GDR_OK
+    assert torch.equal(oq, want[0]) and torch.equal(ok, want[1])
+
+
 def test_in_place_and_empty():
     torch, g = gpu()
     q, k = (torch.randn(2, 70, h, 128, device="cuda").bfloat16() for h in (4, 2))
