@@ -40,6 +40,8 @@ struct QkParams {
 // of 256 tokens spans at most 2^30 bytes, and most bytes of the states of packed sequences.
 constexpr int64_t kMaxRow = 1 << 20, kMaxStates = 1 << 30;
 
+constexpr int64_t kMaxThreads = 0xffffffff;  // of one launch (workgroups times their threads)
+
 // Parameters of one gated linear recurrence call (forward, backward or single step).
 struct ScanParams {
     int B, T, D;  // D channels per token
@@ -65,7 +67,7 @@ struct ScanParams {
 size_t qk_prep_bwd_workspace(const QkParams &p);
 hipError_t launch_qk_prep(const QkParams &p, bool bwd, hipStream_t s);
 size_t scan_workspace(const ScanParams &p);
-long scan_blocks(const ScanParams &p);  // workgroups of a pass
+long scan_threads(const ScanParams &p);  // of a pass's launch
 hipError_t launch_scan_fwd(const ScanParams &p, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanParams &p, hipStream_t s);
 hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s);  // src NULL: zeros

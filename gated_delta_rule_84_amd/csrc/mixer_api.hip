@@ -275,7 +275,7 @@ int gdr_scan_fwd(const gdr_desc *d, const void *x, int64_t ldx, const void *alph
         if (!apart(outs, 4, ins, 5)) return GDR_EINVAL;
     }
     if (p.D == 0 || ns == 0) return GDR_OK;
-    if (scan_blocks(p) > 0x7fffffffLL) return GDR_EUNSUPPORTED;
+    if (scan_threads(p) > kMaxThreads) return GDR_EUNSUPPORTED;
     p.S0 = S0;
     p.y = y;
     p.ST = ST;
@@ -313,7 +313,7 @@ int gdr_scan_bwd(const gdr_desc *d, const void *x, int64_t ldx, const void *alph
         if (!apart(outs, 5, ins, 8)) return GDR_EINVAL;
     }
     if (p.D == 0 || ns == 0) return GDR_OK;
-    if (scan_blocks(p) > 0x7fffffffLL) return GDR_EUNSUPPORTED;
+    if (scan_threads(p) > kMaxThreads) return GDR_EUNSUPPORTED;
     p.S0 = S0;
     p.ckpt = const_cast<float *>(ckpt);
     p.dy = dy;

@@ -99,7 +99,7 @@ struct Step {
 // of either direction: the smallest groups need most
 size_t scan_workspace(const ScanParams &p) { return (size_t)chain_bytes(p, kGroupPacked); }
 
-long scan_blocks(const ScanParams &p) { return columns_of(p) * p.nblk; }
+long scan_threads(const ScanParams &p) { return columns_of(p) * p.nblk * 64 * waves_of(p); }
 
 hipError_t launch_scan_copy(const float *src, float *dst, long n, hipStream_t s) {
     if (!dst || n == 0 || src == dst) return hipSuccess;

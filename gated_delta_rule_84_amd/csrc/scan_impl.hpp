@@ -529,6 +529,12 @@ inline long chain_bytes(const ScanParams &p, int group) {
     return p.nblk <= 1 ? 0 : kChainHead + columns_of(p) * chain_words(p.nblk, group) * CH * 4;
 }
 
+// Waves per workgroup: as many as a call of few tokens has strands for.
+inline int waves_of(const ScanParams &p) {
+    const int strands = ((p.T < kBlk ? p.T : kBlk) + L - 1) / L;
+    return (strands + kWS - 1) / kWS;
+}
+
 // Every word of the chain to kNone (a kernel, so that a captured graph replays it): 2.2 us for one
 // sequence of few channels, 2.8 us for 4 x 16 blocks of 2,048 channels, 6.5 us for 256 of 4,096.
 __global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
@@ -539,8 +545,7 @@ __global__ void __launch_bounds__(256) scan_fill_kernel(u32x4 *ws, long n) {
 // Clears the chain's words and launches the blocks.
 template <class K>
 hipError_t launch_blocks(const ScanParams &p, hipStream_t s) {
-    const int strands = ((p.T < kBlk ? p.T : kBlk) + L - 1) / L, waves = (strands + kWS - 1) / kWS;
-    const long blocks = columns_of(p) * p.nblk;  // fits 31 bits: the host has checked
+    const long blocks = columns_of(p) * p.nblk;  // fits: the host has checked the threads
     if (p.nblk > 1) {
         u32x4 *ws = static_cast<u32x4 *>(p.ws);
         long n = chain_bytes(p, K::group(p)) / 16;
@@ -551,7 +556,7 @@ hipError_t launch_blocks(const ScanParams &p, hipStream_t s) {
     }
     ScanParams q = p;
     void *args[] = {&q};
-    return hipLaunchKernel(pick<K>(p), dim3((unsigned)blocks), dim3(64 * waves), args, 0, s);
+    return hipLaunchKernel(pick<K>(p), dim3((unsigned)blocks), dim3(64 * waves_of(p)), args, 0, s);
 }
 
 }  // namespace

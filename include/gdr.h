@@ -455,7 +455,9 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *   desc       B, T, H, dv >= 1 (any), io_dtype (x, y, dy, dx), gate_dtype (alpha, beta and
  *              their gradients), alpha_mode GDR_ALPHA_CHANNEL (else GDR_EUNSUPPORTED),
  *              flags; dk, chunk and beta_mode are not used.  H * dv and the strides at
- *              most 2^20, B * T < 2^30, the states at most 2^30 bytes (else GDR_EUNSUPPORTED).
+ *              most 2^20, B * T < 2^30, the states at most 2^30 bytes, and
+ *              B * ceil(H * dv / 64) * ceil(T / 256) * min(512, 64 * ceil(T / 32)) threads
+ *              below 2^32 (else GDR_EUNSUPPORTED).
  *   x          [B, T, H, dv] io_dtype;  alpha, beta [B, T, H, dv] gate_dtype, beta may be
  *              NULL; ldx, lda, ldb elements between successive tokens (b, t), 0 for dense
  *              (H * dv), larger for slices of a fused projection's output

@@ -340,6 +340,20 @@ def test_workspace_of_a_call_on_another_stream():
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_the_largest_launch():
+    """2^32 - 64 threads: one token of 2^26 - 1 sequences of one channel."""
+    torch, g = gpu()
+    B = (1 << 26) - 1
+    x, alpha = (torch.randint(-8, 9, (B, 1, 1, 1), device="cuda").to(torch.bfloat16) for _ in range(2))
+    S0 = torch.randint(-8, 9, (B, 1, 1), device="cuda").float()
+    y, ST, ck = g.scan_fwd(x, alpha, S0=S0, want_ckpt=True)
+    want = alpha[:, 0].float() * S0 + x[:, 0].float()  # whole numbers to 72: exact in bf16
+    assert torch.equal(ST, want) and torch.equal(y[:, 0].float(), want)
+    dx, da, _, dS0 = g.scan_bwd(x, alpha, x, ck, S0=S0, dST=S0)
+    G = x[:, 0].float() + S0
+    assert torch.equal(dx[:, 0].float(), G) and torch.equal(da[:, 0].float(), G * S0) and torch.equal(dS0, G * alpha[:, 0].float())
+
+
 def test_offsets_past_32_bits():
     """2.6 billion elements: the last rows, behind a reset, equal a call on them alone."""
     torch, g = gpu()

@@ -136,6 +136,17 @@ def test_scan_descriptor(g, field, value, status):
         assert g.gdr_scan_step(d, x, 0, a, 0, None, 0, S, y, 0) == status
 
 
+@pytest.mark.parametrize("B,T,dv", [(1 << 26, 1, 1), (1 << 26, 15, 4), (1 << 27, 7, 2), (1 << 28, 3, 1), (1, (1 << 30) - 1, 65),
+                                    (3, (1 << 28) + 1, 64 * 9)])
+def test_scan_launches_that_are_too_large(g, B, T, dv):
+    """A launch has fewer than 2^32 threads: refused before any."""
+    x, a, y, ck, dx, da, ws = _ptrs(n=7, step=1 << 50)
+    d = _scan(g, B=B, T=T, H=1, dv=dv)
+    wb = g.gdr_scan_workspace_size(d)
+    assert g.gdr_scan_fwd(d, x, 0, a, 0, None, 0, None, 0, None, y, None, None, ws, wb, 0) == g.GDR_EUNSUPPORTED
+    assert g.gdr_scan_bwd(d, x, 0, a, 0, None, 0, None, 0, None, ck, y, None, dx, da, None, None, ws, wb, 0) == g.GDR_EUNSUPPORTED
+
+
 def test_scan_pointers(g):
     d = _scan(g)
     x, a, b, off, S0, y, ST, ck, ws = _ptrs(n=9, step=0x10000000)
