@@ -55,7 +55,7 @@ int check_qk_desc(const gdr_qk_desc *d) {
     if (!(d->eps >= 0.f) || !(d->q_scale == d->q_scale) || !(d->rot_scale == d->rot_scale)) return GDR_EINVAL;
     if (d->rot_dim < 0 || (d->rot_dim & 1) || d->rot_dim > d->d) return GDR_EINVAL;
     if (d->d < 8 || d->d > 256 || (d->d & 7)) return GDR_EUNSUPPORTED;
-    // tokens and rows are counted in 64 bits, workgroups in 31: each takes at least one token's heads
+    // a token's number fits 31 bits; rows of heads are counted in 64
     if ((long long)d->B * d->T > 0x3fffffffLL || d->Hq > 65536 || d->Hk > 65536) return GDR_EUNSUPPORTED;
     return GDR_OK;
 }

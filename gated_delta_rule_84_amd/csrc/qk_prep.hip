@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gdr_device.hpp"
 #include "gdr_mfma.hpp"
 #include "mixer.hpp"
@@ -358,6 +360,7 @@ const void *pick_layout(int lay) {
 }
 
 constexpr int kMaxBlocks = 768;  // workgroups per tensor of a backward pass: about what the chip holds at once
+constexpr int kMaxGrid = (1 << 23) - 1;  // of a forward pass: a launch of both tensors has fewer than 2^32 threads
 
 // Lanes, heads per group and workgroups of one call.
 void plan(QkParams &p, bool bwd, int &vp, int &lay) {
@@ -377,7 +380,7 @@ void plan(QkParams &p, bool bwd, int &vp, int &lay) {
     for (int i = 0; i < 2; ++i) {
         all[i]->slices = (all[i]->H + p.rows - 1) / p.rows;
         blocks[i] = (p.tokens * all[i]->slices + groups - 1) / groups;
-        if (bwd && blocks[i] > kMaxBlocks) blocks[i] = kMaxBlocks;
+        blocks[i] = std::min<long>(blocks[i], bwd ? kMaxBlocks : kMaxGrid);
     }
     p.blocks_q = (int)blocks[0];
     p.blocks_k = (int)blocks[1];
@@ -407,7 +410,6 @@ hipError_t launch_qk_prep(const QkParams &p0, bool bwd, hipStream_t s) {
     }
     plan(p, bwd, vp, lay);
     const long blocks = (long)p.blocks_q + p.blocks_k;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
     void *args[] = {&p};
     const void *fn = p.io_bf16 ? (bwd ? pick_layout<true, 4, true>(lay) : pick_layout<true, 4, false>(lay))
                                : (bwd ? pick_layout<false, 4, true>(lay) : pick_layout<false, 4, false>(lay));

@@ -203,3 +203,19 @@ def test_many_tokens_split_like_few():
     for t in (0, 1, 12345, 39998):
         b = g.qk_prep(q[:, t:t + 2], k[:, t:t + 2], positions=pos[:, t:t + 2].contiguous(), **how)
         assert torch.equal(a[0][:, t:t + 2], b[0]) and torch.equal(a[1][:, t:t + 2], b[1])
+
+
+def test_more_rows_than_a_launch_has_groups_for():
+    """2^27 + 77 tokens of one head of 256, in place (69 GB): the workgroups come round again, and every row is done once."""
+    torch, g = gpu()
+    n, T = 131071, (1 << 27) + 77
+    base = torch.randn(1, n, 1, 256, device="cuda").bfloat16()
+    none = torch.empty(1, n, 0, 256, device="cuda", dtype=torch.bfloat16)
+    w = torch.rand(256, device="cuda")
+    want, _ = g.qk_prep(base, none, norm="l2", wq=w)
+    q, k = torch.empty(1, T, 1, 256, device="cuda", dtype=torch.bfloat16), none.new_empty(1, T, 0, 256)
+    for t in range(0, T, n):
+        q[:, t:t + n] = base[:, :T - t]
+    log(f"[qk_prep] {T} tokens")
+    g.qk_prep(q, k, norm="l2", wq=w, out=(q, k))
+    assert all(torch.equal(q[:, t:t + n], want[:, :T - t]) for t in range(0, T, n))
