@@ -128,12 +128,12 @@ ScanParams scan_params(const gdr_desc *d) {
     return p;
 }
 
-// The checks of x, alpha and beta; fills them and their byte extents.
-int scan_inputs(ScanParams &p, long long rows, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
-                int64_t ldb, Span (&in)[3]) {
+// The checks of x, alpha and beta, whose rows are at most `most` elements apart; fills them and their byte extents.
+int scan_inputs(ScanParams &p, long long rows, int64_t most, const void *x, int64_t ldx, const void *alpha, int64_t lda,
+                const void *beta, int64_t ldb, Span (&in)[3]) {
     const size_t es = p.io_bf16 ? 2 : 4, gs = p.gate_bf16 ? 2 : 4;
     if (!stride_ok(ldx, rows, p.D) || !stride_ok(lda, rows, p.D) || !stride_ok(ldb, rows, p.D)) return GDR_EINVAL;
-    if (ldx > kMaxRow || lda > kMaxRow || ldb > kMaxRow) return GDR_EUNSUPPORTED;
+    if (ldx > most || lda > most || ldb > most) return GDR_EUNSUPPORTED;
     if (p.coupled && beta) return GDR_EINVAL;
     if (rows > 0 && p.D > 0 && (!x || !alpha)) return GDR_EINVAL;
     if (!aligned_to(x, es) || !aligned_to(alpha, gs) || !aligned_to(beta, gs)) return GDR_EINVAL;
@@ -253,7 +253,7 @@ int gdr_scan_fwd(const gdr_desc *d, const void *x, int64_t ldx, const void *alph
     const long long rows = (long long)d->B * d->T;
     Span ins[5];
     Span in3[3];
-    rc = scan_inputs(p, rows, x, ldx, alpha, lda, beta, ldb, in3);
+    rc = scan_inputs(p, rows, kMaxRow, x, ldx, alpha, lda, beta, ldb, in3);
     if (rc) return rc;
     rc = scan_sequences(p, seq_off, n_seq);
     if (rc) return rc;
@@ -292,7 +292,7 @@ int gdr_scan_bwd(const gdr_desc *d, const void *x, int64_t ldx, const void *alph
     ScanParams p = scan_params(d);
     const long long rows = (long long)d->B * d->T;
     Span in3[3];
-    rc = scan_inputs(p, rows, x, ldx, alpha, lda, beta, ldb, in3);
+    rc = scan_inputs(p, rows, kMaxRow, x, ldx, alpha, lda, beta, ldb, in3);
     if (rc) return rc;
     rc = scan_sequences(p, seq_off, n_seq);
     if (rc) return rc;
@@ -335,7 +335,8 @@ int gdr_scan_step(const gdr_desc *d, const void *x, int64_t ldx, const void *alp
     if (rc) return rc;
     ScanParams p = scan_params(&one);
     Span ins[3];
-    rc = scan_inputs(p, p.B, x, ldx, alpha, lda, beta, ldb, ins);
+    // 64-bit addresses, no block of rows: any stride
+    rc = scan_inputs(p, p.B, INT64_MAX, x, ldx, alpha, lda, beta, ldb, ins);
     if (rc) return rc;
     if (p.B == 0 || p.D == 0) return GDR_OK;
     if (!S || !y) return GDR_EINVAL;

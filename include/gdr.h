@@ -504,7 +504,8 @@ int gdr_scan_bwd(const gdr_desc *desc, const void *x, int64_t ldx, const void *a
 /*
  * One token for every sequence, applied in place to a resident state: x, alpha, beta
  * [B, H, dv] (ldx, lda, ldb elements between sequences, 0 for dense), S [B, H, dv] fp32
- * read and overwritten, y [B, H, dv] dense.  desc->T is ignored.
+ * read and overwritten, y [B, H, dv] dense.  desc->T is ignored, and the strides may pass 2^20
+ * (one token of a long stream is a call without a copy).
  */
 int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
                   int64_t ldb, float *S, void *y, void *stream);

@@ -242,6 +242,22 @@ def test_step_equals_one_token(B, H, dv, io, gate, form, kind):
     assert torch.equal(y[:, 0], ys[0])
 
 
+@pytest.mark.parametrize("io,gate", [("bf16", "f32"), ("f32", "bf16")])
+def test_step_on_a_token_of_a_long_stream(io, gate):
+    """A slice [:, t] whose sequences are more than 2^20 elements apart, read where it lies."""
+    torch, g = gpu()
+    x, alpha, how, _, _ = _inputs(torch, 34, 3, 600, 16, 128, io, gate, "log", "beta")
+    S = how.pop("S0")
+    for t in (0, 599):
+        cut = [v[:, t] for v in (x, alpha, how["beta"])]
+        assert all(v.stride(0) > 1 << 20 for v in cut)
+        Sa, Sb = S.clone(), S.clone()
+        y = g.scan_step(Sa, cut[0], cut[1], **dict(how, beta=cut[2]))
+        cut = [v.contiguous() for v in cut]
+        want = g.scan_step(Sb, cut[0], cut[1], **dict(how, beta=cut[2]))
+        assert torch.equal(y, want) and torch.equal(Sa, Sb)
+
+
 def test_resume_in_place_and_empty():
     torch, g = gpu()
     x, alpha, how, dy, dST = _inputs(torch, 27, 2, 1500, 2, 10, "bf16", "f32", "log", "coupled")

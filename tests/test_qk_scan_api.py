@@ -217,6 +217,17 @@ def test_scan_step_pointers(g):
     assert g._lib.gdr_scan_step(None, None, 0, None, 0, None, 0, None, None, None) == g.GDR_EINVAL
 
 
+def test_scan_step_strides(g):
+    """A stride over 2^20 elements is no reason to refuse; here the NULL output is, or what cannot be addressed."""
+    d = _scan(g)
+    x, a, S, y = _ptrs(n=4, step=0x10000000)
+    for ld in ((1 << 20) + 1, 1 << 40):
+        assert g.gdr_scan_step(d, x, ld, a, 0, None, 0, S, None, 0) == g.GDR_EINVAL
+        assert g.gdr_scan_step(d, x, 0, a, ld, None, 0, S, None, 0) == g.GDR_EINVAL
+        assert g.gdr_scan_step(d, x, 0, a, 0, a, ld, S, None, 0) == g.GDR_EINVAL
+    assert g.gdr_scan_step(d, x, 1 << 60, a, 0, None, 0, S, y, 0) == g.GDR_EINVAL
+
+
 def test_scan_binding(g):
     bf = torch.bfloat16
     x, a = torch.zeros(1, 6, 2, 8, dtype=bf), torch.zeros(1, 6, 2, 8)
