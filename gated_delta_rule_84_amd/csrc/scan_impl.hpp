@@ -289,7 +289,9 @@ constexpr uint32_t kCut = 0xfffffffeu;   // in a map's factor: nothing of what e
 constexpr int kGroupFwd = 8, kGroupPacked = 4, kGroupBwd = 6;  // blocks per group (kGroupPacked: forward with offsets)
 static_assert(kGroupPacked <= kGroupFwd && kGroupPacked <= kGroupBwd, "scan_workspace takes the smallest");
 constexpr int kWindow = 2;               // groups looked back over at a time
-constexpr int kMaxPolls = 1 << 22;       // some seconds: a bound that a sound run never meets
+// Looks before a wait gives up, a bound that a sound run never meets: a look is a trip past the L2 caches, over
+// 100 ns, so half a second at least.  The state is NaN then, and so are the blocks behind.
+constexpr int kMaxPolls = 1 << 22;
 
 __device__ __forceinline__ uint32_t word(float f) {
     const uint32_t u = __float_as_uint(f);

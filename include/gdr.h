@@ -480,7 +480,9 @@ int gdr_qk_prep_bwd(const gdr_qk_desc *desc, const void *q, const void *k, const
  *              serves one call at a time: calls, or graphs, that may run at the same time
  *              need one each.
  * Pointers need their element's alignment only.  Outputs overlap no input and no other output.
- * Results are deterministic.
+ * Results are deterministic.  Blocks of a sequence that run side by side wait for each other, each for
+ * a bounded time: should one wait in vain, which only a fault of the device or the library could
+ * bring about, the channels' states from there on are NaN (the status has long been returned).
  */
 #define GDR_SCAN_BLOCK 256
 size_t gdr_scan_workspace_size(const gdr_desc *desc);

@@ -157,3 +157,20 @@ BAD = [[40, 10], [-5, 2600], [0, 1 << 30], [2 ** 31 - 1, -2 ** 31], [0, 900, 300
 def test_offsets_that_break_the_rules_reach_nothing_outside(program, offsets, at_end):
     _run(program, 1, 2600, 12, "f32", "f32", "log", "beta", offsets=offsets, at_end=at_end)
     _run(program, 1, 300, 70, "bf16", "bf16", "value", "one", offsets=offsets, at_end=at_end)
+
+
+def test_a_wait_in_vain_ends_and_shows(tmp_path):
+    """The first block is never run and the bound is small: every block behind it ends, with NaN and not with numbers."""
+    csrc = tmp_path / "csrc"
+    shutil.copytree(CSRC, csrc)
+    header = csrc / "scan_impl.hpp"
+    text = header.read_text()
+    assert text.count("kMaxPolls = 1 << 22") == 1
+    header.write_text(text.replace("kMaxPolls = 1 << 22", "kMaxPolls = 20"))
+    program = _build(tmp_path / "scan_host", str(csrc))
+    for T, offsets in ((3000, None), (700, None), (3000, [0, 3000]), (3000, [100, 2500])):
+        out, bits, _ = _run(program, 1, T, 12, "f32", "f32", "value", "one", offsets=offsets, skip_first=True)
+        end = T if offsets is None else offsets[-1]
+        assert (bits["y"][:, :256] == 0x5a).all()
+        assert np.isnan(out["y"][:, 256:end]).all() and np.isnan(out["ST"]).all()
+        assert np.isnan(out["ckpt"][:, 1:end // 256]).all()
