@@ -36,6 +36,7 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int VP = 4;  // pairs per lane
 
 // N elements of a row as they are stored, from an element-aligned address (the hardware takes
 // a global access of a dword or more at any byte address).
@@ -89,13 +90,13 @@ struct Elems {
 enum Layout { kAdjacent = 0, kSplit = 1, kScattered = 2 };
 
 // A lane's pairs of one row, as stored.
-template <bool BF, int VP, int LAY>
+template <bool BF, int LAY>
 struct Held {
     Elems<BF, LAY == kAdjacent ? 2 * VP : VP> a, b;  // kAdjacent uses only a
     float e[LAY == kScattered ? VP : 1], o[LAY == kScattered ? VP : 1];
 };
 
-template <bool BF, int VP, int LAY>
+template <bool BF, int LAY>
 struct Row {
     int at[2];      // kAdjacent: [0]; kSplit: both
     int i0, half;   // kScattered
@@ -117,7 +118,7 @@ struct Row {
         const int i = i0 + j;
         return i < half ? i + (second ? half : 0) : 2 * i + second;
     }
-    __device__ __forceinline__ void load(const void *base, long row, Held<BF, VP, LAY> &r) const {
+    __device__ __forceinline__ void load(const void *base, long row, Held<BF, LAY> &r) const {
         if constexpr (LAY == kScattered) {
 #pragma unroll
             for (int j = 0; j < VP; ++j) {
@@ -129,7 +130,7 @@ struct Row {
             if constexpr (LAY == kSplit) r.b.load(base, row + at[1]);
         }
     }
-    __device__ __forceinline__ void unpack(const Held<BF, VP, LAY> &r, float (&e)[VP], float (&o)[VP]) const {
+    __device__ __forceinline__ void unpack(const Held<BF, LAY> &r, float (&e)[VP], float (&o)[VP]) const {
 #pragma unroll
         for (int j = 0; j < VP; ++j) {
             if constexpr (LAY == kAdjacent) {
@@ -152,7 +153,7 @@ struct Row {
                 st_elem(base, row + channel(j, 1), o[j], BF);
             }
         } else {
-            Held<BF, VP, LAY> r;
+            Held<BF, LAY> r;
 #pragma unroll
             for (int j = 0; j < VP; j += 2) {
                 if constexpr (LAY == kAdjacent) {
@@ -170,10 +171,10 @@ struct Row {
 };
 
 // The weights of a lane's pairs, stored as bf16 (WB) or fp32.
-template <bool WB, int VP, int LAY>
+template <bool WB, int LAY>
 __device__ __forceinline__ void weights(const void *w, int pair0, int half, float (&we)[VP], float (&wo)[VP]) {
-    Row<WB, VP, LAY> at;
-    Held<WB, VP, LAY> h;
+    Row<WB, LAY> at;
+    Held<WB, LAY> h;
     at.place(pair0, half);
     at.load(w, 0, h);
     at.unpack(h, we, wo);
@@ -205,7 +206,7 @@ __device__ __forceinline__ float inverse_norm(const QkParams &p, float ss) {
     return m > 0.f || m != m ? 1.f / sqrtf(m) : 0.f;
 }
 
-template <bool BF, int VP, int LAY, bool BWD>
+template <bool BF, int LAY, bool BWD>
 __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
     __shared__ float2 turns[kThreads * VP];
     const bool isk = blockIdx.x >= (unsigned)p.blocks_q;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
     const int gl = threadIdx.x / P, lane = threadIdx.x % P;
     const int i0 = lane * VP;
     const bool holds = i0 < p.d / 2;  // lanes past the row only take part in the sums
-    Row<BF, VP, LAY> at;
+    Row<BF, LAY> at;
     at.place(holds ? i0 : 0, p.rot / 2);
     float we[VP], wo[VP], ae[VP], ao[VP];
 #pragma unroll
@@ -224,8 +225,8 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
         we[j] = wo[j] = 1.f;
         ae[j] = ao[j] = 0.f;
     }
-    if (X.w && p.w_bf16) weights<true, VP, LAY>(X.w, holds ? i0 : 0, p.rot / 2, we, wo);
-    else if (X.w) weights<false, VP, LAY>(X.w, holds ? i0 : 0, p.rot / 2, we, wo);
+    if (X.w && p.w_bf16) weights<true, LAY>(X.w, holds ? i0 : 0, p.rot / 2, we, wo);
+    else if (X.w) weights<false, LAY>(X.w, holds ? i0 : 0, p.rot / 2, we, wo);
     const int pairs = P * VP, shift = __ffs(pairs) - 1;
     const long items = p.tokens * X.slices;
     for (long first = block * groups; first < items; first += nblocks * groups) {
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) qk_prep_kernel(QkParams p) {
         const long token = token0 + step;
         const int h0 = gl < here ? (int)(mine - step * X.slices) * p.rows : X.H, h1 = min(h0 + p.rows, X.H);
         // each row is loaded while the one before it is worked on, the first under the angles
-        Held<BF, VP, LAY> next, gnext;
+        Held<BF, LAY> next, gnext;
         auto fetch = [&](int h) __attribute__((always_inline)) {
             at.load(X.x, token * X.ld + (long)h * p.d, next);
             if constexpr (BWD) at.load(X.g, (token * X.H + h) * p.d, gnext);
@@ -350,25 +351,24 @@ __global__ void __launch_bounds__(256) qk_weight_kernel(QkParams p) {
     }
 }
 
-template <bool BF, int VP, bool BWD>
+template <bool BF, bool BWD>
 const void *pick_layout(int lay) {
     switch (lay) {
-    case kAdjacent: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, VP, kAdjacent, BWD>);
-    case kSplit: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, VP, kSplit, BWD>);
-    default: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, VP, kScattered, BWD>);
+    case kAdjacent: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, kAdjacent, BWD>);
+    case kSplit: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, kSplit, BWD>);
+    default: return reinterpret_cast<const void *>(&qk_prep_kernel<BF, kScattered, BWD>);
     }
 }
 
 constexpr int kMaxBlocks = 768;  // workgroups per tensor of a backward pass: about what the chip holds at once
 constexpr int kMaxGrid = (1 << 23) - 1;  // of a forward pass: a launch of both tensors has fewer than 2^32 threads
 
-// Lanes, heads per group and workgroups of one call.
-void plan(QkParams &p, bool bwd, int &vp, int &lay) {
+// Lanes, heads per group and workgroups of one call; returns its layout.
+int plan(QkParams &p, bool bwd) {
     const int half = p.rot / 2;
-    vp = 4;
-    lay = !p.half_layout || half == 0 ? kAdjacent : (half % vp == 0 ? kSplit : kScattered);
+    const int lay = !p.half_layout || half == 0 ? kAdjacent : (half % VP == 0 ? kSplit : kScattered);
     p.lanes = 1;
-    while (p.lanes * vp < p.d / 2) p.lanes <<= 1;
+    while (p.lanes * VP < p.d / 2) p.lanes <<= 1;
     const int groups = kThreads / p.lanes;
     // Up to 8 heads share a token's angles and follow each other in the pipeline of loads; fewer
     // where that leaves the chip's 1024 SIMDs without 4 waves each and latency is what counts.
@@ -384,20 +384,19 @@ void plan(QkParams &p, bool bwd, int &vp, int &lay) {
     }
     p.blocks_q = (int)blocks[0];
     p.blocks_k = (int)blocks[1];
+    return lay;
 }
 
 }  // namespace
 
 size_t qk_prep_bwd_workspace(const QkParams &p0) {
     QkParams p = p0;
-    int vp, lay;
-    plan(p, true, vp, lay);
+    plan(p, true);
     return (size_t)(p.blocks_q + p.blocks_k) * p.d * sizeof(float);
 }
 
 hipError_t launch_qk_prep(const QkParams &p0, bool bwd, hipStream_t s) {
     QkParams p = p0;
-    int vp, lay;
     p.rot_sin = p.rot_scale;
     if (bwd && p.norm == 0) {
         // without a norm dx = scale Rot^T(g): the gradient's forward pass with its turns the other way, and x is not read
@@ -408,11 +407,11 @@ hipError_t launch_qk_prep(const QkParams &p0, bool bwd, hipStream_t s) {
         p.rot_sin = -p.rot_scale;
         bwd = false;
     }
-    plan(p, bwd, vp, lay);
+    const int lay = plan(p, bwd);
     const long blocks = (long)p.blocks_q + p.blocks_k;
     void *args[] = {&p};
-    const void *fn = p.io_bf16 ? (bwd ? pick_layout<true, 4, true>(lay) : pick_layout<true, 4, false>(lay))
-                               : (bwd ? pick_layout<false, 4, true>(lay) : pick_layout<false, 4, false>(lay));
+    const void *fn = p.io_bf16 ? (bwd ? pick_layout<true, true>(lay) : pick_layout<true, false>(lay))
+                               : (bwd ? pick_layout<false, true>(lay) : pick_layout<false, false>(lay));
     hipError_t e = blocks > 0 ? hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(kThreads), args, 0, s) : hipSuccess;
     if (e == hipSuccess && bwd && (p.q.dw || p.k.dw))
         e = hipLaunchKernel(reinterpret_cast<const void *>(&qk_weight_kernel), dim3((unsigned)((p.d + 15) / 16), 2),
