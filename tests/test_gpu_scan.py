@@ -163,6 +163,34 @@ def test_packed_sequences(case):
         _check(name, got, want[name], step)
 
 
+def test_exponential_of_log_gates():
+    """exp and 1 - exp of a log gate within 2 units in the last place (4 u; the last rounding is u, the polynomial's
+    and the reduced argument's errors are scaled by |q| / a <= 0.6 and stay under 2 u), over the range that counts.
+    A step from S = 1 with x = 0 gives the decay itself, one from S = 0 with x = 1 and coupled gates the factor."""
+    torch, g = gpu()
+    rng = np.random.default_rng(35)
+    n = 1 << 20
+    near = np.exp(rng.uniform(np.log(1e-30), 0, n))
+    borders = (np.arange(-127, 128) + 0.5)[:, None] * np.log(2) + rng.normal(size=(255, 4096)) * 1e-4
+    t = np.concatenate([rng.uniform(-88.5, 88, n), near, -near, borders.ravel(), [0.0, -0.0, -88.0, 88.0]]).astype(np.float32)
+    t = np.resize(t[(t > -88.5) & (t <= 88)], (len(t) // 1024, 1, 1024))
+    al = torch.from_numpy(t).cuda()
+    S, zero, one = torch.ones_like(al), torch.zeros_like(al), torch.ones_like(al)
+    g.scan_step(S, zero, al, log_gate=True)
+    b = torch.zeros_like(al)
+    g.scan_step(b, one, al, log_gate=True, coupled=True)
+    t64 = t.astype(np.float64)
+    for name, got, want in (("exp", S, np.exp(t64)), ("1 - exp", b, -np.expm1(t64))):
+        err = np.abs(to_np(got) - want) / (4 * U * np.abs(want) + 2.0 ** -126)  # decays under the normal range may be 0
+        log(f"[scan] {name}: error / bound {err.max():.3f}")
+        assert err.max() <= 1.0
+    al = torch.tensor([[[float("-inf"), -1e30, -88.1, 88.0, 90.0, 1e30, float("inf"), float("nan")]]], device="cuda")
+    S = torch.ones_like(al)
+    g.scan_step(S, torch.zeros_like(al), al, log_gate=True)
+    S = S.flatten().tolist()
+    assert S[:3] == [0, 0, 0] and S[3:7] == [S[3]] * 4 and abs(S[3] / np.exp(88.0) - 1) < 4 * U and S[7] != S[7]
+
+
 def test_rows_of_no_sequence_and_special_values_stay_apart():
     """Infinities and NaN of one packed sequence, or of rows in none, reach no other sequence, and rows of
     no sequence are left as they were."""
