@@ -758,7 +758,7 @@ def rope_inv_freq(rot_dim, *, base=10000.0, scaling=None, factor=1.0, original_l
         # the (real) channel index whose frequency turns n times over original_len
         at = lambda n: rot_dim * math.log(original_len / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
         lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot_dim - 1)
-        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1) if hi > 0 else torch.ones_like(i)
         f, scale = f * (1 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
     return f.to(device), scale
 

@@ -124,3 +124,16 @@ def test_rope_inv_freq():
                 dict(rot_dim=8, scaling="yarn", factor=2, original_len=64, base=1.0)):
         with pytest.raises(ValueError):
             g.rope_inv_freq(**bad, device="cpu")
+
+
+@pytest.mark.parametrize("original_len", [1, 4, 6, 40])
+def test_yarn_divides_every_frequency_that_turns_too_little(original_len):
+    """Frequencies that turn less than `slow` times over original_len are divided, the first one among them too."""
+    import gated_delta_rule_84_amd as g
+
+    plain = g.rope_inv_freq(64, device="cpu")[0].numpy()
+    ratio = g.rope_inv_freq(64, scaling="yarn", factor=8, original_len=original_len, device="cpu")[0].numpy() / plain
+    turns = original_len * plain / (2 * math.pi)
+    # the mix ends at whole indices, so up to the first index behind the last one that turns enough
+    first = int(np.argmax(turns < 1)) + (1 if turns[0] >= 1 else 0)
+    np.testing.assert_allclose(ratio[first:], 1 / 8)
