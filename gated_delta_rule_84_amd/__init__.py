@@ -166,7 +166,7 @@ def _check_all(specs) -> None:
             raise ValueError(f"{name}: expected {count} elements for this descriptor, got {t.numel()} "
                              f"(shape {tuple(t.shape)})")
         if here is None:
-            here = torch.cuda.current_device() if t.is_cuda else -2
+            here = torch._C._cuda_getDevice() if t.is_cuda else -2  # what current_device() asks, once there is a device
         if wrong is None and t.get_device() != here:
             wrong = name, t
     if wrong is not None:
@@ -203,10 +203,10 @@ def _prefill_specs(desc: Desc, q, k, k_w, v, alpha, beta_k, beta_v, S0, o, ST) -
             ("beta_v", beta_v, n * desc.dv, gt), ("S0", S0, st, torch.float32), ("ST", ST, st, torch.float32)]
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:  # the current stream's handle without building a Stream object
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(_handle(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _handle(stream)
 
 
 def _handle(stream) -> int:
