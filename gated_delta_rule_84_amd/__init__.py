@@ -736,9 +736,9 @@ def rope_inv_freq(rot_dim, *, base=10000.0, scaling=None, factor=1.0, original_l
       "linear"  every frequency divided by the factor (positions interpolated);
       "ntk"     the base raised by factor^(rot_dim / (rot_dim - 2)), which divides the lowest frequency by the
                 factor and leaves the highest as it is;
-      "yarn"    by wavelength: frequencies that turn more than `fast` times over original_len stay, those that
-                turn less than `slow` times are divided by the factor, those between are mixed linearly in the
-                channel's index; scale 0.1 ln(factor) + 1.
+      "yarn"    by wavelength (the YaRN paper, Peng et al., 2023): frequencies that turn more than `fast` times
+                over original_len stay, those that turn less than `slow` times are divided by the factor, those
+                between are mixed linearly in the channel's index; scale 0.1 ln(factor) + 1.
     """
     if rot_dim < 0 or rot_dim % 2:
         raise ValueError(f"rot_dim must be even and not negative, got {rot_dim}")

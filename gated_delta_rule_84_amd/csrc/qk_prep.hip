@@ -19,10 +19,14 @@
 // token, each loaded while the one before it is worked on, and the workgroup forms the
 // cosines and sines of its tokens once, in shared memory (each lane its own pairs' before:
 // 5 us of 91 in the backward pass below).
-// 4 x 4,096 tokens of 16 + 16 bf16 heads of 128: forward 44 us (6.1 TB/s), backward 73 to 80 us
-// (5.0 to 5.5 TB/s); 65,536 tokens of 32 + 8 forward 255 us (5.3 TB/s); fp32 4.8 and 7.1 TB/s.
-// 8 tokens of 16 + 16 take 4.5 us, which is a launch and one trip to memory.  Half rotations of
-// rot_dim / 2 not a multiple of 4 take each member by itself and reach 1.9 to 3.2 TB/s.
+// 4 x 4,096 tokens of 16 + 16 heads of 128, weights, full rotation, median kernel times: bf16 forward
+// 47 us (5.7 TB/s), backward 87 us (4.6 TB/s) and 4.8 us for the weights' sums, 44 us in all without a
+// norm; 65,536 tokens of 32 + 8 bf16 forward 254 us (5.3 TB/s); fp32 forward 111 us (4.8 TB/s), backward
+// with its sums 163 us (4.9 TB/s).  8 tokens of 16 + 16 take 4.1 us, which is a launch and one trip to memory.
+// Half rotations of rot_dim / 2 not a multiple of 4 take each member by itself, all lanes for the sake of
+// the one at the end of the rotated part: 1.6 to 3.3 TB/s.  P is rounded up to a power of two, so heads
+// whose d / 8 is none leave lanes idle: of 65,536 tokens of 16 + 4 heads, bf16 heads of 80, 96, 136 and 192 are
+// done at 3.8, 4.4, 3.7 and 4.7 TB/s forward, at 3.5, 4.1, 3.0 and 4.0 backward; fp32 ones at 4.7 or more.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

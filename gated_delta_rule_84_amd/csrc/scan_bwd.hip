@@ -1,10 +1,14 @@
 // scan_bwd.hip -- gated linear recurrence: the backward pass (see scan_impl.hpp).
 //
-// Measured, with the fill of the chain: 4 x 4,096 tokens of 2,048 channels, log gates coupled:
-// bf16 98 us (3.4 TB/s), bf16 with fp32 gates 114 us (4.1), fp32 138 us (4.9); 65,536 of 2,032 bf16
-// 402 us (3.3) and fp32 516 us (5.2).  The inputs of a block and both of its decays and factors
-// stay in registers (160 to 233), which leaves one workgroup to a compute unit: forcing two spills,
-// and forming the factors again behind the wait costs more than it frees (95 us to 111 and more).
+// Measured, back to back through the binding, so with the fill of the chain: 4 x 4,096 tokens of 2,048
+// channels, log gates coupled: bf16 101 us (3.3 TB/s), bf16 with fp32 gates 114 us (4.1), fp32 138 us
+// (4.9); value gates: 83 us (4.0), 102 us (4.6), 131 us (5.1); 65,536 of 2,032, value gates: bf16 356 us
+// (3.7) and fp32 496 us (5.4).  Packed, 37 sequences of 20,000 x 1,000, beta: bf16 113 us (57 of data), fp32
+// 159 us (114; 133 unpacked).  65,536 of 231 bf16 64 us, of 232 50 us.
+// The inputs of a block and both of its decays and factors stay in registers (160 to 233), which leaves one
+// workgroup to a compute unit.  Forcing two spills; forming the factors of log gates again behind the wait
+// costs more than it frees (95 us to 111 and more), which was not tried with value gates, where a factor
+// is a shift or a difference; nor was keeping inputs in shared memory over the wait.
 #include "scan_impl.hpp"
 
 namespace gdr {

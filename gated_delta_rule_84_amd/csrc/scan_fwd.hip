@@ -1,8 +1,11 @@
 // scan_fwd.hip -- gated linear recurrence: the forward pass (see scan_impl.hpp).
 //
-// Measured, with the fill of the chain: 4 x 4,096 tokens of 2,048 channels, log gates coupled:
-// bf16 48 us (4.1 TB/s), bf16 with fp32 gates 55 us (4.9), fp32 86 us (4.7); 65,536 of 2,032 bf16
-// 204 us (3.9) and fp32 294 us (5.4); 65,536 of 128 bf16 28 us, of which the chain is two thirds.
+// Measured, back to back through the binding, so with the fill of the chain: 4 x 4,096 tokens of 2,048
+// channels, log gates coupled: bf16 50 us (4.0 TB/s), bf16 with fp32 gates 56 to 62 us (4.3 to 4.8), fp32
+// 86 us (4.7); 65,536 of 2,032 bf16 202 us (4.0) and fp32 298 us (5.4).  Bound by the chain: 65,536 of 128
+// bf16 29 us (10 us of data), 400,000 of 40 bf16 79 us (20).  Packed, 37 sequences of 20,000 x 1,000, beta:
+// fp32 96 to 103 us (65 of data; 74 unpacked), bf16 66 us (33).  Channels whose number is not a multiple of
+// 4 go element by element in the last tile: 65,536 of 231 bf16 42 us, of 232 35 us.
 // 128 registers (launch bounds of 4 waves per SIMD) keep two workgroups on a compute unit, so that
 // one loads while the other waits for the chain.
 #include "scan_impl.hpp"

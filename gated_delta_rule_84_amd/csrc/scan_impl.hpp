@@ -19,8 +19,8 @@
 // read once.  The strands' maps are composed over a wave by shuffles, over the 8 waves in shared
 // memory and over the blocks of a sequence by the chain below.
 //
-// Bound by HBM: forward 2 to 4 streams over the tokens for some 25 operations per element,
-// backward 5 to 7; where few channels leave few workgroups, by the chain.  Smaller blocks (128
+// Bound by HBM: forward 3 or 4 streams over the tokens for some 25 operations per element,
+// backward 5 or 7; where few channels leave few workgroups, by the chain.  Smaller blocks (128
 // tokens) or larger ones (512, or 16 tokens per lane), 8 channels per lane and a fixed tile of
 // columns per L2 cache were slower or no faster.
 #pragma once
@@ -159,7 +159,7 @@ struct States {
     }
 };
 
-// exp(x) and 1 - exp(x), both to about 2 units in the last place, for x in -88 .. 88 (below, 0 and 1;
+// exp(x) and 1 - exp(x), both to 2 units in the last place, by Cody and Waite's two-part reduction, for x in -88 .. 88 (below, 0 and 1;
 // above, as at 88).  With n = rint(x / ln 2) and r = x - n ln 2 (ln 2 in two parts), exp(x) = s + s q
 // and exp(x) - 1 = (s - 1) + s q for s = 2^n and q = exp(r) - 1, a polynomial on |r| <= 0.35 whose
 // first term left out is r^8 / 8! < 2^-26 r.  For x near 0, where 1 - exp(x) would cancel, s = 1 and
@@ -270,7 +270,8 @@ struct Marks {
 };
 
 // ---------------------------------------------------------------------------
-// The chain of blocks.  Every block publishes its composed map as soon as it has it.  The last block
+// The chain of blocks: the single-pass scan with decoupled look-back (Merrill and Garland, 2016), with
+// affine maps in the place of sums and groups of blocks as a second level.  Every block publishes its composed map as soon as it has it.  The last block
 // of each group composes the group's map from them and publishes that, and the state behind
 // the group once it is known.  A block takes the state behind the nearest group before it whose state
 // is there, applies the maps of the groups in between and then those of its own group's blocks.  What
@@ -279,7 +280,8 @@ struct Marks {
 // of 4 / 6 / 8 blocks: 65,536 tokens of 128 channels 36.6 / 31.2 / 28.7 us, 400,000 of 40 channels
 // 142 / 106 / 89 us, against 298 / 298 / 304 us for 65,536 of 4,096, where the data is what counts.
 // The backward kernel loses 3 % of its rate on 65,536 x 2,032 with groups of 8 (371 against 358 us),
-// nothing with 6, and the packed forward kernel, whose registers are all in use, spills with more than 4.
+// nothing with 6.  The packed forward kernel has all of its 128 registers in use with 4 (its fp32 forms with
+// beta spill 11 of them, and 16 with log gates as well) and would spill more with larger groups.
 // Words are stored and loaded whole with relaxed atomics that all eight L2 caches see; a word is there
 // once it is no longer kNone, which no value is stored as, so no order between words matters.
 // Blocks are numbered by a counter when they begin: every block before a waiting one is running or

@@ -93,8 +93,8 @@ typedef enum gdr_beta_mode { GDR_BETA_SCALAR = 0, GDR_BETA_SHARED = 1, GDR_BETA_
 #define GDR_FLAG_UNDECAYED_PREDICTION 0x20
 
 /* Flags of the gated linear recurrence (gdr_scan_fwd, gdr_scan_bwd, gdr_scan_step) only:
- *   LOG_GATE:   alpha holds the logarithm of the decay, a = exp(alpha); below -88 (-inf) it is a decay of 0, and
- *               values above 88 act as 88
+ *   LOG_GATE:   alpha holds the logarithm of the decay, a = exp(alpha); below -88 (-inf) it is a decay of 0, which
+ *               decays under fp32's normal range (from about -87.3) may be too, and values above 88 act as 88
  *   COUPLED:    the input factor is b = 1 - a (beta must be NULL) */
 #define GDR_FLAG_LOG_GATE 0x40
 #define GDR_FLAG_COUPLED 0x80
