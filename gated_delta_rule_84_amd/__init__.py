@@ -35,6 +35,8 @@ GDR_FLAG_LOG_GATE, GDR_FLAG_COUPLED = 0x40, 0x80
 GDR_NORM_NONE, GDR_NORM_L2, GDR_NORM_RMS = 0, 1, 2
 GDR_ROT_HALF, GDR_ROT_INTERLEAVED = 0, 1
 GDR_SCAN_BLOCK = 256
+GDR_DELTA_CHUNK = 64
+GDR_ACT_LINEAR, GDR_ACT_SIGMOID, GDR_ACT_SILU = 0, 1, 2
 PATH_MFMA, PATH_VALU = 1, 2
 
 
@@ -53,6 +55,21 @@ class QkDesc(ctypes.Structure):
                                                "rot_dim")]
                 + [(n, ctypes.c_float) for n in ("eps", "q_scale", "rot_scale")]
                 + [(n, ctypes.c_int64) for n in ("ldq", "ldk")])
+
+
+class DeltaDesc(ctypes.Structure):
+    """Mirror of ``gdr_delta_desc``."""
+
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "Hk", "Hv", "dk", "dv", "io_dtype", "gate_dtype")]
+                + [(n, ctypes.c_int64) for n in ("ldq", "ldk", "ldv", "ldg", "ldb")])
+
+
+class BlockNormDesc(ctypes.Structure):
+    """Mirror of ``gdr_block_norm_desc``."""
+
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "H", "d", "io_dtype", "weight_dtype", "norm", "next_norm", "act")]
+                + [(n, ctypes.c_float) for n in ("eps", "scale", "res_scale")]
+                + [(n, ctypes.c_int64) for n in ("ldx", "ldg", "ldr")])
 
 
 if not os.path.exists(LIB_PATH):
@@ -115,6 +132,22 @@ _lib.gdr_scan_bwd.argtypes = [_dp] + _rows + [_vp, ctypes.c_int32] + [_vp] * 8 +
 _lib.gdr_scan_bwd.restype = ctypes.c_int
 _lib.gdr_scan_step.argtypes = [_dp] + _rows + [_vp] * 2 + [_vp]
 _lib.gdr_scan_step.restype = ctypes.c_int
+_ddp = ctypes.POINTER(DeltaDesc)
+_lib.gdr_delta_workspace_size.argtypes = [_ddp, ctypes.c_int32, ctypes.c_int32]
+_lib.gdr_delta_workspace_size.restype = ctypes.c_size_t
+_lib.gdr_delta_fwd.argtypes = [_ddp] + [_vp] * 6 + [ctypes.c_int32] + [_vp] * 4 + [_vp, ctypes.c_size_t, _vp]
+_lib.gdr_delta_fwd.restype = ctypes.c_int
+_lib.gdr_delta_bwd.argtypes = [_ddp] + [_vp] * 6 + [ctypes.c_int32] + [_vp] * 9 + [_vp, ctypes.c_size_t, _vp]
+_lib.gdr_delta_bwd.restype = ctypes.c_int
+_lib.gdr_delta_step.argtypes = [_ddp] + [_vp] * 7 + [_vp]
+_lib.gdr_delta_step.restype = ctypes.c_int
+_np = ctypes.POINTER(BlockNormDesc)
+_lib.gdr_block_norm_fwd.argtypes = [_np] + [_vp] * 7 + [_vp]
+_lib.gdr_block_norm_fwd.restype = ctypes.c_int
+_lib.gdr_block_norm_bwd_workspace_size.argtypes = [_np]
+_lib.gdr_block_norm_bwd_workspace_size.restype = ctypes.c_size_t
+_lib.gdr_block_norm_bwd.argtypes = [_np] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
+_lib.gdr_block_norm_bwd.restype = ctypes.c_int
 
 EXPORTED = ("gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd", "gdr_decode_step", "gdr_chunk_fwd_path",
             "gdr_status_string", "gdr_version", "gdr_chunk_fwd_ckpt", "gdr_mc_readout_workspace_size",
@@ -122,7 +155,8 @@ EXPORTED = ("gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd", "gdr_decode_step", 
             "gdr_sdm_workspace_size", "gdr_sdm_fwd", "gdr_context_create", "gdr_context_destroy",
             "gdr_chunk_fwd_noalloc", "gdr_dmem_fwd", "gdr_chunk_fwd_ctx", "gdr_qk_prep_fwd",
             "gdr_qk_prep_bwd_workspace_size", "gdr_qk_prep_bwd", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_bwd",
-            "gdr_scan_step")
+            "gdr_scan_step", "gdr_delta_workspace_size", "gdr_delta_fwd", "gdr_delta_bwd", "gdr_delta_step",
+            "gdr_block_norm_fwd", "gdr_block_norm_bwd_workspace_size", "gdr_block_norm_bwd")
 
 
 class GdrError(RuntimeError):
@@ -532,6 +566,121 @@ def gdr_scan_step(desc: Desc, x, ldx: int, alpha, lda: int, beta, ldb: int, S, y
                                   _stream(stream)))
 
 
+def gdr_delta_workspace_size(desc: DeltaDesc, n_seq: int = 0, backward: bool = False) -> int:
+    return int(_lib.gdr_delta_workspace_size(ctypes.byref(desc), int(n_seq), int(backward)))
+
+
+def delta_chunks(desc: DeltaDesc, n_seq=None) -> int:
+    """Chunks of a call, the first axis of its ckpt; n_seq None where the rows are not packed."""
+    if n_seq is None:
+        return desc.B * ((desc.T + GDR_DELTA_CHUNK - 1) // GDR_DELTA_CHUNK)
+    return desc.T // GDR_DELTA_CHUNK + int(n_seq) if desc.T > 0 else 0
+
+
+def _delta_kinds(desc: DeltaDesc, rows: int, n_seq):
+    """(count, dtype) of q and k, v, the gates, the states, ckpt and offsets; None for a descriptor that the library
+    rejects."""
+    io, gt = _TORCH_DTYPE.get(desc.io_dtype), _TORCH_DTYPE.get(desc.gate_dtype)
+    n = 0 if n_seq is None else int(n_seq)
+    if io is None or gt is None or min(desc.B, desc.T, desc.Hk, desc.Hv, desc.dk, desc.dv, n) < 0:
+        return None
+    f32, square = torch.float32, desc.dk * desc.dv
+    return ((rows * desc.Hk * desc.dk, io), (rows * desc.Hv * desc.dv, io), (rows * desc.Hv, gt),
+            ((desc.B if n_seq is None else n) * desc.Hv * square, f32),
+            (delta_chunks(desc, n_seq) * desc.Hv * (desc.dk + GDR_DELTA_CHUNK) * desc.dv, f32), (n + 1, torch.int32))
+
+
+def _addr_flat(name: str, t, ld: int, inner: int):
+    """_addr of a tensor whose last axis alone is a row (gates [.., H])."""
+    return _addr(name, t.unsqueeze(-1) if isinstance(t, torch.Tensor) else t, ld, inner)
+
+
+def _delta_rows(desc: DeltaDesc, q, k, v, log_gate, beta):
+    key, value = desc.Hk * desc.dk, desc.Hv * desc.dv
+    return (_addr("q", q, desc.ldq, key), _addr("k", k, desc.ldk, key), _addr("v", v, desc.ldv, value),
+            _addr_flat("log_gate", log_gate, desc.ldg, desc.Hv), _addr_flat("beta", beta, desc.ldb, desc.Hv))
+
+
+def gdr_delta_fwd(desc: DeltaDesc, q, k, v, log_gate, beta, seq_off, n_seq: int, S0, o, ST, ckpt, workspace,
+                  workspace_bytes: int, stream=None) -> int:
+    kinds = _delta_kinds(desc, desc.B * desc.T, None if seq_off is None else n_seq)
+    if kinds is not None:
+        key, value, gate, state, blocks, offsets = kinds
+        _check_all((("q", q) + key, ("k", k) + key, ("v", v) + value, ("log_gate", log_gate) + gate, ("beta", beta) + gate,
+                    ("o", o) + value, ("S0", S0) + state, ("ST", ST) + state, ("ckpt", ckpt) + blocks,
+                    ("seq_off", seq_off) + offsets))
+    _check_workspace(workspace, workspace_bytes)
+    return int(_lib.gdr_delta_fwd(ctypes.byref(desc), *_delta_rows(desc, q, k, v, log_gate, beta), _ptr(seq_off), int(n_seq),
+                                  _ptr(S0), _ptr(o), _ptr(ST), _ptr(ckpt), _ptr(workspace), int(workspace_bytes),
+                                  _stream(stream)))
+
+
+def gdr_delta_bwd(desc: DeltaDesc, q, k, v, log_gate, beta, seq_off, n_seq: int, ckpt, d_o, dST, dq, dk, dv, dlog_gate, dbeta,
+                  dS0, workspace, workspace_bytes: int, stream=None) -> int:
+    kinds = _delta_kinds(desc, desc.B * desc.T, None if seq_off is None else n_seq)
+    if kinds is not None:
+        key, value, gate, state, blocks, offsets = kinds
+        _check_all((("q", q) + key, ("k", k) + key, ("v", v) + value, ("log_gate", log_gate) + gate, ("beta", beta) + gate,
+                    ("d_o", d_o) + value, ("dq", dq) + key, ("dk", dk) + key, ("dv", dv) + value,
+                    ("dlog_gate", dlog_gate) + gate, ("dbeta", dbeta) + gate, ("dST", dST) + state, ("dS0", dS0) + state,
+                    ("ckpt", ckpt) + blocks, ("seq_off", seq_off) + offsets))
+    _check_workspace(workspace, workspace_bytes)
+    return int(_lib.gdr_delta_bwd(ctypes.byref(desc), *_delta_rows(desc, q, k, v, log_gate, beta), _ptr(seq_off), int(n_seq),
+                                  _ptr(ckpt), _ptr(d_o), _ptr(dST), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog_gate), _ptr(dbeta),
+                                  _ptr(dS0), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def gdr_delta_step(desc: DeltaDesc, q, k, v, log_gate, beta, S, o, stream=None) -> int:
+    kinds = _delta_kinds(desc, desc.B, None)
+    if kinds is not None:
+        key, value, gate, state = kinds[:4]
+        _check_all((("q", q) + key, ("k", k) + key, ("v", v) + value, ("log_gate", log_gate) + gate, ("beta", beta) + gate,
+                    ("S", S) + state, ("o", o) + value))
+    return int(_lib.gdr_delta_step(ctypes.byref(desc), *_delta_rows(desc, q, k, v, log_gate, beta), _ptr(S), _ptr(o),
+                                   _stream(stream)))
+
+
+def _norm_kinds(desc: BlockNormDesc):
+    """(count, dtype) of the rows, the weights and their gradients; None for a descriptor that the library rejects."""
+    io, wt = _TORCH_DTYPE.get(desc.io_dtype), _TORCH_DTYPE.get(desc.weight_dtype)
+    if io is None or wt is None or min(desc.B, desc.T, desc.H, desc.d) < 0:
+        return None
+    return (desc.B * desc.T * desc.H * desc.d, io), (desc.d, wt), (desc.d, torch.float32)
+
+
+def _norm_rows(desc: BlockNormDesc, x, gate, residual):
+    D = desc.H * desc.d
+    return _addr("x", x, desc.ldx, D), _addr("gate", gate, desc.ldg, D), _addr("residual", residual, desc.ldr, D)
+
+
+def gdr_block_norm_fwd(desc: BlockNormDesc, x, gate, residual, w, w_next, y, n, stream=None) -> int:
+    kinds = _norm_kinds(desc)
+    if kinds is not None:
+        io, wt, _ = kinds
+        _check_all((("x", x) + io, ("gate", gate) + io, ("residual", residual) + io, ("w", w) + wt, ("w_next", w_next) + wt,
+                    ("y", y) + io, ("n", n) + io))
+    return int(_lib.gdr_block_norm_fwd(ctypes.byref(desc), *_norm_rows(desc, x, gate, residual), _ptr(w), _ptr(w_next), _ptr(y),
+                                       _ptr(n), _stream(stream)))
+
+
+def gdr_block_norm_bwd_workspace_size(desc: BlockNormDesc) -> int:
+    return int(_lib.gdr_block_norm_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def gdr_block_norm_bwd(desc: BlockNormDesc, x, gate, residual, w, w_next, dy, dn, dx, dgate, dresidual, dw, dw_next, workspace,
+                       workspace_bytes: int, stream=None) -> int:
+    kinds = _norm_kinds(desc)
+    if kinds is not None:
+        io, wt, sums = kinds
+        _check_all((("x", x) + io, ("gate", gate) + io, ("residual", residual) + io, ("w", w) + wt, ("w_next", w_next) + wt,
+                    ("dy", dy) + io, ("dn", dn) + io, ("dx", dx) + io, ("dgate", dgate) + io, ("dresidual", dresidual) + io,
+                    ("dw", dw) + sums, ("dw_next", dw_next) + sums))
+    _check_workspace(workspace, workspace_bytes)
+    return int(_lib.gdr_block_norm_bwd(ctypes.byref(desc), *_norm_rows(desc, x, gate, residual), _ptr(w), _ptr(w_next), _ptr(dy),
+                                       _ptr(dn), _ptr(dx), _ptr(dgate), _ptr(dresidual), _ptr(dw), _ptr(dw_next),
+                                       _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
 # ---------------------------------------------------------------------------
 # convenience wrappers (allocate outputs, raise on error)
 # ---------------------------------------------------------------------------
@@ -902,6 +1051,144 @@ def scan_step(S, x, alpha, *, beta=None, log_gate=False, coupled=False, out=None
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_scan_step")
     return y
+
+
+def _ld(name, t, inner) -> int:
+    return 0 if t is None or t.is_contiguous() else _row_stride(name, t, inner)
+
+
+def _delta_desc(q, k, v, log_gate, beta, step=False) -> DeltaDesc:
+    lead = 1 if step else 2
+    qs, vs = tuple(q.shape), tuple(v.shape)
+    if (len(qs) != lead + 2 or tuple(k.shape) != qs or len(vs) != lead + 2 or vs[:lead] != qs[:lead]
+            or tuple(log_gate.shape) != vs[:-1] or tuple(beta.shape) != vs[:-1]):
+        T = "" if step else "T, "
+        raise ValueError(f"expected q, k [B, {T}Hk, dk], v [B, {T}Hv, dv] and log_gate, beta [B, {T}Hv], got {qs}, "
+                         f"{tuple(k.shape)}, {vs}, {tuple(log_gate.shape)} and {tuple(beta.shape)}")
+    if k.dtype != q.dtype or v.dtype != q.dtype or log_gate.dtype != beta.dtype:
+        raise ValueError(f"q, k and v must have one type, and log_gate and beta, got {q.dtype}, {k.dtype}, {v.dtype}, "
+                         f"{log_gate.dtype} and {beta.dtype}")
+    Hk, dk, Hv, dv = qs[-2], qs[-1], vs[-2], vs[-1]
+    return DeltaDesc(qs[0], 1 if step else qs[1], Hk, Hv, dk, dv, _dtype_code(q), _dtype_code(log_gate), _ld("q", q, Hk * dk),
+                     _ld("k", k, Hk * dk), _ld("v", v, Hv * dv), _ld("log_gate", log_gate.unsqueeze(-1), Hv),
+                     _ld("beta", beta.unsqueeze(-1), Hv))
+
+
+def _packed(seq_offsets):
+    return None if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
+
+
+@_on_its_stream
+def delta_fwd(q, k, v, log_gate, beta, *, S0=None, seq_offsets=None, want_state=True, want_ckpt=False, workspace=None,
+              stream=None):
+    """Trainable delta rule S = a S + beta k (v - a S^T k)^T, o = S^T q with a = exp(log_gate), every product and state at
+    fp32's precision.
+
+    q, k [B, T, Hk, dk], v [B, T, Hv, dv], log_gate, beta [B, T, Hv], Hv a multiple of Hk; all may be slices of a fused
+    projection's output.  seq_offsets [n + 1] int32 cuts the T rows of a B = 1 batch into packed sequences; S0
+    [B or n, Hv, dk, dv] fp32.  Returns (o like v, ST like S0 or None, ckpt [chunks, Hv, dk + 64, dv] fp32 for delta_bwd or
+    None).  Rows of o that belong to no packed sequence are left unwritten."""
+    desc, n = _delta_desc(q, k, v, log_gate, beta), _packed(seq_offsets)
+    f32 = torch.float32
+    o = v.new_empty(v.shape)
+    ST = v.new_empty((desc.B if n is None else n, desc.Hv, desc.dk, desc.dv), dtype=f32) if want_state else None
+    ckpt = v.new_empty((delta_chunks(desc, n), desc.Hv, desc.dk + GDR_DELTA_CHUNK, desc.dv), dtype=f32) if want_ckpt else None
+    workspace = _room(workspace, gdr_delta_workspace_size(desc, n or 0), v.device)
+    rc = gdr_delta_fwd(desc, q, k, v, log_gate, beta, seq_offsets, n or 0, S0, o, ST, ckpt, workspace, _nbytes(workspace), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_delta_fwd")
+    return o, ST, ckpt
+
+
+@_on_its_stream
+def delta_bwd(q, k, v, log_gate, beta, d_o, ckpt, *, dST=None, seq_offsets=None, want_dS0=True, workspace=None, stream=None):
+    """Backward pass of delta_fwd with its inputs and its ckpt: gradients d_o of o (dense) and dST of ST.
+    Returns (dq, dk, dv, dlog_gate, dbeta, dS0 or None), dense, in their inputs' types; dS0 fp32."""
+    desc, n = _delta_desc(q, k, v, log_gate, beta), _packed(seq_offsets)
+    dq, dk, dv, dg, db = (t.new_empty(t.shape) for t in (q, k, v, log_gate, beta))
+    dS0 = (v.new_empty((desc.B if n is None else n, desc.Hv, desc.dk, desc.dv), dtype=torch.float32) if want_dS0 else None)
+    workspace = _room(workspace, gdr_delta_workspace_size(desc, n or 0, True), v.device)
+    rc = gdr_delta_bwd(desc, q, k, v, log_gate, beta, seq_offsets, n or 0, ckpt, d_o, dST, dq, dk, dv, dg, db, dS0, workspace,
+                       _nbytes(workspace), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_delta_bwd")
+    return dq, dk, dv, dg, db, dS0
+
+
+@_on_its_stream
+def delta_step(S, q, k, v, log_gate, beta, *, out=None, stream=None):
+    """One token of the delta rule for every sequence: q, k [B, Hk, dk], v [B, Hv, dv], log_gate, beta [B, Hv]; S
+    [B, Hv, dk, dv] fp32 is updated in place.  Returns o [B, Hv, dv]."""
+    desc = _delta_desc(q, k, v, log_gate, beta, step=True)
+    o = out if out is not None else v.new_empty(v.shape)
+    rc = gdr_delta_step(desc, q, k, v, log_gate, beta, S, o, stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_delta_step")
+    return o
+
+
+_ACTS = {"none": None, None: None, "linear": GDR_ACT_LINEAR, "sigmoid": GDR_ACT_SIGMOID, "silu": GDR_ACT_SILU}
+
+
+def _norm_desc(x, norm, weight, gate, act, scale, residual, res_scale, eps, next_norm, next_weight) -> BlockNormDesc:
+    if norm not in _NORMS or next_norm not in _NORMS:
+        raise ValueError(f"norm and next_norm must be None, 'none', 'l2' or 'rms', got {norm!r} and {next_norm!r}")
+    if act not in _ACTS:
+        raise ValueError(f"act must be None, 'none', 'linear', 'sigmoid' or 'silu', got {act!r}")
+    if (gate is None) != (_ACTS[act] is None):
+        raise ValueError(f"a gate needs an act, and an act a gate, got act {act!r}")
+    shape = tuple(x.shape)
+    if len(shape) != 4:
+        raise ValueError(f"expected x [B, T, H, d], got {shape}")
+    for name, t in (("gate", gate), ("residual", residual)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != x.dtype):
+            raise ValueError(f"{name}: expected {shape} {x.dtype} like x, got {tuple(t.shape)} {t.dtype}")
+    if weight is not None and next_weight is not None and weight.dtype != next_weight.dtype:
+        raise ValueError(f"weight and next_weight must have one type, got {weight.dtype} and {next_weight.dtype}")
+    B, T, H, d = shape
+    w = weight if weight is not None else next_weight
+    return BlockNormDesc(B, T, H, d, _dtype_code(x), GDR_F32 if w is None else _dtype_code(w), _NORMS[norm], _NORMS[next_norm],
+                         _ACTS[act] or 0, eps, scale, res_scale, _ld("x", x, H * d), _ld("gate", gate, H * d),
+                         _ld("residual", residual, H * d))
+
+
+@_on_its_stream
+def block_norm(x, *, norm="rms", weight=None, gate=None, act=None, scale=1.0, residual=None, res_scale=1.0, eps=1e-6,
+               next_norm=None, next_weight=None, out=None, stream=None):
+    """Norm behind a block with its gate and the scaled residual, and the norm in front of the next block, in one pass:
+
+        y = res_scale * residual + scale * act(gate) * weight * norm(x),   n = next_weight * next_norm(y)
+
+    over the d channels of every row of x [B, T, H, d] (the heads of the delta rule's output, or H = 1 for whole rows).
+    norm and next_norm None, "l2" or "rms"; act of the gate "linear", "sigmoid" or "silu"; gate and residual like x, slices of
+    a fused projection's output allowed; weights [d].  Returns (y, n or None), dense; `out` a tensor to write y to (the
+    residual itself where dense)."""
+    desc = _norm_desc(x, norm, weight, gate, act, scale, residual, res_scale, eps, next_norm, next_weight)
+    y = out if out is not None else x.new_empty(x.shape)
+    n = x.new_empty(x.shape) if desc.next_norm else None
+    rc = gdr_block_norm_fwd(desc, x, gate, residual, weight, next_weight, y, n, stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_block_norm_fwd")
+    return y, n
+
+
+@_on_its_stream
+def block_norm_bwd(x, dy, *, dn=None, norm="rms", weight=None, gate=None, act=None, scale=1.0, residual=None, res_scale=1.0,
+                   eps=1e-6, next_norm=None, next_weight=None, workspace=None, stream=None):
+    """Backward pass of block_norm, from its inputs and the (dense) gradients dy of y and dn of n.
+    Returns (dx, dgate, dresidual, dweight, dnext_weight): dense gradients in x's type, weight gradients [d] in fp32,
+    None for what was not given."""
+    desc = _norm_desc(x, norm, weight, gate, act, scale, residual, res_scale, eps, next_norm, next_weight)
+    dx = x.new_empty(x.shape)
+    dgate, dres = (None if t is None else x.new_empty(x.shape) for t in (gate, residual))
+    dw, dw_next = (None if w is None else w.new_empty(w.shape, dtype=torch.float32) for w in (weight, next_weight))
+    if dw is not None or dw_next is not None:
+        workspace = _room(workspace, gdr_block_norm_bwd_workspace_size(desc), x.device)
+    rc = gdr_block_norm_bwd(desc, x, gate, residual, weight, next_weight, dy, dn, dx, dgate, dres, dw, dw_next, workspace,
+                            _nbytes(workspace), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_block_norm_bwd")
+    return dx, dgate, dres, dw, dw_next
 
 
 def loaded_library_path() -> str:

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libgdr.so")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["gdr_api.hip", "decode.hip", "chunk_valu.hip", "chunk_mfma.hip", "mc_readout.hip", "osdn_precond.hip", "sdm.hip", "dmem.hip",
-           "mixer_api.hip", "qk_prep.hip", "scan_fwd.hip", "scan_bwd.hip", "scan.hip"]
+           "mixer_api.hip", "qk_prep.hip", "scan_fwd.hip", "scan_bwd.hip", "scan.hip", "delta_prep.hip", "delta_chain.hip", "delta_grad.hip", "delta_step.hip",
+           "block_norm.hip", "delta_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

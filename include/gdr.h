@@ -512,6 +512,139 @@ int gdr_scan_bwd(const gdr_desc *desc, const void *x, int64_t ldx, const void *a
 int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *alpha, int64_t lda, const void *beta,
                   int64_t ldb, float *S, void *y, void *stream);
 
+/*
+ * Trainable delta rule: the scalar-gate recurrence of gdr_chunk_fwd (w = beta k, vh = beta-free v),
+ *
+ *     S_t = a_t S_{t-1} + beta_t k_t (v_t - a_t S_{t-1}^T k_t)^T,   o_t = S_t^T q_t
+ *
+ * with a = exp(log_gate), over dense batches or packed sequences, with key heads shared by groups of value
+ * heads, inputs that may be slices of a fused projection's output, and a backward pass.  Every product and
+ * state keeps fp32's precision whatever the types; outputs are rounded once.  (gdr_chunk_fwd is the forward pass of
+ * dense batches at the precision of its two-term states, and takes gates per channel, write keys and gates of the value.)
+ *
+ * A log gate of -inf is a hard reset: the state before it is forgotten, and the gate's gradient is 0.  Gates above
+ * 0 grow the state; where a product of gates passes fp32's range the results are not finite.  NaN and infinities in
+ * q, k, v or beta make the results of their sequence and head (and, in the gradients of q and k, of the heads that share
+ * them) up to its end, or start in the backward pass, not finite.
+ */
+#define GDR_DELTA_CHUNK 64
+
+/* Descriptor of the trainable delta rule.
+ *   B, T >= 0 (T is ignored by a step), Hk >= 0 key heads, Hv a multiple of Hk (else GDR_EINVAL): value head h goes with
+ *            key head h / (Hv / Hk)
+ *   dk, dv   multiples of 8 in [8, 128]                        (else GDR_EUNSUPPORTED)
+ *   io_dtype: q, k, v, o and their gradients;  gate_dtype: log_gate, beta and their gradients
+ *   ldq, ldk, ldv, ldg, ldb  elements between successive tokens (b, t) of q, k, v, log_gate and beta; 0 means dense,
+ *            larger for slices of a fused projection's output
+ * B * T below 2^30, heads at most 65536, and chunks times value heads times 512 below 2^32 (else GDR_EUNSUPPORTED); chunks
+ * are B * ceil(T / 64), or floor(T / 64) + n_seq when packed. */
+typedef struct gdr_delta_desc {
+    int32_t B, T, Hk, Hv, dk, dv;
+    int32_t io_dtype;
+    int32_t gate_dtype;
+    int64_t ldq, ldk, ldv, ldg, ldb;
+} gdr_delta_desc;
+
+/*
+ *   q, k      [B, T, Hk, dk], v [B, T, Hv, dv]  io_dtype, heads and channels dense
+ *   log_gate, beta  [B, T, Hv] gate_dtype
+ *   seq_off   NULL, or [n_seq + 1] int32 on the device with B == 1: sequence i is the rows seq_off[i] .. seq_off[i + 1] - 1
+ *             of the T packed ones.  The offsets must not decrease and lie in 0 .. T; a sequence may be empty; rows before
+ *             the first and behind the last one are left as they were, and what they hold does not matter.  Offsets that
+ *             break this give undefined values in the outputs, and no access outside the tensors.  n_seq is 0 with a NULL
+ *             seq_off.
+ *   S0, ST    [B, Hv, dk, dv] fp32 ([n_seq, ...] when packed): state before and after each sequence; S0 NULL means zero,
+ *             ST NULL not written, ST == S0 is allowed (in-place resume) without seq_off; an empty sequence gives ST = S0
+ *   o         [B, T, Hv, dv] io_dtype, dense
+ *   ckpt      NULL, or [chunks, Hv, dk + GDR_DELTA_CHUNK, dv] fp32: of each chunk of 64 tokens the state before it and
+ *             what its tokens write, for the backward pass; chunks that hold no rows are not written.  A sequence's chunks
+ *             begin at its first row.
+ *   workspace at least gdr_delta_workspace_size(desc, n_seq, 0) bytes, 16-byte aligned; its contents on entry do not matter.
+ *             n_seq is 0 for dense batches.  One workspace serves one call at a time: calls, or graphs, that may run at the
+ *             same time need one each.
+ * Pointers need their element's alignment only, S0, ST, ckpt, dST and dS0 16 bytes.  Outputs overlap no input and no
+ * other output.  Results are deterministic.
+ */
+size_t gdr_delta_workspace_size(const gdr_delta_desc *desc, int32_t n_seq, int32_t backward);
+int gdr_delta_fwd(const gdr_delta_desc *desc, const void *q, const void *k, const void *v, const void *log_gate,
+                  const void *beta, const int32_t *seq_off, int32_t n_seq, const float *S0, void *o, float *ST, float *ckpt,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its backward pass, with the inputs of the forward call and the ckpt that it wrote.
+ *   d_o       [B, T, Hv, dv] io_dtype, dense: gradient of o;  dST: gradient of ST, or NULL for zero
+ *   dq, dk, dv  like q, k, v, dense (those of a shared key head summed over its value heads);  dlog_gate, dbeta
+ *             [B, T, Hv] gate_dtype, dense;  dS0 like S0, or NULL.  Rows in no sequence are not written.
+ *   workspace at least gdr_delta_workspace_size(desc, n_seq, 1) bytes, 16-byte aligned
+ */
+int gdr_delta_bwd(const gdr_delta_desc *desc, const void *q, const void *k, const void *v, const void *log_gate,
+                  const void *beta, const int32_t *seq_off, int32_t n_seq, const float *ckpt, const void *d_o, const float *dST,
+                  void *dq, void *dk, void *dv, void *dlog_gate, void *dbeta, float *dS0, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * One token for every sequence, applied in place to a resident state: q, k [B, Hk, dk], v [B, Hv, dv], log_gate, beta
+ * [B, Hv] (ld* elements between sequences), S [B, Hv, dk, dv] fp32 read and overwritten (16-byte aligned), o [B, Hv, dv]
+ * io_dtype, dense.  desc->T is ignored.
+ */
+int gdr_delta_step(const gdr_delta_desc *desc, const void *q, const void *k, const void *v, const void *log_gate,
+                   const void *beta, float *S, void *o, void *stream);
+
+/*
+ * Block norm: the norm behind a block with its gate and the scaled residual, and the norm in front of the next
+ * block, in one pass.  For each row x (d channels of one head of one token; the gated norm of the delta rule's heads,
+ * or with H = 1 the join of a block's output with the residual stream)
+ *
+ *     r = (sum x^2 + eps)^(-1/2) GDR_NORM_L2, (mean x^2 + eps)^(-1/2) GDR_NORM_RMS, 1 GDR_NORM_NONE
+ *     h = res_scale residual + scale act(gate) (.) w (.) r x        factors that are NULL are left out
+ *     y = h,   n = w_next (.) r' h                                   r' likewise from h, by next_norm
+ *
+ * r is 0 where its bracket is 0.  n is formed from h before h is rounded.  Sums are formed in fp32.
+ */
+typedef enum gdr_act { GDR_ACT_LINEAR = 0, GDR_ACT_SIGMOID = 1, GDR_ACT_SILU = 2 } gdr_act;
+
+/* Descriptor of a block norm.
+ *   B, T, H >= 0, B * T * H below 2^31;  d a multiple of 8 in [8, 8192]   (else GDR_EUNSUPPORTED)
+ *   next_norm  GDR_NORM_NONE: no n (n and w_next must be NULL)
+ *   act        of the gate (not used without one)
+ *   ldx, ldg, ldr  elements between successive tokens (b, t) of x, gate and residual, 0 for dense (H * d)
+ *   io_dtype: x, gate, residual, y, n and their gradients;  weight_dtype: w, w_next */
+typedef struct gdr_block_norm_desc {
+    int32_t B, T, H, d;
+    int32_t io_dtype;
+    int32_t weight_dtype;
+    int32_t norm;
+    int32_t next_norm;
+    int32_t act;
+    float eps;
+    float scale;
+    float res_scale;
+    int64_t ldx, ldg, ldr;
+} gdr_block_norm_desc;
+
+/*
+ *   x, gate, residual  [B, T, H, d] io_dtype, heads dense; gate and residual may be NULL
+ *   w, w_next  [d] weight_dtype or NULL
+ *   y, n       dense, io_dtype (n required exactly with a next norm).  y may be the residual itself where that is dense;
+ *              outputs overlap nothing else
+ * Pointers need their element's alignment only.
+ */
+int gdr_block_norm_fwd(const gdr_block_norm_desc *desc, const void *x, const void *gate, const void *residual, const void *w,
+                       const void *w_next, void *y, void *n, void *stream);
+
+/*
+ * Its backward pass, from the inputs and the gradients of the outputs:
+ *   dy, dn     dense, io_dtype: gradients of y and n (dn required exactly with a next norm)
+ *   dx, dgate, dresidual  dense, io_dtype (the latter two required exactly with those inputs); overlap nothing else
+ *   dw, dw_next  [d] fp32 or NULL (not computed): sums over every row
+ *   workspace  at least gdr_block_norm_bwd_workspace_size(desc) bytes, 16-byte aligned, when dw or dw_next is given
+ * Results are deterministic.  No rows: dw, dw_next are set to 0.
+ */
+size_t gdr_block_norm_bwd_workspace_size(const gdr_block_norm_desc *desc);
+int gdr_block_norm_bwd(const gdr_block_norm_desc *desc, const void *x, const void *gate, const void *residual, const void *w,
+                       const void *w_next, const void *dy, const void *dn, void *dx, void *dgate, void *dresidual, float *dw,
+                       float *dw_next, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Which prefill kernel `desc` selects: 1 = bf16 matrix-core kernel,
  * 2 = fp32 vector-ALU kernel, or a negative gdr_status if desc is rejected. */
 int gdr_chunk_fwd_path(const gdr_desc *desc);
