@@ -135,6 +135,8 @@ _lib.gdr_scan_step.restype = ctypes.c_int
 _ddp = ctypes.POINTER(DeltaDesc)
 _lib.gdr_delta_workspace_size.argtypes = [_ddp, ctypes.c_int32, ctypes.c_int32]
 _lib.gdr_delta_workspace_size.restype = ctypes.c_size_t
+_lib.gdr_delta_ckpt_size.argtypes = [_ddp, ctypes.c_int32]
+_lib.gdr_delta_ckpt_size.restype = ctypes.c_size_t
 _lib.gdr_delta_fwd.argtypes = [_ddp] + [_vp] * 6 + [ctypes.c_int32] + [_vp] * 4 + [_vp, ctypes.c_size_t, _vp]
 _lib.gdr_delta_fwd.restype = ctypes.c_int
 _lib.gdr_delta_bwd.argtypes = [_ddp] + [_vp] * 6 + [ctypes.c_int32] + [_vp] * 9 + [_vp, ctypes.c_size_t, _vp]
@@ -155,7 +157,7 @@ EXPORTED = ("gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd", "gdr_decode_step", 
             "gdr_sdm_workspace_size", "gdr_sdm_fwd", "gdr_context_create", "gdr_context_destroy",
             "gdr_chunk_fwd_noalloc", "gdr_dmem_fwd", "gdr_chunk_fwd_ctx", "gdr_qk_prep_fwd",
             "gdr_qk_prep_bwd_workspace_size", "gdr_qk_prep_bwd", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_bwd",
-            "gdr_scan_step", "gdr_delta_workspace_size", "gdr_delta_fwd", "gdr_delta_bwd", "gdr_delta_step",
+            "gdr_scan_step", "gdr_delta_workspace_size", "gdr_delta_ckpt_size", "gdr_delta_fwd", "gdr_delta_bwd", "gdr_delta_step",
             "gdr_block_norm_fwd", "gdr_block_norm_bwd_workspace_size", "gdr_block_norm_bwd")
 
 
@@ -570,11 +572,8 @@ def gdr_delta_workspace_size(desc: DeltaDesc, n_seq: int = 0, backward: bool = F
     return int(_lib.gdr_delta_workspace_size(ctypes.byref(desc), int(n_seq), int(backward)))
 
 
-def delta_chunks(desc: DeltaDesc, n_seq=None) -> int:
-    """Chunks of a call, the first axis of its ckpt; n_seq None where the rows are not packed."""
-    if n_seq is None:
-        return desc.B * ((desc.T + GDR_DELTA_CHUNK - 1) // GDR_DELTA_CHUNK)
-    return desc.T // GDR_DELTA_CHUNK + int(n_seq) if desc.T > 0 else 0
+def gdr_delta_ckpt_size(desc: DeltaDesc, n_seq: int = 0) -> int:
+    return int(_lib.gdr_delta_ckpt_size(ctypes.byref(desc), int(n_seq)))
 
 
 def _delta_kinds(desc: DeltaDesc, rows: int, n_seq):
@@ -587,7 +586,7 @@ def _delta_kinds(desc: DeltaDesc, rows: int, n_seq):
     f32, square = torch.float32, desc.dk * desc.dv
     return ((rows * desc.Hk * desc.dk, io), (rows * desc.Hv * desc.dv, io), (rows * desc.Hv, gt),
             ((desc.B if n_seq is None else n) * desc.Hv * square, f32),
-            (delta_chunks(desc, n_seq) * desc.Hv * (desc.dk + GDR_DELTA_CHUNK) * desc.dv, f32), (n + 1, torch.int32))
+            (gdr_delta_ckpt_size(desc, n) // 4, f32), (n + 1, torch.int32))
 
 
 def _addr_flat(name: str, t, ld: int, inner: int):
@@ -1086,13 +1085,12 @@ def delta_fwd(q, k, v, log_gate, beta, *, S0=None, seq_offsets=None, want_state=
 
     q, k [B, T, Hk, dk], v [B, T, Hv, dv], log_gate, beta [B, T, Hv], Hv a multiple of Hk; all may be slices of a fused
     projection's output.  seq_offsets [n + 1] int32 cuts the T rows of a B = 1 batch into packed sequences; S0
-    [B or n, Hv, dk, dv] fp32.  Returns (o like v, ST like S0 or None, ckpt [chunks, Hv, dk + 64, dv] fp32 for delta_bwd or
-    None).  Rows of o that belong to no packed sequence are left unwritten."""
+    [B or n, Hv, dk, dv] fp32.  Returns (o like v, ST like S0 or None, ckpt, a flat fp32 tensor for delta_bwd, or None).  Rows of o that belong to no packed sequence are left unwritten."""
     desc, n = _delta_desc(q, k, v, log_gate, beta), _packed(seq_offsets)
     f32 = torch.float32
     o = v.new_empty(v.shape)
     ST = v.new_empty((desc.B if n is None else n, desc.Hv, desc.dk, desc.dv), dtype=f32) if want_state else None
-    ckpt = v.new_empty((delta_chunks(desc, n), desc.Hv, desc.dk + GDR_DELTA_CHUNK, desc.dv), dtype=f32) if want_ckpt else None
+    ckpt = v.new_empty(gdr_delta_ckpt_size(desc, n or 0) // 4, dtype=f32) if want_ckpt else None
     workspace = _room(workspace, gdr_delta_workspace_size(desc, n or 0), v.device)
     rc = gdr_delta_fwd(desc, q, k, v, log_gate, beta, seq_offsets, n or 0, S0, o, ST, ckpt, workspace, _nbytes(workspace), stream)
     if rc != GDR_OK:

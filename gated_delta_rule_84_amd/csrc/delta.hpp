@@ -29,7 +29,7 @@
 namespace gdr {
 
 constexpr int kDeltaC = 64;        // tokens of a chunk
-constexpr int kDeltaGates = 144;   // floats kept per (slot, value head): front, behind * beta, whole
+constexpr int kDeltaGates = 256;   // floats kept per (slot, value head), a fragment: front, behind * beta, whole
 constexpr int kDeltaTri = 18;      // fragments of a triangular 64 x 64 matrix: 6 places of 3 terms
 
 // Parameters of one call, already validated by the entry points.
@@ -45,7 +45,7 @@ struct DeltaParams {
     const float *S0;
     void *o;
     float *ST;
-    float *ckpt;  // [nslot, Hv, dk + 64, dv]: the state before each chunk and its D; NULL: not kept
+    float *ckpt;  // per (slot, value head) the tiles of the state before the chunk and of its D; NULL: not kept
     const void *dout;
     const float *dST;
     void *dq, *dkk, *dvv, *dg, *db;
@@ -53,7 +53,9 @@ struct DeltaParams {
     // workspace
     char *kf, *ktf, *qf, *qtf;  // per (slot, key head)
     char *tf, *pf;              // per (slot, value head): T and Q, or their transposes (backward)
-    float *gates, *y, *G;
+    float *gates;
+    float *back;  // like ckpt: the gradient of the state behind the chunk, and y
+    float *sum;   // gradients of q and k of shared key heads while they are summed
 };
 
 // Parameters of a single-token step.
@@ -74,6 +76,12 @@ hipError_t launch_delta_prep(const DeltaParams &p, bool bwd, hipStream_t s);
 hipError_t launch_delta_chain(const DeltaParams &p, bool bwd, hipStream_t s);
 hipError_t launch_delta_grad(const DeltaParams &p, hipStream_t s);
 hipError_t launch_delta_step(const DeltaStepParams &p, hipStream_t s);
+
+// Tiles are 16 x 16: lane (r, q) has rows 4 q .. 4 q + 3 of column r, as the matrix cores leave a result.  A chunk's
+// tiles lie by columns of the state, of each first those of the state's rows and then those of its 64 tokens.
+inline __host__ __device__ int delta_row_tiles(int dk) { return (dk + 15) / 16; }
+inline __host__ __device__ int delta_col_tiles(int dv) { return (dv + 15) / 16; }
+inline __host__ __device__ long delta_tiles(int dk, int dv) { return (long)delta_col_tiles(dv) * (delta_row_tiles(dk) + kDeltaC / 16); }
 
 // Blocks of 32 channels that a kernel is built for.
 inline int delta_blocks(int d) { return d <= 64 ? 2 : 4; }
@@ -162,15 +170,24 @@ __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, bf16x8 (&t)[NT]) {
     split<NT>(x, t);
 }
 
-// acc += A B over one 32-block, terms i and j with i + j < the larger count
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 acc) {
+// acc[k] += A[k] B[k] over one 32-block for K results, terms i and j with i + j < the larger count, the smallest first.
+// Term by term over all results: a matrix instruction that adds to what the one before it gives would wait for it.
+template <int NA, int NB, int K, class A, class B, class C>
+__device__ __forceinline__ void products(A &&a, B &&b, C &&acc) {
     constexpr int N = NA > NB ? NA : NB;
 #pragma unroll
-    for (int s = N - 1; s >= 0; --s)  // the smallest first
+    for (int s = N - 1; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-            if (s - i >= 0 && s - i < NB) acc = mfma(a[i], b[s - i], acc);
+            if (s - i >= 0 && s - i < NB) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) acc(k) = mfma(a(k, i), b(k, s - i), acc(k));
+            }
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 acc) {
+    products<NA, NB, 1>([&](int, int i) { return a[i]; }, [&](int, int j) { return b[j]; }, [&](int) -> f32x4 & { return acc; });
     return acc;
 }
 
@@ -198,6 +215,31 @@ __device__ __forceinline__ void load8(const void *base, long at, bool there, bf1
         }
         split<NT>(x, t);
     }
+}
+
+// A range-checked buffer: loads from outside give 0, stores to outside are dropped.  A lane that is
+// to be left out adds kNowhere to its offset.
+typedef __amdgpu_buffer_rsrc_t Buf;
+constexpr uint32_t kNowhere = 0x7ff00000u;
+
+__device__ __forceinline__ Buf buffer(const void *base, long bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)bytes, 0x00020000);
+}
+
+// An element's bits, to be made a number where it is used: made one here, it would be waited for here.
+template <bool BF>
+__device__ __forceinline__ uint32_t load1(Buf b, uint32_t at) {
+    if constexpr (BF) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0);
+    return __builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0);
+}
+
+template <bool BF>
+__device__ __forceinline__ float number(uint32_t bits) { return __uint_as_float(BF ? bits << 16 : bits); }
+
+template <bool BF>
+__device__ __forceinline__ void store1(Buf b, uint32_t at, float x) {
+    if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pk_bf16(x, x), b, at, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, at, 0, 0);
 }
 
 __device__ __forceinline__ bf16x8 fragment(const char *base, long at, int lane) {

@@ -30,7 +30,7 @@ struct DeltaCall {
 };
 
 // Descriptor, sequences, strides: what no pointer is needed for.
-int delta_call(const gdr_delta_desc *d, const int32_t *seq_off, int32_t n_seq, DeltaCall &c) {
+int delta_call(const gdr_delta_desc *d, const int32_t *seq_off, int32_t n_seq, DeltaCall &c, bool step = false) {
     const int rc = check_delta_desc(d);
     if (rc) return rc;
     if (n_seq < 0 || (!seq_off && n_seq != 0)) return GDR_EINVAL;
@@ -67,6 +67,9 @@ int delta_call(const gdr_delta_desc *d, const int32_t *seq_off, int32_t n_seq, D
     if (!stride_ok(p.ldq, c.rows, key) || !stride_ok(p.ldk, c.rows, key) || !stride_ok(p.ldv, c.rows, value) ||
         !stride_ok(p.ldg, c.rows, d->Hv) || !stride_ok(p.ldb, c.rows, d->Hv))
         return GDR_EINVAL;
+    if (key > kMaxRow || value > kMaxRow) return GDR_EUNSUPPORTED;
+    // a chunk's rows span less than 2^30 bytes; a step takes rows by themselves
+    if (!step && (p.ldq > kMaxRow || p.ldk > kMaxRow || p.ldv > kMaxRow || p.ldg > kMaxRow || p.ldb > kMaxRow)) return GDR_EUNSUPPORTED;
     return GDR_OK;
 }
 
@@ -90,7 +93,7 @@ int delta_inputs(DeltaCall &c, const void *q, const void *k, const void *v, cons
     return GDR_OK;
 }
 
-size_t ckpt_bytes(const DeltaParams &p) { return (size_t)p.nslot * p.Hv * (p.dk + GDR_DELTA_CHUNK) * p.dv * 4; }
+size_t ckpt_bytes(const DeltaParams &p) { return (size_t)p.nslot * p.Hv * delta_tiles(p.dk, p.dv) * 1024; }
 
 int check_norm_desc(const gdr_block_norm_desc *d) {
     if (!d || d->B < 0 || d->T < 0 || d->H < 0) return GDR_EINVAL;
@@ -161,6 +164,13 @@ size_t gdr_delta_workspace_size(const gdr_delta_desc *d, int32_t n_seq, int32_t 
     static const int32_t packed = 0;  // only says that the rows are packed
     if (delta_call(d, n_seq > 0 ? &packed : nullptr, n_seq, c) || c.empty || c.p.nslot == 0) return 0;
     return delta_workspace(c.p, backward != 0, nullptr);
+}
+
+size_t gdr_delta_ckpt_size(const gdr_delta_desc *d, int32_t n_seq) {
+    DeltaCall c;
+    static const int32_t packed = 0;
+    if (delta_call(d, n_seq > 0 ? &packed : nullptr, n_seq, c) || c.empty) return 0;
+    return ckpt_bytes(c.p);
 }
 
 int gdr_delta_fwd(const gdr_delta_desc *d, const void *q, const void *k, const void *v, const void *log_gate, const void *beta,
@@ -240,7 +250,7 @@ int gdr_delta_step(const gdr_delta_desc *d, const void *q, const void *k, const 
     gdr_delta_desc one = *d;  // a step is one token, whatever the descriptor's T
     one.T = 1;
     DeltaCall c;
-    int rc = delta_call(&one, nullptr, 0, c);
+    int rc = delta_call(&one, nullptr, 0, c, true);
     if (rc) return rc;
     rc = delta_inputs(c, q, k, v, log_gate, beta);
     if (rc) return rc;

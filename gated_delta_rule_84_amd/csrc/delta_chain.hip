@@ -1,218 +1,395 @@
 // delta_chain.hip -- the recurrence of the delta rule over a sequence's chunks, forward and backward (delta.hpp).
+#include <stdlib.h>
+
+#include <type_traits>
+
 #include "delta.hpp"
 
 namespace gdr {
 namespace {
 
-template <int NT>
-__device__ __forceinline__ void fragments(const char *base, long at, int lane, bf16x8 (&t)[NT]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) t[n] = fragment(base, at + n, lane);
+constexpr int kRing = 3;      // pieces in shared memory at once
+constexpr int kPiece = 50;    // most fragments of a piece
+constexpr int kLoaders = 2;   // waves that copy
+constexpr int kGroup = 12;    // most fragments that a wave reads ahead
+
+// LDS traffic waited for, global memory not.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// At most N vector memory operations of this wave still under way.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    static_assert(N < 64, "the counter's range");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | N >> 4 << 14);
 }
 
-// Places (16-row tile, 32-column block) of triangular operands: i counts the six that are not zero.
+template <int I, int N, class F>
+__device__ __forceinline__ void each(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        each<I + 1, N>(f);
+    }
+}
+
+// Places (16-row tile, 32-column block) of triangular operands: the six that are not zero.
 template <bool UPPER>
 constexpr int tri_index(int a, int b) {
     return UPPER ? (a < 2 ? 2 * a + b : b == 1 ? a + 2 : -1) : (a < 2 ? (b == 0 ? a : -1) : 2 * a - 2 + b);
 }
 
-// One wave has 16 columns of one value head's state, all of its rows, in registers.  Nothing is
-// exchanged: every product's result is the next one's operand as it lies (perm in delta.hpp).
+// A chunk's operands, copied in pieces of at most 50 fragments of 1 KB, and the groups of products that read them.
+// (fp32 operands have three fragments for one: more pieces, and smaller groups.)
+enum Part { kK, kQ, kT, kP, kC, kQC };  // k, q, T, Q (their transposes in the backward pass), k^T, q^T
+
 template <int NT, int KB, bool BWD>
-__global__ void __launch_bounds__(64) delta_chain_kernel(DeltaParams p, int heads8) {
+struct Plan {
+    static constexpr int key = 4 * KB * NT;  // fragments of k, q, k^T, q^T
+    static constexpr int N = NT == 1 ? 2 : BWD ? 5 : 4;  // pieces
+    // parts in the order in which they are copied, and the piece of each
+    static constexpr Part part(int i) {
+        constexpr Part f[] = {kK, kQ, kT, kP, kC}, b[] = {kP, kK, kQC, kT, kC};
+        return BWD ? b[i] : f[i];
+    }
+    static constexpr int piece(int i) {
+        constexpr int f1[] = {0, 0, 0, 1, 1}, b1[] = {0, 0, 1, 1, 1}, f3[] = {0, 1, 2, 2, 3};
+        return NT == 1 ? (BWD ? b1[i] : f1[i]) : BWD ? i : f3[i];
+    }
+    static constexpr int size(int i) { return part(i) == kT || part(i) == kP ? kDeltaTri : key; }
+    static constexpr int first(int i) { return i > 0 && piece(i - 1) == piece(i) ? first(i - 1) + size(i - 1) : 0; }
+    static constexpr int count(int m) {  // with the gates, behind the first piece
+        int n = m == 0;
+        for (int i = 0; i < 5; ++i) n += piece(i) == m ? size(i) : 0;
+        return n;
+    }
+    static constexpr int copies(int m) { return (count(m) + kLoaders - 1) / kLoaders; }
+    static constexpr int part_of(int m, int f) {
+        for (int i = 0; i < 5; ++i)
+            if (piece(i) == m && f >= first(i) && f < first(i) + size(i)) return i;
+        return -1;
+    }
+    static constexpr int index(Part x) {
+        for (int i = 0; i < 5; ++i)
+            if (part(i) == x) return i;
+        return -1;
+    }
+    // groups: of k a block of channels, of q GQ blocks, of T and Q a block of their columns, of k^T and q^T GC tiles of
+    // channels.  Backward with bf16, q^T's second half comes behind T: products beside the splits that T's result needs.
+    static constexpr int GQ = NT == 1 ? 2 : 1, GC = NT == 1 ? 2 * KB : 4;
+    static constexpr int nQ = KB / GQ, nC = 4 * KB / GC, late = BWD && NT == 1 ? nC / 2 : 0;
+    static constexpr int groups = BWD ? 2 + KB + nC + 2 + nC : KB + nQ + 2 + 2 + nC;
+    struct At {
+        Part x;
+        int g;
+    };
+    static constexpr At at(int i) {
+        const Part f[] = {kK, kQ, kT, kP, kC}, b[] = {kP, kK, kQC, kT, kQC, kC};
+        const int nf[] = {KB, nQ, 2, 2, nC}, nb[] = {2, KB, nC - late, 2, late, nC};
+        for (int s = 0; s < (BWD ? 6 : 5); ++s) {
+            const int n = BWD ? nb[s] : nf[s];
+            if (i < n) return {BWD ? b[s] : f[s], i + (BWD && s == 4 ? nC - late : 0)};
+            i -= n;
+        }
+        return {kK, 0};
+    }
+    static constexpr bool opens(int i) {  // the group is the first of a piece
+        if (i == 0) return true;
+        return piece(index(at(i).x)) != piece(index(at(i - 1).x));
+    }
+};
+
+// A workgroup has NW tiles of 16 columns of one value head's state, a wave each, all rows of it in registers.
+// Between those waves nothing is exchanged: every product's result is the next one's operand as it
+// lies (perm in delta.hpp).  Two more waves copy the operands, which the tiles share, to a ring in shared
+// memory, up to two pieces ahead.
+// KEEP: the states before the chunks and E are stored, for the backward pass.
+template <int NT, int KB, bool BWD, bool KEEP, int NW>
+__global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(DeltaParams p, int heads8) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
-    const int head = blockIdx.x % heads8, tile = blockIdx.x / heads8;
-    if (head >= p.nseq * p.Hv) return;
+    typedef Plan<NT, KB, BWD> P;
+    __shared__ __attribute__((aligned(16))) char ring[kRing][kPiece * 1024];
+    __shared__ __attribute__((aligned(16))) float gring[4][kDeltaGates];  // of chunk c in c % 4: copies run less than three chunks ahead
+    const int head = blockIdx.x % heads8;
+    if (head >= p.nseq * p.Hv) return;  // uniform over the workgroup
     const int seq = head / p.Hv, hv = head % p.Hv, hk = hv / p.group;
-    const int l = threadIdx.x, r = l & 15, q = l >> 4, col = 16 * tile + r;
-    const bool mine = col < p.dv;
     long row0;
     const int len = tokens_of(p, seq, row0), nc = (len + kDeltaC - 1) / kDeltaC;
     const int slot0 = first_slot(p, seq);
-    const long sstate = (long)p.dk * p.dv, sckpt = sstate + (long)kDeltaC * p.dv;
-    f32x4 S[2 * KB];
-    const float *init = BWD ? p.dST : p.S0;
-#pragma unroll
-    for (int a = 0; a < 2 * KB; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ch = 16 * a + 4 * q + i;
-            S[a][i] = init && mine && ch < p.dk ? init[head * sstate + (long)ch * p.dv + col] : 0.f;
-        }
-    auto keep = [&](float *to) __attribute__((always_inline)) {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+
+    if (w >= NW) {  // a copying wave has every second fragment
+        if (nc == 0) return;
+        const int half = w - NW;
+        int to = 0;  // place in the ring of the next piece
+        auto copy = [&](int c, auto M) __attribute__((always_inline)) {  // piece M of chunk c
+            constexpr int m = M;
+            c = min(c, nc - 1);  // behind the last chunk its pieces come again, to be counted
+            const long slot = slot0 + (BWD ? nc - 1 - c : c), kh = slot * p.Hk + hk, vh = slot * p.Hv + hv;
+            const char *gates = reinterpret_cast<const char *>(p.gates + vh * kDeltaGates);
+            each<0, P::copies(m)>([&](auto U) __attribute__((always_inline)) {
+                // both waves' fragments of this turn are of one part, or the second's is the next part's first
+                auto from = [&](auto F) __attribute__((always_inline)) -> const char * {
+                    constexpr int f = F < P::count(m) ? int(F) : P::count(m) - 1, i = P::part_of(m, f);
+                    if constexpr (i < 0) return gates;
+                    else {
+                        constexpr Part x = P::part(i);
+                        const char *base = x == kK ? p.kf : x == kQ ? p.qf : x == kT ? p.tf : x == kP ? p.pf : x == kC ? p.ktf : p.qtf;
+                        return base + ((x == kT || x == kP ? vh * kDeltaTri : kh * P::key) + (f - P::first(i))) * 1024;
+                    }
+                };
+                constexpr int f0 = 2 * U, f1 = 2 * U + 1;
+                const char *src = half ? from(std::integral_constant<int, f1>()) : from(std::integral_constant<int, f0>());
+                const int f = half ? f1 : f0;
+                dma16(src + l * 16, m == 0 && f >= P::count(0) - 1 ? reinterpret_cast<char *>(gring[c & 3]) : &ring[to][f * 1024]);
+            });
+            to = to == kRing - 1 ? 0 : to + 1;
+        };
+        copy(0, std::integral_constant<int, 0>());
+        copy(0, std::integral_constant<int, 1>());
+        for (int c = 0; c < nc; ++c)
+            each<0, P::N>([&](auto M) __attribute__((always_inline)) {
+                constexpr int m = M;
+                wait_copies<P::copies((m + 1) % P::N)>();  // this piece is there, the one behind it may not be
+                lds_barrier();                            // and the piece before is no longer read
+                copy(c + (m + 2) / P::N, std::integral_constant<int, (m + 2) % P::N>());
+            });
+        wait_copies<0>();  // no copy outlives the workgroup
+        return;
+    }
+
+    const int r = l & 15, q = l >> 4, col = 16 * ((int)(blockIdx.x / heads8) * NW + w) + r;
+    const bool mine = col < p.dv;
+    const long sstate = (long)p.dk * p.dv;
+    const int tile = (blockIdx.x / heads8) * NW + w, na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv);
+    int turn = 0;
+    const char *piece = nullptr;
+    auto next = [&]() __attribute__((always_inline)) {
+        lds_barrier();
+        piece = ring[turn];
+        turn = turn == kRing - 1 ? 0 : turn + 1;
+    };
+    // accesses by tiles go through range-checked buffers: no branch per element for rows and channels that are not there
+    constexpr bool BF = NT == 1;
+    constexpr int es = BF ? 2 : 4;
+    const uint32_t away = mine ? 0 : kNowhere, srow = 4 * p.dv, sat = 4 * q * srow + 4 * col + away;
+    auto keep = [&](float *to, const f32x4 (&S)[2 * KB]) __attribute__((always_inline)) {
+        const Buf b = buffer(to, 4 * sstate);
 #pragma unroll
         for (int a = 0; a < 2 * KB; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ch = 16 * a + 4 * q + i;
-                if (mine && ch < p.dk) to[(long)ch * p.dv + col] = S[a][i];
-            }
+            for (int i = 0; i < 4; ++i) store1<false>(b, sat + (16 * a + i) * srow, S[a][i]);
+    };
+    f32x4 S[2 * KB];
+    {
+        const float *init = BWD ? p.dST : p.S0;
+        const Buf b = buffer(init + (init ? head * sstate : 0), init ? 4 * sstate : 0);
+#pragma unroll
+        for (int a = 0; a < 2 * KB; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[a][i] = number<false>(load1<false>(b, sat + (16 * a + i) * srow));
+    }
+    // v, or do, of the lane's rows 16 a + 4 q + i of a chunk
+    const int64_t ldx = BWD ? (int64_t)p.Hv * p.dv : p.ldv;
+    const uint32_t xrow = ldx * es, orow = (uint32_t)p.Hv * p.dv * es;
+    auto values = [&](int c, uint32_t (&x)[4][4]) __attribute__((always_inline)) {
+        const int n = min(kDeltaC, len - c * kDeltaC);
+        const char *from = static_cast<const char *>(BWD ? p.dout : p.v) + ((row0 + (long)c * kDeltaC) * ldx + (long)hv * p.dv) * es;
+        const Buf b = buffer(from, (long)(n - 1) * xrow + p.dv * es);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[a][i] = load1<BF>(b, 4 * q * xrow + es * col + away + (16 * a + i) * xrow);
     };
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    uint32_t x_[4][4];
+    auto value = [&](int a) __attribute__((always_inline)) -> f32x4 {
+        return (f32x4){number<BF>(x_[a][0]), number<BF>(x_[a][1]), number<BF>(x_[a][2]), number<BF>(x_[a][3])};
+    };
+    bf16x8 sf[KB][3], df[2][NT];
+    auto ahead = [&]() __attribute__((always_inline)) {  // the first operands of a chunk
+        split<3>(S[0], S[1], sf[0]);
+        if constexpr (BWD) {
+            split<NT>(value(0), value(1), df[0]);
+            split<NT>(value(2), value(3), df[1]);
+        }
+    };
+    if (nc > 0) {
+        values(BWD ? nc - 1 : 0, x_);
+        ahead();
+    }
     for (int cc = 0; cc < nc; ++cc) {
         const int c = BWD ? nc - 1 - cc : cc;
         const int n = min(kDeltaC, len - c * kDeltaC);
-        const long slot = slot0 + c, vh = slot * p.Hv + hv, kh = slot * p.Hk + hk;
-        const long row = row0 + (long)c * kDeltaC;
-        const float *gates = p.gates + vh * kDeltaGates;
-        const long kbase = kh * (4 * KB * NT), tbase = vh * kDeltaTri;
-        if constexpr (BWD) keep(p.G + vh * sstate);
-        else if (p.ckpt) keep(p.ckpt + vh * sckpt);
-        // v, or do, of the lane's rows 16 a + 4 q + i
-        f32x4 x[4];
+        const long vh = (long)(slot0 + c) * p.Hv + hv, row = row0 + (long)c * kDeltaC;
+        const float *gates = gring[cc & 3] + 4 * q;  // read from the chunk's first piece on
+        auto front = [&](int a) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4 *>(gates + 16 * a); };
+        auto wb = [&](int a) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4 *>(gates + 64 + 16 * a); };
+        f32x4 R[4] = {zero, zero, zero, zero}, E[4] = {zero, zero, zero, zero};
+        f32x4 O[4] = {zero, zero, zero, zero};  // o; backward: Q^T do
+        bf16x8 rf[2][3], ef[2][3], of[2][NX], xf[2][3];
+        // tiles are kept as they lie: 16 bytes a lane (by elements of rows, 48 stores a chunk, their acknowledgements
+        // held the wave up)
+        auto tiles = [&](int n) __attribute__((always_inline)) {
+            return buffer((BWD ? p.back : p.ckpt) + (vh * nj + tile) * (na + kDeltaC / 16) * 256, tile < nj ? n * 1024 : 0);
+        };
+        auto put_tile = [&](Buf b, int a, f32x4 x) __attribute__((always_inline)) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, a * 1024 + l * 16, 0, 0);
+        };
+        // reads the fragments of group G
+        auto load = [&](auto G, bf16x8 (&to)[kGroup]) __attribute__((always_inline)) {
+            constexpr Part x = P::at(G).x;
+            constexpr int g = P::at(G).g, at = P::first(P::index(x));
+            if constexpr (P::opens(G)) next();
+            if constexpr (x == kT || x == kP) {
+                constexpr int NF = x == kP && !BWD ? NX : 3;
+                constexpr int t0 = BWD ? 0 : 2 * g, nt = BWD ? 2 + 2 * g : 4 - 2 * g;
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+                for (int k = 0; k < nt; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * a + 4 * q + i;
-                const long at = BWD ? ((row + t) * p.Hv + hv) * p.dv + col : (row + t) * p.ldv + (long)hv * p.dv + col;
-                x[a][i] = mine && t < n ? ld_elem(BWD ? p.dout : p.v, at, NT == 1) : 0.f;
+                    for (int n = 0; n < NF; ++n) to[k * NF + n] = fragment(piece, at + 3 * tri_index<BWD>(t0 + k, g) + n, l);
+            } else {
+                constexpr int n = (x == kK ? 4 : x == kQ ? 4 * P::GQ : P::GC) * NT;
+#pragma unroll
+                for (int k = 0; k < n; ++k) to[k] = fragment(piece, at + g * n + k, l);
             }
-        f32x4 front[4], wb[4];
+        };
+        // the products of group G, and beside them the operands of later groups
+        auto run = [&](auto G, const bf16x8 (&from)[kGroup]) __attribute__((always_inline)) {
+            constexpr Part x = P::at(G).x;
+            constexpr int g = P::at(G).g;
+            constexpr int t0 = BWD ? 0 : 2 * g, nt = BWD ? 2 + 2 * g : 4 - 2 * g;  // row tiles of a triangle's block g
+            if constexpr (x == kK) {  // R = k S
+                products<NT, 3, 4>([&](int k, int i) { return from[k * NT + i]; }, [&](int, int j) { return sf[g][j]; },
+                                   [&](int k) -> f32x4 & { return R[k]; });
+                if constexpr (g + 1 < KB) split<3>(S[2 * g + 2], S[2 * g + 3], sf[g + 1]);
+                if constexpr (g == 0) {
+                    if constexpr (KEEP) {
+                        const Buf b = tiles(na);  // tiles past dk are dropped
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            front[a] = *reinterpret_cast<const f32x4 *>(gates + 16 * a + 4 * q);
-            wb[a] = *reinterpret_cast<const f32x4 *>(gates + 64 + 16 * a + 4 * q);
-        }
-        const float whole = gates[128];
-        f32x4 R[4] = {zero, zero, zero, zero}, O[4] = {zero, zero, zero, zero};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            bf16x8 sf[3];
-            split<3>(S[2 * kb], S[2 * kb + 1], sf);
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                bf16x8 kf[NT];
-                fragments<NT>(p.kf, kbase + (a * KB + kb) * NT, l, kf);
-                R[a] = product<NT, 3>(kf, sf, R[a]);
-            }
-            if constexpr (!BWD) {
-                bf16x8 sx[NX];
-#pragma unroll
-                for (int m = 0; m < NX; ++m) sx[m] = sf[m];
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    bf16x8 qf[NT];
-                    fragments<NT>(p.qf, kbase + (a * KB + kb) * NT, l, qf);
-                    O[a] = product<NT, NX>(qf, sx, O[a]);
+                        for (int a = 0; a < 2 * KB; ++a) put_tile(b, a, S[a]);
+                    }
                 }
-            }
-        }
-        f32x4 E[4] = {zero, zero, zero, zero};
-        if constexpr (!BWD) {
-            // E = T (v - front k S), o = front q S + Q E
+                if constexpr (BWD && g == KB - 1) {
+                    const float whole = gring[cc & 3][128];
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                R[a] = x[a] - front[a] * R[a];
-                O[a] = front[a] * O[a];
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                bf16x8 rf[3];
-                split<3>(R[2 * b], R[2 * b + 1], rf);
-#pragma unroll
-                for (int a = 2 * b; a < 4; ++a) {
-                    bf16x8 tf[3];
-                    fragments<3>(p.tf, tbase + 3 * tri_index<false>(a, b), l, tf);
-                    E[a] = product<3, 3>(tf, rf, E[a]);
+                    for (int a = 0; a < 2 * KB; ++a) S[a] = whole * S[a];
                 }
-            }
+            } else if constexpr (x == kQ) {  // O = q S
+                products<NT, NX, 4 * P::GQ>([&](int k, int i) { return from[k * NT + i]; },
+                                            [&](int k, int j) { return sf[g * P::GQ + k / 4][j]; },
+                                            [&](int k) -> f32x4 & { return O[k % 4]; });
+                if constexpr (g == 0) {  // R = v - front k S
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                bf16x8 ef[NX];
-                split<NX>(E[2 * b], E[2 * b + 1], ef);
-#pragma unroll
-                for (int a = 2 * b; a < 4; ++a) {
-                    bf16x8 pf[NX];
-                    fragments<NX>(p.pf, tbase + 3 * tri_index<false>(a, b), l, pf);
-                    O[a] = product<NX, NX>(pf, ef, O[a]);
+                    for (int a = 0; a < 4; ++a) R[a] = value(a) - front(a) * R[a];
+                    split<3>(R[0], R[1], rf[0]);
                 }
-            }
-        } else {
-            // E = T^T (Q^T do + wb k G)
-#pragma unroll
-            for (int a = 0; a < 4; ++a) R[a] = wb[a] * R[a];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                bf16x8 df[NT];
-                split<NT>(x[2 * b], x[2 * b + 1], df);
-#pragma unroll
-                for (int a = 0; a < 2 + 2 * b; ++a) {
-                    bf16x8 pf[3];
-                    fragments<3>(p.pf, tbase + 3 * tri_index<true>(a, b), l, pf);
-                    R[a] = product<3, NT>(pf, df, R[a]);
+                if constexpr (g == P::nQ - 1) {
+                    split<3>(R[2], R[3], rf[1]);
+                    values(min(c + 1, nc - 1), x_);
                 }
-            }
+            } else if constexpr (x == kT) {  // E = T R, or T^T R
+                products<3, 3, nt>([&](int k, int i) { return from[3 * k + i]; }, [&](int, int j) { return rf[g][j]; },
+                                   [&](int k) -> f32x4 & { return E[t0 + k]; });
+                if constexpr (!BWD && g == 0) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                bf16x8 rf[3];
-                split<3>(R[2 * b], R[2 * b + 1], rf);
-#pragma unroll
-                for (int a = 0; a < 2 + 2 * b; ++a) {
-                    bf16x8 tf[3];
-                    fragments<3>(p.tf, tbase + 3 * tri_index<true>(a, b), l, tf);
-                    E[a] = product<3, 3>(tf, rf, E[a]);
+                    for (int a = 0; a < 4; ++a) O[a] = front(a) * O[a];
                 }
-            }
-        }
-        // S = whole S + k^T (wb E), or whole S + q^T (front do) - k^T (front E)
-#pragma unroll
-        for (int a = 0; a < 2 * KB; ++a) S[a] = whole * S[a];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            bf16x8 ef[3];
-            if constexpr (BWD) split<3>(-front[2 * b] * E[2 * b], -front[2 * b + 1] * E[2 * b + 1], ef);
-            else split<3>(wb[2 * b] * E[2 * b], wb[2 * b + 1] * E[2 * b + 1], ef);
-#pragma unroll
-            for (int a = 0; a < 2 * KB; ++a) {
-                bf16x8 kt[NT];
-                fragments<NT>(p.ktf, kbase + (a * 2 + b) * NT, l, kt);
-                S[a] = product<NT, 3>(kt, ef, S[a]);
-            }
-            if constexpr (BWD) {
-                bf16x8 df[3];
-                split<3>(front[2 * b] * x[2 * b], front[2 * b + 1] * x[2 * b + 1], df);
-#pragma unroll
-                for (int a = 0; a < 2 * KB; ++a) {
-                    bf16x8 qt[NT];
-                    fragments<NT>(p.qtf, kbase + (a * 2 + b) * NT, l, qt);
-                    S[a] = product<NT, 3>(qt, df, S[a]);
+                if constexpr (!BWD && g == 1) {  // rows 0 to 31 of E were done with the first block
+                    split<NX>(E[0], E[1], of[0]);
+                    split<3>(wb(0) * E[0], wb(1) * E[1], ef[0]);
                 }
-            }
-        }
-        float *Et = BWD ? p.y + vh * ((long)kDeltaC * p.dv) : p.ckpt ? p.ckpt + vh * sckpt + sstate : nullptr;
+                if constexpr (BWD && g == 1 && P::late == 0) {
+                    split<3>(-front(0) * E[0], -front(1) * E[1], ef[0]);
+                    split<3>(-front(2) * E[2], -front(3) * E[3], ef[1]);
+                }
+            } else if constexpr (x == kP && !BWD) {  // o = front q S + Q E
+                if constexpr (g == 0) {
+                    split<NX>(E[2], E[3], of[1]);
+                    split<3>(wb(2) * E[2], wb(3) * E[3], ef[1]);
+                    const float whole = gring[cc & 3][128];
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+                    for (int a = 0; a < 2 * KB; ++a) S[a] = whole * S[a];
+                }
+                products<NX, NX, nt>([&](int k, int i) { return from[NX * k + i]; }, [&](int, int j) { return of[g][j]; },
+                                     [&](int k) -> f32x4 & { return O[t0 + k]; });
+            } else if constexpr (x == kP) {  // Q^T do
+                products<3, NT, nt>([&](int k, int i) { return from[3 * k + i]; }, [&](int, int j) { return df[g][j]; },
+                                    [&](int k) -> f32x4 & { return O[t0 + k]; });
+                split<3>(front(2 * g) * value(2 * g), front(2 * g + 1) * value(2 * g + 1), xf[g]);
+                if constexpr (g == 1) values(max(c - 1, 0), x_);
+            } else {  // S = whole S + k^T (wb E), or whole S + q^T (front do) - k^T (front E)
+                constexpr int b = g * P::GC / (2 * KB);
+                products<NT, 3, P::GC>([&](int k, int i) { return from[k * NT + i]; },
+                                       [&](int, int j) { return x == kC ? ef[b][j] : xf[b][j]; },
+                                       [&](int k) -> f32x4 & { return S[(g * P::GC + k) % (2 * KB)]; });
+                if constexpr (x == kQC && g == 0) {  // R = Q^T do + wb k G
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * a + 4 * q + i;
-                if (!mine) continue;
-                if (Et) Et[(long)t * p.dv + col] = E[a][i];
-                if (t < n) st_elem(BWD ? p.dvv : p.o, ((row + t) * p.Hv + hv) * p.dv + col, BWD ? E[a][i] : O[a][i], NT == 1);
+                    for (int a = 0; a < 4; ++a) R[a] = O[a] + wb(a) * R[a];
+                    split<3>(R[0], R[1], rf[0]);
+                    split<3>(R[2], R[3], rf[1]);
+                }
+                if constexpr (x == kQC && P::late > 0 && g == P::nC - P::late) {
+                    split<3>(-front(0) * E[0], -front(1) * E[1], ef[0]);
+                    split<3>(-front(2) * E[2], -front(3) * E[3], ef[1]);
+                }
+                if constexpr (x == kC && g == 0) {
+                    if constexpr (KEEP) {
+                        const Buf b = tiles(na + kDeltaC / 16);
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) put_tile(b, na + a, E[a]);
+                    }
+                    char *to = static_cast<char *>(BWD ? p.dvv : p.o) + (row * p.Hv + hv) * p.dv * es;
+                    const Buf b = buffer(to, (long)(n - 1) * orow + p.dv * es);
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store1<BF>(b, 4 * q * orow + es * col + away + (16 * a + i) * orow, BWD ? E[a][i] : O[a][i]);
+                }
+                if constexpr (x == kC && g == P::nC - 1) ahead();
             }
+        };
+        bf16x8 f[2][kGroup];
+        load(std::integral_constant<int, 0>(), f[0]);
+        each<0, P::groups>([&](auto G) __attribute__((always_inline)) {
+            constexpr int g = G;
+            if constexpr (g + 1 < P::groups) load(std::integral_constant<int, g + 1>(), f[(g + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            run(G, f[g & 1]);
+            // a matrix instruction takes the time of four others: three of the vector ALU between two of them
+            each<0, 24>([&](auto) __attribute__((always_inline)) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+            });
+        });
     }
     float *last = BWD ? p.dS0 : p.ST;
-    if (last) keep(last + head * sstate);
+    if (last) keep(last + head * sstate, S);
 }
 
-template <bool BWD>
+template <bool BWD, bool KEEP, int NW>
 const void *pick(int nt, int kb) {
-    if (nt == 1) return kb == 2 ? reinterpret_cast<const void *>(&delta_chain_kernel<1, 2, BWD>) : reinterpret_cast<const void *>(&delta_chain_kernel<1, 4, BWD>);
-    return kb == 2 ? reinterpret_cast<const void *>(&delta_chain_kernel<3, 2, BWD>) : reinterpret_cast<const void *>(&delta_chain_kernel<3, 4, BWD>);
+    return nt == 1 ? (kb == 2 ? reinterpret_cast<const void *>(&delta_chain_kernel<1, 2, BWD, KEEP, NW>)
+                              : reinterpret_cast<const void *>(&delta_chain_kernel<1, 4, BWD, KEEP, NW>))
+                   : (kb == 2 ? reinterpret_cast<const void *>(&delta_chain_kernel<3, 2, BWD, KEEP, NW>)
+                              : reinterpret_cast<const void *>(&delta_chain_kernel<3, 4, BWD, KEEP, NW>));
 }
 
-// Heads of the grid: a multiple of 8, so that the column tiles of one head run on one of the 8 XCDs
-// (workgroups go round them in turn) and share its operands in that one's cache.
-long heads_of(const DeltaParams &p) { return ((long)p.nseq * p.Hv + 7) / 8 * 8; }
+template <int NW>
+const void *pick(bool bwd, bool keep, int nt, int kb) {
+    return bwd ? pick<true, true, NW>(nt, kb) : keep ? pick<false, true, NW>(nt, kb) : pick<false, false, NW>(nt, kb);
+}
 
 }  // namespace
 
 hipError_t launch_delta_chain(const DeltaParams &p0, bool bwd, hipStream_t s) {
     DeltaParams p = p0;
-    int heads = (int)heads_of(p);
+    // a multiple of 8, so that the workgroups of one head run on one of the 8 XCDs (workgroups go round
+    // them in turn) and share its operands in that one's cache
+    int heads = (int)(((long)p.nseq * p.Hv + 7) / 8 * 8);
     void *args[] = {&p, &heads};
-    const int nt = p.io_bf16 ? 1 : 3, kb = delta_blocks(p.dk);
-    return hipLaunchKernel(bwd ? pick<true>(nt, kb) : pick<false>(nt, kb), dim3((unsigned)heads * ((p.dv + 15) / 16)), dim3(64), args, 0, s);
+    const int nt = p.io_bf16 ? 1 : 3, kb = delta_blocks(p.dk), tiles = (p.dv + 15) / 16;
+    const int nw = getenv("NW4") ? 4 : 2;
+    const void *fn = nw == 2 ? pick<2>(bwd, p.ckpt != nullptr, nt, kb) : pick<4>(bwd, p.ckpt != nullptr, nt, kb);
+    return hipLaunchKernel(fn, dim3((unsigned)heads * ((tiles + nw - 1) / nw)), dim3(64 * (nw + kLoaders)), args, 0, s);
 }
 
 hipError_t launch_delta_fwd(const DeltaParams &p, hipStream_t s) {

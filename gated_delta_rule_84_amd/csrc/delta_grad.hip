@@ -8,6 +8,12 @@
 // and the gradient of a log gate is the sum of what passes it: from the state before to the one behind,
 // from earlier writes to the state behind, from the state before to later reads, from earlier writes to
 // later reads.
+//
+// Products are formed with channels as rows and tokens as columns, so that a lane's results are four
+// channels of one token: q and k of the dot products lie in its fragments already, gates are one value a lane,
+// and stores are whole words.  All contractions over the value's columns run in one pass over
+// blocks of 32 of them, which are split into terms once, into shared memory, column by column; the
+// transposing LDS read turns them into operands.
 #include "delta.hpp"
 
 namespace gdr {
@@ -15,235 +21,306 @@ namespace {
 
 constexpr int kLC = kDeltaC + 4;
 
-template <int JB>
+typedef __attribute__((address_space(3))) char *lds_bytes;
+typedef __attribute__((address_space(3))) u32x2 *lds_u32x2;
+
+// Terms of a block of 32 columns: [term][column][row], the 32-byte units of 16 rows swapped about so that eight columns
+// lie in different banks.  A lane's place for all tiles is one offset: the tile's number changes bits of it that only
+// the swap also holds.
+template <int ROWS>
+struct Staged {
+    uint16_t x[3][32][ROWS];
+    static constexpr int kCol = 2 * ROWS, kTerm = 32 * kCol;
+    static __device__ __forceinline__ uint32_t place(int j) { return j * kCol + ((ROWS == 64 ? j >> 1 & 3 : j & (ROWS / 16 - 1)) << 5); }
+    // of rows 4 q .. 4 q + 3 of column j
+    static __device__ __forceinline__ uint32_t put_place(int j, int q) { return place(j) + 8 * q; }
+    __device__ __forceinline__ void put(uint32_t at, int tile, f32x4 v) {
+        lds_bytes to = (lds_bytes)&x[0][0][0] + (at ^ (uint32_t)tile << 5);
+        float r[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            *(lds_u32x2)(to + n * kTerm) = (u32x2){high_halves(r[0], r[1]), high_halves(r[2], r[3])};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
+        }
+    }
+    // of the operand whose rows are the 16 of a tile and whose contraction the 32 columns (perm)
+    static __device__ __forceinline__ uint32_t get_place(int r, int q) { return place(4 * q + (r >> 2)) + 8 * (r & 3); }
+    __device__ __forceinline__ void get(uint32_t at, int tile, bf16x8 (&t)[3]) {
+        lds_bytes from = (lds_bytes)&x[0][0][0] + (at ^ (uint32_t)tile << 5);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm)));
+            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm + 16 * kCol)));
+            t[n] = as_bf16x8((u32x4){a[0], a[1], b[0], b[1]});
+        }
+    }
+};
+
+template <int KB>
 struct GradShared {
-    static constexpr int LJ = 32 * JB + 8;
-    union {
-        uint16_t D[3][kDeltaC][LJ];
-        uint16_t SG[2][3][32][LJ];
-    };
     union {
         struct {
-            float C1[kDeltaC][kLC], C2[kDeltaC][kLC];
+            Staged<32 * KB> S, G;
+            Staged<64> D, Y;
         };
-        float qk[2][kDeltaC][36];  // q and k of 32 channels
+        struct {
+            float C1[kDeltaC][kLC], C2[kDeltaC][kLC];  // [t][s]
+        };
     };
-    float col_m[4][kDeltaC], col_pair[4][kDeltaC], row_m[2][kDeltaC], read[2][kDeltaC], write[2][kDeltaC], dot[8];
+    float col_m[2][kDeltaC], col_pair[2][kDeltaC], row_m[2][kDeltaC], read[2][kDeltaC], write[2][kDeltaC], dot[4];
     ChunkGates gt;
 };
 
-__device__ __forceinline__ float row_lanes(float x) {  // over the 16 lanes of a row of tiles
+__device__ __forceinline__ float row_lanes(float x) {  // over the 16 lanes of a quarter
 #pragma unroll
     for (int s = 1; s < 16; s <<= 1) x += __shfl_xor(x, s);
     return x;
 }
 
-__device__ __forceinline__ float column_lanes(float x) {  // over the four quarters
+__device__ __forceinline__ float quarters(float x) {  // over the four quarters
     x += __shfl_xor(x, 16);
     return x + __shfl_xor(x, 32);
 }
 
-// Eight waves: w has the 16-row tile w of tokens; of each 32 channels half hf's 16.
-template <int NT, int KB, int JB>
-__global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
+// Four waves: wave (th, ch) has token tiles 2 th and 2 th + 1 and half ch of the channels.
+template <int NT, int KB>
+__global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
-    __shared__ __attribute__((aligned(16))) GradShared<JB> sh;
+    __shared__ __attribute__((aligned(16))) GradShared<KB> sh;
     const int hk = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
     const Place at = place_of(p, slot);
     if (at.n <= 0) return;  // uniform over the workgroup
-    const int tid = threadIdx.x, w = tid >> 6 & 3, hf = tid >> 8, l = tid & 63, r = l & 15, q = l >> 4;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 1, ch = w & 1;
     const long key = ((long)slot * p.Hk + hk) * (4 * KB * NT);
-    const long sstate = (long)p.dk * p.dv, sckpt = sstate + (long)kDeltaC * p.dv;
+    const int na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv), jblocks = (nj + 1) / 2;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 dq[KB], dk[KB];
-#pragma unroll
-    for (int a = 0; a < KB; ++a) dq[a] = dk[a] = zero;
-    const int trow = 16 * w + 4 * q;  // first of the lane's rows
+#pragma unroll 1
     for (int h = 0; h < p.group; ++h) {
+        int l = tid & 63;
+        asm volatile("" : "+v"(l));  // addresses are formed for each head: kept over the heads they would take the registers
+        const int r = l & 15, q = l >> 4;
         const int hv = hk * p.group + h;
-        const long vh = (long)slot * p.Hv + hv;
-        const float *S = p.ckpt + vh * sckpt, *D = S + sstate, *G = p.G + vh * sstate, *Y = p.y + vh * ((long)kDeltaC * p.dv);
+        const long vh = (long)slot * p.Hv + hv, base = vh * nj * (na + 4) * 256;
+        const float *ST = p.ckpt + base, *GT = p.back + base;
         if (h) __syncthreads();
-        if (tid < 64) make_gates(p, at, hv, l, sh.gt);
-        bf16x8 dof[JB][NT], yf[JB][3], df[JB][3];
+        if (w == 0) make_gates(p, at, hv, l, sh.gt);
+        f32x4 oS[KB][2], yS[KB][2], dG[KB][2], n1[2][2], n2[2][2];  // [channel tile][token tile], [s tile][token tile]
 #pragma unroll
-        for (int jb = 0; jb < JB; ++jb) {
-            const int j = 32 * jb + 8 * q, t = 16 * w + r;
-            load8<NT>(p.dout, ((at.row0 + t) * p.Hv + hv) * p.dv + j, t < at.n && j < p.dv, dof[jb]);
-            load8<3>(Y, (long)t * p.dv + j, j < p.dv, yf[jb]);
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int c = 0; c < KB; ++c) oS[c][t] = yS[c][t] = dG[c][t] = zero;
+            n1[0][t] = n1[1][t] = n2[0][t] = n2[1][t] = zero;
         }
-        for (int i = tid; i < kDeltaC * 4 * JB; i += 512) {
-            const int t = i / (4 * JB), j = i % (4 * JB) * 8;
-            bf16x8 x[3];
-            load8<3>(D, (long)t * p.dv + j, j < p.dv, x);
-#pragma unroll
-            for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8 *>(&sh.D[n][t][j]) = x[n];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int jb = 0; jb < JB; ++jb)
-#pragma unroll
-            for (int n = 0; n < 3; ++n) df[jb][n] = *reinterpret_cast<const bf16x8 *>(&sh.D[n][16 * w + r][32 * jb + 8 * q]);
-        float rm[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = hf; j < 4; j += 2) {
-            f32x4 n1 = zero, n2 = zero, qk = zero, kk = zero;
-            if (j <= w) {
-#pragma unroll
-                for (int jb = 0; jb < JB; ++jb) {
-                    bf16x8 b[3];
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) b[n] = *reinterpret_cast<const bf16x8 *>(&sh.D[n][16 * j + r][32 * jb + 8 * q]);
-                    n1 = product<NT, 3>(dof[jb], b, n1);
-                    n2 = product<3, 3>(yf[jb], b, n2);
-                }
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    bf16x8 b[NT], aq[NT], ak[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        b[n] = fragment(p.kf, key + (j * KB + kb) * NT + n, l);
-                        aq[n] = fragment(p.qf, key + (w * KB + kb) * NT + n, l);
-                        ak[n] = fragment(p.kf, key + (w * KB + kb) * NT + n, l);
-                    }
-                    qk = product<NT, NT>(aq, b, qk);
-                    kk = product<NT, NT>(ak, b, kk);
-                }
-            }
-            const int s = 16 * j + r;
-            const float beta = sh.gt.beta[s];
-            float cm = 0.f, cp = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = trow + i;
-                const float e = t >= s ? sh.gt.decay(t, s) : 0.f;
-                const float a1 = t >= s ? n1[i] : 0.f, a2 = t > s ? n2[i] : 0.f;
-                sh.C1[t][s] = e * beta * a1;
-                sh.C2[t][s] = -e * beta * a2;
-                const float pair = t >= s ? e * (a1 * qk[i] - a2 * kk[i]) : 0.f;
-                cp += pair;
-                if (t > s) {  // a token's own pair does not pass its gate
-                    rm[i] += pair * beta;
-                    cm += pair * beta;
-                }
-            }
-            cm = column_lanes(cm);
-            cp = column_lanes(cp);
-            if (q == 0) {
-                sh.col_m[w][s] = cm;
-                sh.col_pair[w][s] = cp;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = row_lanes(rm[i]);
-            if (r == 0) sh.row_m[hf][trow + i] = x;
-        }
-        __syncthreads();
-        // C1 k, C1^T q, (C2 + C2^T) k
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float x1[8], x1t[8], x2[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int m = 16 * w + r, o = 32 * b + perm(q, e);
-                x1[e] = sh.C1[m][o];
-                x1t[e] = sh.C1[o][m];
-                x2[e] = sh.C2[m][o] + sh.C2[o][m];
-            }
-            bf16x8 c1[NX], c1t[NX], c2[NX];
-            split<NX>(x1, c1);
-            split<NX>(x1t, c1t);
-            split<NX>(x2, c2);
-#pragma unroll
-            for (int a = 0; a < KB; ++a) {
-                bf16x8 kt[NT], qt[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    kt[n] = fragment(p.ktf, key + ((2 * a + hf) * 2 + b) * NT + n, l);
-                    qt[n] = fragment(p.qtf, key + ((2 * a + hf) * 2 + b) * NT + n, l);
-                }
-                dq[a] = product<NX, NT>(c1, kt, dq[a]);
-                dk[a] = product<NX, NT>(c1t, qt, dk[a]);
-                dk[a] = product<NX, NT>(c2, kt, dk[a]);
-            }
-        }
-        float read[4] = {0.f, 0.f, 0.f, 0.f}, write[4] = {0.f, 0.f, 0.f, 0.f}, dot = 0.f;
-#pragma unroll
-        for (int cb = 0; cb < KB; ++cb) {
-            __syncthreads();  // the last reads of D or of the block before
+        float dot = 0.f;
+#pragma unroll 1
+        for (int jb = 0; jb < jblocks; ++jb) {
+            // formed again for each block: kept for all tiles they would take the registers of the sums
+            uint32_t pS = Staged<32 * KB>::put_place(16 * (w & 1) + r, q), gS = Staged<32 * KB>::get_place(r, q);
+            uint32_t pD = Staged<64>::put_place(16 * (w & 1) + r, q), gD = Staged<64>::get_place(r, q);
+            asm volatile("" : "+v"(pS), "+v"(gS), "+v"(pD), "+v"(gD));
+            // wave w brings column tile w & 1 of the block, half of its row tiles
             {
-                const int m = tid >> 8, t = tid >> 2 & 63, c = (tid & 3) * 8, ch = 32 * cb + c;
-                const void *from = m ? p.k : p.q;
-                const long o = (at.row0 + t) * (m ? p.ldk : p.ldq) + (long)hk * p.dk + ch;
-                const bool there = t < at.n && ch < p.dk;
+                const int jt = 2 * jb + (w & 1);
+                const bool there = jt < nj;
+                const float *s = ST + (long)jt * (na + 4) * 256 + l * 4, *g = GT + (long)jt * (na + 4) * 256 + l * 4;
+                f32x4 a[KB], b[KB], d[2], y[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sh.qk[m][t][c + e] = there ? ld_elem(from, o + e, NT == 1) : 0.f;
-            }
-            for (int i = tid; i < 32 * 4 * JB; i += 512) {
-                const int c = i / (4 * JB), j = i % (4 * JB) * 8, ch = 32 * cb + c;
-                const bool there = ch < p.dk && j < p.dv;
-                float x[2][8];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float *from = (m ? G : S) + (long)ch * p.dv + j;
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4) {
-                        f32x4 z = zero;
-                        if (there) z = *reinterpret_cast<const f32x4 *>(from + e);
-#pragma unroll
-                        for (int i4 = 0; i4 < 4; ++i4) x[m][e + i4] = z[i4];
+                for (int c = 0; c < KB; ++c) {
+                    const int tile = (w >> 1) * KB + c;
+                    a[c] = b[c] = zero;
+                    if (there && tile < na) {
+                        a[c] = *reinterpret_cast<const f32x4 *>(s + tile * 256);
+                        b[c] = *reinterpret_cast<const f32x4 *>(g + tile * 256);
                     }
-                    bf16x8 t[3];
-                    split<3>(x[m], t);
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8 *>(&sh.SG[m][n][c][j]) = t[n];
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dot = fmaf(x[0][e], x[1][e], dot);
+                for (int c = 0; c < 2; ++c) {
+                    const int tile = na + (w >> 1) * 2 + c;
+                    d[c] = y[c] = zero;
+                    if (there) {
+                        d[c] = *reinterpret_cast<const f32x4 *>(s + tile * 256);
+                        y[c] = *reinterpret_cast<const f32x4 *>(g + tile * 256);
+                    }
+                }
+                __syncthreads();  // the block before is no longer read
+#pragma unroll
+                for (int c = 0; c < KB; ++c) {
+                    sh.S.put(pS, (w >> 1) * KB + c, a[c]);
+                    sh.G.put(pS, (w >> 1) * KB + c, b[c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dot = fmaf(a[c][i], b[c][i], dot);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    sh.D.put(pD, (w >> 1) * 2 + c, d[c]);
+                    sh.Y.put(pD, (w >> 1) * 2 + c, y[c]);
+                }
+            }
+            bf16x8 fo[2][NT], fy[2][3], fd[2][3];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {  // do, by rows: its columns in the operands' order
+                const int row = 16 * (2 * th + t) + r;
+                const long o = ((at.row0 + row) * p.Hv + hv) * p.dv;
+                float x[8];
+                u32x2 wd[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int j = 32 * jb + 16 * k + 4 * q;
+                    const bool there = row < at.n && j < p.dv;
+                    if constexpr (NT == 1) {
+                        typedef uint32_t wu2 __attribute__((ext_vector_type(2), aligned(2)));
+                        wu2 z = {0, 0};
+                        if (there) z = *reinterpret_cast<const wu2 *>(static_cast<const uint16_t *>(p.dout) + o + j);
+                        wd[k] = (u32x2){z[0], z[1]};
+                    } else {
+                        wu4 z = {0, 0, 0, 0};
+                        if (there) z = *reinterpret_cast<const wu4 *>(static_cast<const float *>(p.dout) + o + j);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[4 * k + i] = __uint_as_float(z[i]);
+                    }
+                }
+                if constexpr (NT == 1) fo[t][0] = as_bf16x8((u32x4){wd[0][0], wd[0][1], wd[1][0], wd[1][1]});
+                else split<NT>(x, fo[t]);
             }
             __syncthreads();
-            f32x4 oS = zero, yS = zero, dG = zero;
 #pragma unroll
-            for (int jb = 0; jb < JB; ++jb) {
-                bf16x8 s[3], g[3];
+            for (int t = 0; t < 2; ++t) {
+                sh.Y.get(gD, 2 * th + t, fy[t]);
+                sh.D.get(gD, 2 * th + t, fd[t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    s[n] = *reinterpret_cast<const bf16x8 *>(&sh.SG[0][n][16 * hf + r][32 * jb + 8 * q]);
-                    g[n] = *reinterpret_cast<const bf16x8 *>(&sh.SG[1][n][16 * hf + r][32 * jb + 8 * q]);
+            for (int m = 0; m < 2; ++m) {
+                const int sa = 2 * m + ch;  // s tiles of this wave
+                if (sa > 2 * th + 1) continue;
+                bf16x8 d[3];
+                sh.D.get(gD, sa, d);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (sa > 2 * th + t) continue;
+                    n1[m][t] = product<3, NT>(d, fo[t], n1[m][t]);
+                    n2[m][t] = product<3, 3>(d, fy[t], n2[m][t]);
                 }
-                oS = product<NT, 3>(dof[jb], s, oS);
-                yS = product<3, 3>(yf[jb], s, yS);
-                dG = product<3, 3>(df[jb], g, dG);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = trow + i;
-                const float qv = sh.qk[0][t][16 * hf + r], kv = sh.qk[1][t][16 * hf + r];
-                const float fo = sh.gt.front[t] * oS[i], fy = sh.gt.front[t] * yS[i], bg = sh.gt.behind[t] * dG[i];
-                dq[cb][i] += fo;
-                dk[cb][i] += fmaf(sh.gt.beta[t], bg, -fy);
-                read[i] += qv * fo - kv * fy;
-                write[i] = fmaf(kv, bg, write[i]);
+            for (int c = 0; c < KB; ++c) {
+                bf16x8 s[3], g[3];
+                sh.S.get(gS, ch * KB + c, s);
+                sh.G.get(gS, ch * KB + c, g);
+                products<3, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fo[k][j]; },
+                                   [&](int k) -> f32x4 & { return oS[c][k]; });
+                products<3, 3, 4>([&](int k, int i) { return k < 2 ? s[i] : g[i]; }, [&](int k, int j) { return k < 2 ? fy[k][j] : fd[k - 2][j]; },
+                                  [&](int k) -> f32x4 & { return k < 2 ? yS[c][k] : dG[c][k - 2]; });
+                __builtin_amdgcn_sched_barrier(0);  // no operands of later tiles in registers yet
             }
         }
+        __syncthreads();
+        // pairs of tokens: rows s, columns t
+        float cm[2][4] = {}, cp[2][4] = {}, rm[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = row_lanes(read[i]), z = row_lanes(write[i]);
-            if (r == 0) {
-                sh.read[hf][trow + i] = x;
-                sh.write[hf][trow + i] = z;
+        for (int t = 0; t < 2; ++t) {
+            const int ta = 2 * th + t, tt = 16 * ta + r;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int sa = 2 * m + ch;
+                f32x4 c1 = zero, c2 = zero;
+                __builtin_amdgcn_sched_barrier(0);
+                if (sa <= ta) {
+                    f32x4 qk = zero, kk = zero;
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        bf16x8 s[NT], tq[NT], tk[NT];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            s[n] = fragment(p.kf, key + (kb * 4 + sa) * NT + n, l);
+                            tq[n] = fragment(p.qf, key + (kb * 4 + ta) * NT + n, l);
+                            tk[n] = fragment(p.kf, key + (kb * 4 + ta) * NT + n, l);
+                        }
+                        qk = product<NT, NT>(s, tq, qk);
+                        kk = product<NT, NT>(s, tk, kk);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int s = 16 * sa + 4 * q + i;
+                        const float e = tt >= s ? sh.gt.decay(tt, s) : 0.f, beta = sh.gt.beta[s];
+                        const float a1 = tt >= s ? n1[m][t][i] : 0.f, a2 = tt > s ? n2[m][t][i] : 0.f;
+                        c1[i] = e * beta * a1;
+                        c2[i] = -e * beta * a2;
+                        const float pair = tt >= s ? e * (a1 * qk[i] - a2 * kk[i]) : 0.f;
+                        cp[m][i] += pair;
+                        if (tt > s) {  // a token's own pair does not pass its gate
+                            rm[t] += pair * beta;
+                            cm[m][i] += pair * beta;
+                        }
+                    }
+                }
+                *reinterpret_cast<f32x4 *>(&sh.C1[tt][16 * sa + 4 * q]) = c1;
+                *reinterpret_cast<f32x4 *>(&sh.C2[tt][16 * sa + 4 * q]) = c2;
+            }
+            rm[t] = quarters(rm[t]);
+            if (q == 0) sh.row_m[ch][tt] = rm[t];
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = row_lanes(cm[m][i]), z = row_lanes(cp[m][i]);
+                if (r == 0) {
+                    sh.col_m[th][16 * (2 * m + ch) + 4 * q + i] = x;
+                    sh.col_pair[th][16 * (2 * m + ch) + 4 * q + i] = z;
+                }
+            }
+        // what the states give, and its dot products with q and k
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int ta = 2 * th + t, tt = 16 * ta + r;
+            const float front = sh.gt.front[tt], behind = sh.gt.behind[tt], beta = sh.gt.beta[tt];
+            float read = 0.f, write = 0.f;
+#pragma unroll
+            for (int c = 0; c < KB; c += 2) {
+                const int kb = (ch * KB + c) / 2;
+                __builtin_amdgcn_sched_barrier(0);
+                float qv[8], kv[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) qv[e] = kv[e] = 0.f;
+#pragma unroll
+                for (int n = NT - 1; n >= 0; --n) {
+                    const u32x4 a = __builtin_bit_cast(u32x4, fragment(p.qf, key + (kb * 4 + ta) * NT + n, l));
+                    const u32x4 b = __builtin_bit_cast(u32x4, fragment(p.kf, key + (kb * 4 + ta) * NT + n, l));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        qv[e] += __uint_as_float(e & 1 ? a[e / 2] & 0xffff0000u : a[e / 2] << 16);
+                        kv[e] += __uint_as_float(e & 1 ? b[e / 2] & 0xffff0000u : b[e / 2] << 16);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int cc = c + e / 4, i = e % 4;
+                    const float fo = front * oS[cc][t][i], fy = front * yS[cc][t][i], bg = behind * dG[cc][t][i];
+                    oS[cc][t][i] = fo;
+                    dG[cc][t][i] = fmaf(beta, bg, -fy);
+                    read += qv[e] * fo - kv[e] * fy;
+                    write = fmaf(kv[e], bg, write);
+                }
+            }
+            read = quarters(read);
+            write = quarters(write);
+            if (q == 0) {
+                sh.read[ch][tt] = read;
+                sh.write[ch][tt] = write;
             }
         }
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) dot += __shfl_xor(dot, s);
-        if (l == 0) sh.dot[tid >> 6] = dot;
+        if (l == 0) sh.dot[w] = dot;
         __syncthreads();
-        if (tid < 64) {
+        if (w == 0) {
             float db = sh.write[0][l] + sh.write[1][l], up = db * sh.gt.beta[l];
-            float down = sh.read[0][l] + sh.read[1][l] + sh.row_m[0][l] + sh.row_m[1][l], dots = 0.f;
+            float down = sh.read[0][l] + sh.read[1][l] + sh.row_m[0][l] + sh.row_m[1][l];
             const float mine = up;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
+            for (int m = 0; m < 2; ++m) {
                 db += sh.col_pair[m][l];
                 down -= sh.col_m[m][l];
             }
@@ -253,9 +330,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
                 if (l + d < 64) down += x;
                 if (l >= d) up += y;
             }
-#pragma unroll
-            for (int m = 0; m < 8; ++m) dots += sh.dot[m];
-            const float kept = sh.gt.whole * dots;
+            const float kept = sh.gt.whole * (sh.dot[0] + sh.dot[1] + sh.dot[2] + sh.dot[3]);
             const bool cuts = l ? sh.gt.cut[l] != sh.gt.cut[l - 1] : sh.gt.cut[0] != 0;
             if (l < at.n) {
                 const long o = (at.row0 + l) * p.Hv + hv;
@@ -263,22 +338,76 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
                 st_elem(p.db, o, db, p.gate_bf16);
             }
         }
-    }
+        // + C1 k to dq, + C1^T q + (C2 + C2^T) k to dk
 #pragma unroll
-    for (int a = 0; a < KB; ++a)
+        for (int b = 0; b < 2; ++b) {
+            bf16x8 c1[2][NX], c1t[2][NX], c2[2][NX];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = trow + i, ch = 32 * a + 16 * hf + r;
-            if (t >= at.n || ch >= p.dk) continue;
-            const long o = ((at.row0 + t) * p.Hk + hk) * p.dk + ch;
-            st_elem(p.dq, o, dq[a][i], NT == 1);
-            st_elem(p.dkk, o, dk[a][i], NT == 1);
+            for (int t = 0; t < 2; ++t) {
+                float x1[8], x1t[8], x2[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int m = 16 * (2 * th + t) + r, o = 32 * b + perm(q, e);
+                    x1[e] = sh.C1[m][o];
+                    x1t[e] = sh.C1[o][m];
+                    x2[e] = sh.C2[m][o] + sh.C2[o][m];
+                }
+                split<NX>(x1, c1[t]);
+                split<NX>(x1t, c1t[t]);
+                split<NX>(x2, c2[t]);
+            }
+#pragma unroll
+            for (int c = 0; c < KB; ++c) {
+                bf16x8 kt[NT], qt[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    kt[n] = fragment(p.ktf, key + (b * 2 * KB + ch * KB + c) * NT + n, l);
+                    qt[n] = fragment(p.qtf, key + (b * 2 * KB + ch * KB + c) * NT + n, l);
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    oS[c][t] = product<NT, NX>(kt, c1[t], oS[c][t]);
+                    dG[c][t] = product<NT, NX>(qt, c1t[t], dG[c][t]);
+                    dG[c][t] = product<NT, NX>(kt, c2[t], dG[c][t]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
-}
-
-template <int NT, int KB>
-const void *pick(int jb) {
-    return jb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<NT, KB, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<NT, KB, 4>);
+        // a shared key head's gradients are summed over its value heads, always in the same order
+        const bool last = h == p.group - 1;
+#pragma unroll
+        for (int c = 0; c < KB; ++c)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (p.group > 1) {
+                    f32x4 *sum = reinterpret_cast<f32x4 *>(p.sum) + ((((long)slot * p.Hk + hk) * 4 + w) * KB + c) * 256 + t * 128 + l;
+                    if (h) {
+                        oS[c][t] += sum[0];
+                        dG[c][t] += sum[64];
+                    }
+                    if (!last) {
+                        sum[0] = oS[c][t];
+                        sum[64] = dG[c][t];
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                const int row = 16 * (2 * th + t) + r, chan = 16 * (ch * KB + c) + 4 * q;
+                if (!last || row >= at.n || chan >= p.dk) continue;
+                const long o = ((at.row0 + row) * p.Hk + hk) * p.dk + chan;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const f32x4 x = m ? dG[c][t] : oS[c][t];
+                    void *out = m ? p.dkk : p.dq;
+                    if constexpr (NT == 1) {
+                        typedef uint32_t wu2 __attribute__((ext_vector_type(2), aligned(2)));
+                        *reinterpret_cast<wu2 *>(static_cast<uint16_t *>(out) + o) = (wu2){pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+                    } else {
+                        typedef float wf4 __attribute__((ext_vector_type(4), aligned(4)));
+                        *reinterpret_cast<wf4 *>(static_cast<float *>(out) + o) = (wf4){x[0], x[1], x[2], x[3]};
+                    }
+                }
+            }
+    }
 }
 
 }  // namespace
@@ -286,9 +415,10 @@ const void *pick(int jb) {
 hipError_t launch_delta_grad(const DeltaParams &p0, hipStream_t s) {
     DeltaParams p = p0;
     void *args[] = {&p};
-    const int kb = delta_blocks(p.dk), jb = delta_blocks(p.dv);
-    const void *fn = p.io_bf16 ? (kb == 2 ? pick<1, 2>(jb) : pick<1, 4>(jb)) : (kb == 2 ? pick<3, 2>(jb) : pick<3, 4>(jb));
-    return hipLaunchKernel(fn, dim3((unsigned)p.nslot * p.Hk), dim3(512), args, 0, s);
+    const int kb = delta_blocks(p.dk);
+    const void *fn = p.io_bf16 ? (kb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<1, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<1, 4>))
+                               : (kb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<3, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<3, 4>));
+    return hipLaunchKernel(fn, dim3((unsigned)p.nslot * p.Hk), dim3(256), args, 0, s);
 }
 
 }  // namespace gdr

@@ -92,16 +92,16 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaParams p) {
     }
     if (hv % p.group) return;
     const long key = (long)slot * p.Hk + hk;
-    for (int i = w; i < 4 * KB * NT; i += 4) {  // k and q by rows: tile a, block kb of channels, term n
-        const int n = i % NT, kb = i / NT % KB, a = i / NT / KB;
+    for (int i = w; i < 4 * KB * NT; i += 4) {  // k and q by rows: block kb of channels, tile a, term n
+        const int n = i % NT, a = i / NT % 4, kb = i / NT / 4;
         const uint16_t *kr = &Kt[n][16 * a + r][32 * kb + 4 * q], *qr = &Qt[n][16 * a + r][32 * kb + 4 * q];
         const u32x2 k0 = *reinterpret_cast<const u32x2 *>(kr), k1 = *reinterpret_cast<const u32x2 *>(kr + 16);
         const u32x2 q0 = *reinterpret_cast<const u32x2 *>(qr), q1 = *reinterpret_cast<const u32x2 *>(qr + 16);
         put_fragment(p.kf, key * (4 * KB * NT) + i, l, as_bf16x8((u32x4){k0[0], k0[1], k1[0], k1[1]}));
         put_fragment(p.qf, key * (4 * KB * NT) + i, l, as_bf16x8((u32x4){q0[0], q0[1], q1[0], q1[1]}));
     }
-    for (int i = w; i < 4 * KB * NT; i += 4) {  // and by channels: tile a of channels, block tb of tokens
-        const int n = i % NT, tb = i / NT % 2, a = i / NT / 2;
+    for (int i = w; i < 4 * KB * NT; i += 4) {  // and by channels: block tb of tokens, tile a of channels
+        const int n = i % NT, a = i / NT % (2 * KB), tb = i / NT / (2 * KB);
         u32x4 kw, qw;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -138,8 +138,8 @@ size_t delta_workspace(DeltaParams &p, bool bwd, char *base) {
     p.tf = take(heads * kDeltaTri * 1024);
     p.pf = take(heads * kDeltaTri * 1024);
     p.gates = reinterpret_cast<float *>(take(heads * kDeltaGates * 4));
-    p.y = bwd ? reinterpret_cast<float *>(take(heads * kDeltaC * p.dv * 4)) : nullptr;
-    p.G = bwd ? reinterpret_cast<float *>(take(heads * p.dk * p.dv * 4)) : nullptr;
+    p.back = bwd ? reinterpret_cast<float *>(take(heads * delta_tiles(p.dk, p.dv) * 1024)) : nullptr;
+    p.sum = bwd && p.group > 1 ? reinterpret_cast<float *>(take((size_t)p.nslot * p.Hk * 16 * delta_blocks(p.dk) * 1024)) : nullptr;
     return at;
 }
 

@@ -536,7 +536,7 @@ int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *
  *   io_dtype: q, k, v, o and their gradients;  gate_dtype: log_gate, beta and their gradients
  *   ldq, ldk, ldv, ldg, ldb  elements between successive tokens (b, t) of q, k, v, log_gate and beta; 0 means dense,
  *            larger for slices of a fused projection's output
- * B * T below 2^30, heads at most 65536, and chunks times value heads times 512 below 2^32 (else GDR_EUNSUPPORTED); chunks
+ * B * T below 2^30, heads at most 65536, Hk * dk, Hv * dv and the strides (a step's excepted) at most 2^20, and chunks times value heads times 512 below 2^32 (else GDR_EUNSUPPORTED); chunks
  * are B * ceil(T / 64), or floor(T / 64) + n_seq when packed. */
 typedef struct gdr_delta_desc {
     int32_t B, T, Hk, Hv, dk, dv;
@@ -556,9 +556,9 @@ typedef struct gdr_delta_desc {
  *   S0, ST    [B, Hv, dk, dv] fp32 ([n_seq, ...] when packed): state before and after each sequence; S0 NULL means zero,
  *             ST NULL not written, ST == S0 is allowed (in-place resume) without seq_off; an empty sequence gives ST = S0
  *   o         [B, T, Hv, dv] io_dtype, dense
- *   ckpt      NULL, or [chunks, Hv, dk + GDR_DELTA_CHUNK, dv] fp32: of each chunk of 64 tokens the state before it and
- *             what its tokens write, for the backward pass; chunks that hold no rows are not written.  A sequence's chunks
- *             begin at its first row.
+ *   ckpt      NULL, or gdr_delta_ckpt_size(desc, n_seq) bytes: of each chunk of GDR_DELTA_CHUNK tokens the state before it
+ *             and what its tokens write, fp32, for the backward pass of the same library (the order of its values is the
+ *             library's own).  A sequence's chunks begin at its first row.
  *   workspace at least gdr_delta_workspace_size(desc, n_seq, 0) bytes, 16-byte aligned; its contents on entry do not matter.
  *             n_seq is 0 for dense batches.  One workspace serves one call at a time: calls, or graphs, that may run at the
  *             same time need one each.
@@ -566,6 +566,7 @@ typedef struct gdr_delta_desc {
  * other output.  Results are deterministic.
  */
 size_t gdr_delta_workspace_size(const gdr_delta_desc *desc, int32_t n_seq, int32_t backward);
+size_t gdr_delta_ckpt_size(const gdr_delta_desc *desc, int32_t n_seq);
 int gdr_delta_fwd(const gdr_delta_desc *desc, const void *q, const void *k, const void *v, const void *log_gate,
                   const void *beta, const int32_t *seq_off, int32_t n_seq, const float *S0, void *o, float *ST, float *ckpt,
                   void *workspace, size_t workspace_bytes, void *stream);
