@@ -51,8 +51,9 @@ struct DeltaParams {
     void *dq, *dkk, *dvv, *dg, *db;
     float *dS0;
     // workspace
-    char *kf, *ktf, *qf, *qtf;  // per (slot, key head)
-    char *tf, *pf;              // per (slot, value head): T and Q, or their transposes (backward)
+    int raw;         // k and q are copied to shared memory as they are (bf16, 16-byte aligned rows)
+    char *kf, *qf;   // per (slot, key head), as operands: not used when raw
+    char *tf, *pf;   // per (slot, value head), as operands: T and Q, or their transposes (backward)
     float *gates;
     float *back;  // like ckpt: the gradient of the state behind the chunk, and y
     float *sum;   // gradients of q and k of shared key heads while they are summed
@@ -79,7 +80,8 @@ hipError_t launch_delta_step(const DeltaStepParams &p, hipStream_t s);
 
 // Tiles are 16 x 16: lane (r, q) has rows 4 q .. 4 q + 3 of column r, as the matrix cores leave a result.  A chunk's
 // tiles lie by columns of the state, of each first those of the state's rows and then those of its 64 tokens.
-inline __host__ __device__ int delta_row_tiles(int dk) { return (dk + 15) / 16; }
+// Row 4 q + i of tile a is channel 32 (a / 2) + 8 q + 4 (a % 2) + i: eight channels of a lane quarter in a row.
+inline __host__ __device__ int delta_row_tiles(int dk) { return (dk + 31) / 32 * 2; }
 inline __host__ __device__ int delta_col_tiles(int dv) { return (dv + 15) / 16; }
 inline __host__ __device__ long delta_tiles(int dk, int dv) { return (long)delta_col_tiles(dv) * (delta_row_tiles(dk) + kDeltaC / 16); }
 
@@ -195,6 +197,29 @@ __device__ __forceinline__ f32x4 product(const bf16x8 (&a)[NA], const bf16x8 (&b
 // more at any byte address) as terms: bf16 as they are, fp32 split.
 typedef uint32_t wu4 __attribute__((ext_vector_type(4), aligned(2)));
 
+// Elements 0 to 3 and 16 to 19 from there on: a lane's part of a block of 32 in the order of perm.
+template <int NT>
+__device__ __forceinline__ void load44(const void *base, long at, bool first, bool second, bf16x8 (&t)[NT]) {
+    if constexpr (NT == 1) {
+        typedef uint32_t wu2 __attribute__((ext_vector_type(2), aligned(2)));
+        wu2 a = {0, 0}, b = {0, 0};
+        if (first) a = *reinterpret_cast<const wu2 *>(static_cast<const uint16_t *>(base) + at);
+        if (second) b = *reinterpret_cast<const wu2 *>(static_cast<const uint16_t *>(base) + at + 16);
+        t[0] = as_bf16x8((u32x4){a[0], a[1], b[0], b[1]});
+    } else {
+        wu4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+        if (first) a = *reinterpret_cast<const wu4 *>(static_cast<const float *>(base) + at);
+        if (second) b = *reinterpret_cast<const wu4 *>(static_cast<const float *>(base) + at + 16);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __uint_as_float(a[i]);
+            x[4 + i] = __uint_as_float(b[i]);
+        }
+        split<NT>(x, t);
+    }
+}
+
 template <int NT>
 __device__ __forceinline__ void load8(const void *base, long at, bool there, bf16x8 (&t)[NT]) {
     if constexpr (NT == 1) {
@@ -242,6 +267,10 @@ __device__ __forceinline__ void store1(Buf b, uint32_t at, float x) {
     else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, at, 0, 0);
 }
 
+// Place in an operand's kilobyte of lane (r, q)'s 16 bytes, of k and q: the rows swapped about by quarters, for the
+// transposing reads.
+__device__ __forceinline__ int key_place(int r, int q) { return 16 * q + (r ^ 4 * q); }
+
 __device__ __forceinline__ bf16x8 fragment(const char *base, long at, int lane) {
     return as_bf16x8(*reinterpret_cast<const u32x4 *>(base + at * 1024 + lane * 16));
 }
@@ -249,6 +278,67 @@ __device__ __forceinline__ bf16x8 fragment(const char *base, long at, int lane) 
 __device__ __forceinline__ void put_fragment(char *base, long at, int lane, bf16x8 x) {
     *reinterpret_cast<u32x4 *>(base + at * 1024 + lane * 16) = __builtin_bit_cast(u32x4, x);
 }
+
+typedef __attribute__((address_space(3))) char *lds_bytes;
+typedef __attribute__((address_space(3))) u32x2 *lds_u32x2;
+typedef __attribute__((address_space(3))) u32x4 *lds_u32x4;
+
+// A matrix of ROWS x COLS as NT terms in shared memory, [term][column][row], the 32-byte units of 16 rows swapped about so
+// that eight columns lie in different banks.  A lane's place for all tiles of 16 rows is one offset: the tile's
+// number changes bits of it that only the swap also holds.  The transposing LDS read makes operands of it whose
+// contraction runs over the columns.
+template <int ROWS, int NT, int COLS>
+struct Staged {
+    uint16_t x[NT][COLS][ROWS];
+    static constexpr int kCol = 2 * ROWS, kTerm = COLS * kCol;
+    static __device__ __forceinline__ uint32_t place(int j) { return j * kCol + ((ROWS == 64 ? j >> 1 & 3 : j & (ROWS / 16 - 1)) << 5); }
+    __device__ __forceinline__ lds_bytes base() { return (lds_bytes)&x[0][0][0]; }
+    // rows 4 q .. 4 q + 3 of a tile in column j, at put_place(j, q)
+    static __device__ __forceinline__ uint32_t put_place(int j, int q) { return place(j) + 8 * q; }
+    __device__ __forceinline__ void put(uint32_t at, int tile, f32x4 v) {
+        lds_bytes to = base() + (at ^ (uint32_t)tile << 5);
+        float r[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            *(lds_u32x2)(to + n * kTerm) = (u32x2){high_halves(r[0], r[1]), high_halves(r[2], r[3])};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
+        }
+    }
+    // rows 8 m .. 8 m + 7 of column j, put or got whole
+    __device__ __forceinline__ void put8(int j, int m, const bf16x8 (&t)[NT]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) *(lds_u32x4)(base() + (place(j) ^ (uint32_t)(m >> 1) << 5) + 16 * (m & 1) + n * kTerm) = __builtin_bit_cast(u32x4, t[n]);
+    }
+    __device__ __forceinline__ void get8(int j, int m, bf16x8 (&t)[NT]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) t[n] = as_bf16x8(*(lds_u32x4)(base() + (place(j) ^ (uint32_t)(m >> 1) << 5) + 16 * (m & 1) + n * kTerm));
+    }
+    // the operand whose rows are channel tile a's (delta_row_tiles) of matrices with channels as rows, at key_get_place(r, q)
+    static __device__ __forceinline__ uint32_t key_get_place(int r, int q) {
+        return (place(4 * q + (r >> 2)) ^ (uint32_t)(r & 2) << 4) + 16 * (r & 1);
+    }
+    __device__ __forceinline__ void key_get(uint32_t at, int a, int b, bf16x8 (&t)[NT]) {
+        lds_bytes from = base() + (at ^ (uint32_t)(a >> 1) << 6) + 8 * (a & 1) + b * 32 * kCol;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm)));
+            const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm + 16 * kCol)));
+            t[n] = as_bf16x8((u32x4){x[0], x[1], y[0], y[1]});
+        }
+    }
+    // the operand whose rows are the 16 of a tile and whose contraction the 32 columns from 32 b on (perm), at get_place(r, q)
+    static __device__ __forceinline__ uint32_t get_place(int r, int q) { return place(4 * q + (r >> 2)) + 8 * (r & 3); }
+    __device__ __forceinline__ void get(uint32_t at, int tile, bf16x8 (&t)[NT], int b = 0) {
+        lds_bytes from = base() + (at ^ (uint32_t)tile << 5) + b * 32 * kCol;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm)));
+            const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm + 16 * kCol)));
+            t[n] = as_bf16x8((u32x4){a[0], a[1], c[0], c[1]});
+        }
+    }
+};
 
 // The gates of a chunk, in shared memory.  P is summed in 64 bits: behind a strong decay the
 // difference of two fp32 sums would have lost the weak ones.  A gate of -inf cuts: it adds nothing to P,
@@ -260,7 +350,8 @@ struct ChunkGates {
     float whole;
 
     __device__ __forceinline__ float decay(int t, int s) const {
-        return cut[t] == cut[s] ? expf((float)(P[t] - P[s])) : 0.f;
+        const float e = expf((float)(P[t] - P[s]));
+        return cut[t] == cut[s] ? e : 0.f;
     }
 };
 

@@ -1,6 +1,4 @@
 // delta_chain.hip -- the recurrence of the delta rule over a sequence's chunks, forward and backward (delta.hpp).
-#include <stdlib.h>
-
 #include <type_traits>
 
 #include "delta.hpp"
@@ -8,20 +6,15 @@
 namespace gdr {
 namespace {
 
-constexpr int kRing = 3;      // pieces in shared memory at once
-constexpr int kPiece = 50;    // most fragments of a piece
 constexpr int kLoaders = 2;   // waves that copy
 constexpr int kGroup = 12;    // most fragments that a wave reads ahead
+
+__device__ const u32x4 kNothing = {0, 0, 0, 0};  // what is copied for rows and channels that are not there
 
 // LDS traffic waited for, global memory not.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// At most N vector memory operations of this wave still under way.
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-    static_assert(N < 64, "the counter's range");
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | N >> 4 << 14);
-}
+__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
 template <int I, int N, class F>
 __device__ __forceinline__ void each(F &&f) {
@@ -37,41 +30,15 @@ constexpr int tri_index(int a, int b) {
     return UPPER ? (a < 2 ? 2 * a + b : b == 1 ? a + 2 : -1) : (a < 2 ? (b == 0 ? a : -1) : 2 * a - 2 + b);
 }
 
-// A chunk's operands, copied in pieces of at most 50 fragments of 1 KB, and the groups of products that read them.
-// (fp32 operands have three fragments for one: more pieces, and smaller groups.)
+// Groups of products, by the operand that they read from shared memory.
 enum Part { kK, kQ, kT, kP, kC, kQC };  // k, q, T, Q (their transposes in the backward pass), k^T, q^T
 
 template <int NT, int KB, bool BWD>
 struct Plan {
-    static constexpr int key = 4 * KB * NT;  // fragments of k, q, k^T, q^T
-    static constexpr int N = NT == 1 ? 2 : BWD ? 5 : 4;  // pieces
-    // parts in the order in which they are copied, and the piece of each
-    static constexpr Part part(int i) {
-        constexpr Part f[] = {kK, kQ, kT, kP, kC}, b[] = {kP, kK, kQC, kT, kC};
-        return BWD ? b[i] : f[i];
-    }
-    static constexpr int piece(int i) {
-        constexpr int f1[] = {0, 0, 0, 1, 1}, b1[] = {0, 0, 1, 1, 1}, f3[] = {0, 1, 2, 2, 3};
-        return NT == 1 ? (BWD ? b1[i] : f1[i]) : BWD ? i : f3[i];
-    }
-    static constexpr int size(int i) { return part(i) == kT || part(i) == kP ? kDeltaTri : key; }
-    static constexpr int first(int i) { return i > 0 && piece(i - 1) == piece(i) ? first(i - 1) + size(i - 1) : 0; }
-    static constexpr int count(int m) {  // with the gates, behind the first piece
-        int n = m == 0;
-        for (int i = 0; i < 5; ++i) n += piece(i) == m ? size(i) : 0;
-        return n;
-    }
-    static constexpr int copies(int m) { return (count(m) + kLoaders - 1) / kLoaders; }
-    static constexpr int part_of(int m, int f) {
-        for (int i = 0; i < 5; ++i)
-            if (piece(i) == m && f >= first(i) && f < first(i) + size(i)) return i;
-        return -1;
-    }
-    static constexpr int index(Part x) {
-        for (int i = 0; i < 5; ++i)
-            if (part(i) == x) return i;
-        return -1;
-    }
+    // a chunk's operands in shared memory, in fragments of 1 KB: k, q, T, Q
+    static constexpr int key = 4 * KB * NT, atQ = key, atT = 2 * key, atP = atT + kDeltaTri;
+    static constexpr int nP = BWD || NT == 3 ? 3 : 2, size = atP + 6 * nP;  // terms of Q: forward, only o reads it
+    static constexpr int sets = NT == 1 ? 2 : 1;  // chunks at once
     // groups: of k a block of channels, of q GQ blocks, of T and Q a block of their columns, of k^T and q^T GC tiles of
     // channels.  Backward with bf16, q^T's second half comes behind T: products beside the splits that T's result needs.
     static constexpr int GQ = NT == 1 ? 2 : 1, GC = NT == 1 ? 2 * KB : 4;
@@ -91,92 +58,94 @@ struct Plan {
         }
         return {kK, 0};
     }
-    static constexpr bool opens(int i) {  // the group is the first of a piece
-        if (i == 0) return true;
-        return piece(index(at(i).x)) != piece(index(at(i - 1).x));
-    }
 };
 
 // A workgroup has NW tiles of 16 columns of one value head's state, a wave each, all rows of it in registers.
-// Between those waves nothing is exchanged: every product's result is the next one's operand as it
-// lies (perm in delta.hpp).  Two more waves copy the operands, which the tiles share, to a ring in shared
-// memory, up to two pieces ahead.
+// Between those waves nothing is exchanged: every product's result is the next one's operand as it lies (perm in
+// delta.hpp).  Two more waves copy the operands, which the tiles share, to shared memory: with bf16 a chunk ahead, with
+// fp32, whose operands are three times as large, as soon as the chunk before is done with a part.
 // KEEP: the states before the chunks and E are stored, for the backward pass.
 template <int NT, int KB, bool BWD, bool KEEP, int NW>
 __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(DeltaParams p, int heads8) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
     typedef Plan<NT, KB, BWD> P;
-    __shared__ __attribute__((aligned(16))) char ring[kRing][kPiece * 1024];
-    __shared__ __attribute__((aligned(16))) float gring[4][kDeltaGates];  // of chunk c in c % 4: copies run less than three chunks ahead
+    __shared__ __attribute__((aligned(16))) char sets[P::sets][P::size * 1024];
+    __shared__ __attribute__((aligned(16))) float gring[2][kDeltaGates];
     const int head = blockIdx.x % heads8;
     if (head >= p.nseq * p.Hv) return;  // uniform over the workgroup
     const int seq = head / p.Hv, hv = head % p.Hv, hk = hv / p.group;
     long row0;
     const int len = tokens_of(p, seq, row0), nc = (len + kDeltaC - 1) / kDeltaC;
     const int slot0 = first_slot(p, seq);
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, r = l & 15, q = l >> 4;
 
     if (w >= NW) {  // a copying wave has every second fragment
-        if (nc == 0) return;
         const int half = w - NW;
-        int to = 0;  // place in the ring of the next piece
-        auto copy = [&](int c, auto M) __attribute__((always_inline)) {  // piece M of chunk c
-            constexpr int m = M;
-            c = min(c, nc - 1);  // behind the last chunk its pieces come again, to be counted
-            const long slot = slot0 + (BWD ? nc - 1 - c : c), kh = slot * p.Hk + hk, vh = slot * p.Hv + hv;
-            const char *gates = reinterpret_cast<const char *>(p.gates + vh * kDeltaGates);
-            each<0, P::copies(m)>([&](auto U) __attribute__((always_inline)) {
-                // both waves' fragments of this turn are of one part, or the second's is the next part's first
-                auto from = [&](auto F) __attribute__((always_inline)) -> const char * {
-                    constexpr int f = F < P::count(m) ? int(F) : P::count(m) - 1, i = P::part_of(m, f);
-                    if constexpr (i < 0) return gates;
-                    else {
-                        constexpr Part x = P::part(i);
-                        const char *base = x == kK ? p.kf : x == kQ ? p.qf : x == kT ? p.tf : x == kP ? p.pf : x == kC ? p.ktf : p.qtf;
-                        return base + ((x == kT || x == kP ? vh * kDeltaTri : kh * P::key) + (f - P::first(i))) * 1024;
+        // of chunk number c in the order of the pass: k and the gates (first), the rest
+        auto copy = [&](int c, bool first, bool rest) __attribute__((always_inline)) {
+            const int pos = BWD ? nc - 1 - c : c, n = len - pos * kDeltaC;
+            const long slot = slot0 + pos, kh = slot * p.Hk + hk, vh = slot * p.Hv + hv;
+            char *to = sets[P::sets == 2 ? c & 1 : 0];
+            auto keys = [&](const void *x, int64_t ld, const char *made, int at) __attribute__((always_inline)) {
+                if (NT == 1 && p.raw) {  // lane's place: row pr, channels from 8 q on
+                    const int pr = r ^ 4 * q;
+                    const uint16_t *from = static_cast<const uint16_t *>(x) + (row0 + (long)pos * kDeltaC + pr) * ld + (long)hk * p.dk + 8 * q;
+#pragma unroll
+                    for (int f = 0; f < P::key; f += kLoaders) {
+                        const int i = f + half, a = i & 3, kb = i >> 2;
+                        const bool there = 16 * a + pr < n && 32 * kb + 8 * q < p.dk;
+                        dma16(there ? static_cast<const void *>(from + 16 * a * ld + 32 * kb) : &kNothing, to + (at + i) * 1024);
                     }
-                };
-                constexpr int f0 = 2 * U, f1 = 2 * U + 1;
-                const char *src = half ? from(std::integral_constant<int, f1>()) : from(std::integral_constant<int, f0>());
-                const int f = half ? f1 : f0;
-                dma16(src + l * 16, m == 0 && f >= P::count(0) - 1 ? reinterpret_cast<char *>(gring[c & 3]) : &ring[to][f * 1024]);
-            });
-            to = to == kRing - 1 ? 0 : to + 1;
+                } else {
+                    const char *from = made + (kh * P::key + half) * 1024 + l * 16;
+#pragma unroll 8
+                    for (int f = 0; f < P::key; f += kLoaders) dma16(from + f * 1024, to + (at + half + f) * 1024);
+                }
+            };
+            if (first) {
+                keys(p.k, p.ldk, p.kf, 0);
+                if (half) dma16(reinterpret_cast<const char *>(p.gates + vh * kDeltaGates) + l * 16, gring[c & 1]);
+            }
+            if (rest) {
+                keys(p.q, p.ldq, p.qf, P::atQ);
+                const char *t = p.tf + (vh * kDeltaTri + half) * 1024 + l * 16, *s = p.pf + (vh * kDeltaTri + half) * 1024 + l * 16;
+#pragma unroll
+                for (int f = 0; f < kDeltaTri; f += kLoaders) dma16(t + f * 1024, to + (P::atT + half + f) * 1024);
+#pragma unroll
+                for (int f = 0; f < 6 * P::nP; f += kLoaders) dma16(s + f * 1024, to + (P::atP + half + f) * 1024);
+            }
         };
-        copy(0, std::integral_constant<int, 0>());
-        copy(0, std::integral_constant<int, 1>());
-        for (int c = 0; c < nc; ++c)
-            each<0, P::N>([&](auto M) __attribute__((always_inline)) {
-                constexpr int m = M;
-                wait_copies<P::copies((m + 1) % P::N)>();  // this piece is there, the one behind it may not be
-                lds_barrier();                            // and the piece before is no longer read
-                copy(c + (m + 2) / P::N, std::integral_constant<int, (m + 2) % P::N>());
-            });
-        wait_copies<0>();  // no copy outlives the workgroup
+        if (nc > 0) copy(0, true, true);
+        for (int c = 0; c < nc; ++c) {
+            wait_copies();  // this chunk's are there
+            lds_barrier();  // and the chunk before is done
+            if constexpr (P::sets == 2) {
+                if (c + 1 < nc) copy(c + 1, true, true);
+            } else {
+                lds_barrier();  // q, T and Q are no longer read
+                if (c + 1 < nc) copy(c + 1, false, true);
+                lds_barrier();  // nor is k
+                if (c + 1 < nc) copy(c + 1, true, false);
+            }
+        }
         return;
     }
 
-    const int r = l & 15, q = l >> 4, col = 16 * ((int)(blockIdx.x / heads8) * NW + w) + r;
+    const int col = 16 * ((int)(blockIdx.x / heads8) * NW + w) + r;
     const bool mine = col < p.dv;
     const long sstate = (long)p.dk * p.dv;
     const int tile = (blockIdx.x / heads8) * NW + w, na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv);
-    int turn = 0;
-    const char *piece = nullptr;
-    auto next = [&]() __attribute__((always_inline)) {
-        lds_barrier();
-        piece = ring[turn];
-        turn = turn == kRing - 1 ? 0 : turn + 1;
-    };
     // accesses by tiles go through range-checked buffers: no branch per element for rows and channels that are not there
     constexpr bool BF = NT == 1;
     constexpr int es = BF ? 2 : 4;
-    const uint32_t away = mine ? 0 : kNowhere, srow = 4 * p.dv, sat = 4 * q * srow + 4 * col + away;
+    const uint32_t away = mine ? 0 : kNowhere, srow = 4 * p.dv, sat = 8 * q * srow + 4 * col + away;
+    auto channel = [](int a, int i) { return 32 * (a / 2) + 4 * (a % 2) + i; };  // of a tile's row, from 8 q on
     auto keep = [&](float *to, const f32x4 (&S)[2 * KB]) __attribute__((always_inline)) {
         const Buf b = buffer(to, 4 * sstate);
 #pragma unroll
         for (int a = 0; a < 2 * KB; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) store1<false>(b, sat + (16 * a + i) * srow, S[a][i]);
+            for (int i = 0; i < 4; ++i) store1<false>(b, sat + channel(a, i) * srow, S[a][i]);
     };
     f32x4 S[2 * KB];
     {
@@ -185,7 +154,7 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
 #pragma unroll
         for (int a = 0; a < 2 * KB; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[a][i] = number<false>(load1<false>(b, sat + (16 * a + i) * srow));
+            for (int i = 0; i < 4; ++i) S[a][i] = number<false>(load1<false>(b, sat + channel(a, i) * srow));
     }
     // v, or do, of the lane's rows 16 a + 4 q + i of a chunk
     const int64_t ldx = BWD ? (int64_t)p.Hv * p.dv : p.ldv;
@@ -220,7 +189,10 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
         const int c = BWD ? nc - 1 - cc : cc;
         const int n = min(kDeltaC, len - c * kDeltaC);
         const long vh = (long)(slot0 + c) * p.Hv + hv, row = row0 + (long)c * kDeltaC;
-        const float *gates = gring[cc & 3] + 4 * q;  // read from the chunk's first piece on
+        const float *gates = gring[cc & 1] + 4 * q;
+        const char *ops = sets[P::sets == 2 ? cc & 1 : 0];
+        const int keyl = key_place(r, q);
+        const lds_bytes ctl = (lds_bytes)(char *)ops + key_place(4 * q + (r >> 2), r & 3) * 16;  // of the transposing reads
         auto front = [&](int a) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4 *>(gates + 16 * a); };
         auto wb = [&](int a) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4 *>(gates + 64 + 16 * a); };
         f32x4 R[4] = {zero, zero, zero, zero}, E[4] = {zero, zero, zero, zero};
@@ -237,19 +209,31 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
         // reads the fragments of group G
         auto load = [&](auto G, bf16x8 (&to)[kGroup]) __attribute__((always_inline)) {
             constexpr Part x = P::at(G).x;
-            constexpr int g = P::at(G).g, at = P::first(P::index(x));
-            if constexpr (P::opens(G)) next();
+            constexpr int g = P::at(G).g;
+            if constexpr (P::sets == 1 && x == kC && g == 0) lds_barrier();  // q, T and Q are no longer read
             if constexpr (x == kT || x == kP) {
-                constexpr int NF = x == kP && !BWD ? NX : 3;
+                constexpr int NF = x == kP ? P::nP : 3, at = x == kT ? P::atT : P::atP;
                 constexpr int t0 = BWD ? 0 : 2 * g, nt = BWD ? 2 + 2 * g : 4 - 2 * g;
 #pragma unroll
                 for (int k = 0; k < nt; ++k)
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) to[k * NF + n] = fragment(piece, at + 3 * tri_index<BWD>(t0 + k, g) + n, l);
-            } else {
-                constexpr int n = (x == kK ? 4 : x == kQ ? 4 * P::GQ : P::GC) * NT;
+                    for (int n = 0; n < NF; ++n) to[k * NF + n] = fragment(ops, at + NF * tri_index<BWD>(t0 + k, g) + n, l);
+            } else if constexpr (x == kK || x == kQ) {
+                constexpr int n = (x == kK ? 4 : 4 * P::GQ) * NT, at = (x == kK ? 0 : P::atQ) + g * n;
 #pragma unroll
-                for (int k = 0; k < n; ++k) to[k] = fragment(piece, at + g * n + k, l);
+                for (int k = 0; k < n; ++k) to[k] = fragment(ops, at + k, keyl);
+            } else {
+#pragma unroll
+                for (int k = 0; k < P::GC; ++k)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        constexpr int b = g * P::GC / (2 * KB);
+                        const int a = (g * P::GC + k) % (2 * KB);
+                        const int at = (x == kC ? 0 : P::atQ) + ((a / 2) * 4 + 2 * b) * NT + n;
+                        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(ctl + at * 1024 + 8 * (a & 1))));
+                        const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(ctl + (at + NT) * 1024 + 8 * (a & 1))));
+                        to[k * NT + n] = as_bf16x8((u32x4){y[0], y[1], z[0], z[1]});
+                    }
             }
         };
         // the products of group G, and beside them the operands of later groups
@@ -269,7 +253,7 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
                     }
                 }
                 if constexpr (BWD && g == KB - 1) {
-                    const float whole = gring[cc & 3][128];
+                    const float whole = gring[cc & 1][128];
 #pragma unroll
                     for (int a = 0; a < 2 * KB; ++a) S[a] = whole * S[a];
                 }
@@ -305,7 +289,7 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
                 if constexpr (g == 0) {
                     split<NX>(E[2], E[3], of[1]);
                     split<3>(wb(2) * E[2], wb(3) * E[3], ef[1]);
-                    const float whole = gring[cc & 3][128];
+                    const float whole = gring[cc & 1][128];
 #pragma unroll
                     for (int a = 0; a < 2 * KB; ++a) S[a] = whole * S[a];
                 }
@@ -347,6 +331,7 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
                 if constexpr (x == kC && g == P::nC - 1) ahead();
             }
         };
+        lds_barrier();  // the chunk's operands are there
         bf16x8 f[2][kGroup];
         load(std::integral_constant<int, 0>(), f[0]);
         each<0, P::groups>([&](auto G) __attribute__((always_inline)) {
@@ -360,6 +345,7 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
                 __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
             });
         });
+        if constexpr (P::sets == 1) lds_barrier();  // k is no longer read
     }
     float *last = BWD ? p.dS0 : p.ST;
     if (last) keep(last + head * sstate, S);
@@ -387,7 +373,7 @@ hipError_t launch_delta_chain(const DeltaParams &p0, bool bwd, hipStream_t s) {
     int heads = (int)(((long)p.nseq * p.Hv + 7) / 8 * 8);
     void *args[] = {&p, &heads};
     const int nt = p.io_bf16 ? 1 : 3, kb = delta_blocks(p.dk), tiles = (p.dv + 15) / 16;
-    const int nw = getenv("NW4") ? 4 : 2;
+    const int nw = (long)heads * ((tiles + 1) / 2) > 256 ? 4 : 2;
     const void *fn = nw == 2 ? pick<2>(bwd, p.ckpt != nullptr, nt, kb) : pick<4>(bwd, p.ckpt != nullptr, nt, kb);
     return hipLaunchKernel(fn, dim3((unsigned)heads * ((tiles + nw - 1) / nw)), dim3(64 * (nw + kLoaders)), args, 0, s);
 }

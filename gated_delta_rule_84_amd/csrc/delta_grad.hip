@@ -21,51 +21,16 @@ namespace {
 
 constexpr int kLC = kDeltaC + 4;
 
-typedef __attribute__((address_space(3))) char *lds_bytes;
-typedef __attribute__((address_space(3))) u32x2 *lds_u32x2;
-
-// Terms of a block of 32 columns: [term][column][row], the 32-byte units of 16 rows swapped about so that eight columns
-// lie in different banks.  A lane's place for all tiles is one offset: the tile's number changes bits of it that only
-// the swap also holds.
-template <int ROWS>
-struct Staged {
-    uint16_t x[3][32][ROWS];
-    static constexpr int kCol = 2 * ROWS, kTerm = 32 * kCol;
-    static __device__ __forceinline__ uint32_t place(int j) { return j * kCol + ((ROWS == 64 ? j >> 1 & 3 : j & (ROWS / 16 - 1)) << 5); }
-    // of rows 4 q .. 4 q + 3 of column j
-    static __device__ __forceinline__ uint32_t put_place(int j, int q) { return place(j) + 8 * q; }
-    __device__ __forceinline__ void put(uint32_t at, int tile, f32x4 v) {
-        lds_bytes to = (lds_bytes)&x[0][0][0] + (at ^ (uint32_t)tile << 5);
-        float r[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            *(lds_u32x2)(to + n * kTerm) = (u32x2){high_halves(r[0], r[1]), high_halves(r[2], r[3])};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
-        }
-    }
-    // of the operand whose rows are the 16 of a tile and whose contraction the 32 columns (perm)
-    static __device__ __forceinline__ uint32_t get_place(int r, int q) { return place(4 * q + (r >> 2)) + 8 * (r & 3); }
-    __device__ __forceinline__ void get(uint32_t at, int tile, bf16x8 (&t)[3]) {
-        lds_bytes from = (lds_bytes)&x[0][0][0] + (at ^ (uint32_t)tile << 5);
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm)));
-            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(from + n * kTerm + 16 * kCol)));
-            t[n] = as_bf16x8((u32x4){a[0], a[1], b[0], b[1]});
-        }
-    }
-};
-
-template <int KB>
+template <int NT, int KB>
 struct GradShared {
     union {
         struct {
-            Staged<32 * KB> S, G;
-            Staged<64> D, Y;
+            Staged<32 * KB, 3, 32> S, G;
+            Staged<64, 3, 32> D, Y;
         };
         struct {
             float C1[kDeltaC][kLC], C2[kDeltaC][kLC];  // [t][s]
+            Staged<32 * KB, NT, kDeltaC> x;            // k or q
         };
     };
     float col_m[2][kDeltaC], col_pair[2][kDeltaC], row_m[2][kDeltaC], read[2][kDeltaC], write[2][kDeltaC], dot[4];
@@ -87,12 +52,11 @@ __device__ __forceinline__ float quarters(float x) {  // over the four quarters
 template <int NT, int KB>
 __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
-    __shared__ __attribute__((aligned(16))) GradShared<KB> sh;
+    __shared__ __attribute__((aligned(16))) GradShared<NT, KB> sh;
     const int hk = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
     const Place at = place_of(p, slot);
     if (at.n <= 0) return;  // uniform over the workgroup
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 1, ch = w & 1;
-    const long key = ((long)slot * p.Hk + hk) * (4 * KB * NT);
     const int na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv), jblocks = (nj + 1) / 2;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -116,8 +80,8 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
 #pragma unroll 1
         for (int jb = 0; jb < jblocks; ++jb) {
             // formed again for each block: kept for all tiles they would take the registers of the sums
-            uint32_t pS = Staged<32 * KB>::put_place(16 * (w & 1) + r, q), gS = Staged<32 * KB>::get_place(r, q);
-            uint32_t pD = Staged<64>::put_place(16 * (w & 1) + r, q), gD = Staged<64>::get_place(r, q);
+            uint32_t pS = Staged<32 * KB, 3, 32>::put_place(16 * (w & 1) + r, q), gS = Staged<32 * KB, 3, 32>::get_place(r, q);
+            uint32_t pD = Staged<64, 3, 32>::put_place(16 * (w & 1) + r, q), gD = Staged<64, 3, 32>::get_place(r, q);
             asm volatile("" : "+v"(pS), "+v"(gS), "+v"(pD), "+v"(gD));
             // wave w brings column tile w & 1 of the block, half of its row tiles
             {
@@ -162,26 +126,8 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
             for (int t = 0; t < 2; ++t) {  // do, by rows: its columns in the operands' order
                 const int row = 16 * (2 * th + t) + r;
                 const long o = ((at.row0 + row) * p.Hv + hv) * p.dv;
-                float x[8];
-                u32x2 wd[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int j = 32 * jb + 16 * k + 4 * q;
-                    const bool there = row < at.n && j < p.dv;
-                    if constexpr (NT == 1) {
-                        typedef uint32_t wu2 __attribute__((ext_vector_type(2), aligned(2)));
-                        wu2 z = {0, 0};
-                        if (there) z = *reinterpret_cast<const wu2 *>(static_cast<const uint16_t *>(p.dout) + o + j);
-                        wd[k] = (u32x2){z[0], z[1]};
-                    } else {
-                        wu4 z = {0, 0, 0, 0};
-                        if (there) z = *reinterpret_cast<const wu4 *>(static_cast<const float *>(p.dout) + o + j);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[4 * k + i] = __uint_as_float(z[i]);
-                    }
-                }
-                if constexpr (NT == 1) fo[t][0] = as_bf16x8((u32x4){wd[0][0], wd[0][1], wd[1][0], wd[1][1]});
-                else split<NT>(x, fo[t]);
+                const int j = 32 * jb + 4 * q;
+                load44<NT>(p.dout, o + j, row < at.n && j < p.dv, row < at.n && j + 16 < p.dv, fo[t]);
             }
             __syncthreads();
 #pragma unroll
@@ -215,6 +161,11 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                 __builtin_amdgcn_sched_barrier(0);  // no operands of later tiles in registers yet
             }
         }
+        // tile t of the rows of k or q, block kb of channels
+        auto rows = [&](const void *x, int64_t ld, int t, int kb, bf16x8 (&to)[NT]) __attribute__((always_inline)) {
+            const int row = 16 * t + r, c = 32 * kb + 8 * q;
+            load8<NT>(x, (at.row0 + row) * ld + (long)hk * p.dk + c, row < at.n && c < p.dk, to);
+        };
         __syncthreads();
         // pairs of tokens: rows s, columns t
         float cm[2][4] = {}, cp[2][4] = {}, rm[2] = {0.f, 0.f};
@@ -231,12 +182,9 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
                         bf16x8 s[NT], tq[NT], tk[NT];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            s[n] = fragment(p.kf, key + (kb * 4 + sa) * NT + n, l);
-                            tq[n] = fragment(p.qf, key + (kb * 4 + ta) * NT + n, l);
-                            tk[n] = fragment(p.kf, key + (kb * 4 + ta) * NT + n, l);
-                        }
+                        rows(p.k, p.ldk, sa, kb, s);
+                        rows(p.q, p.ldq, ta, kb, tq);
+                        rows(p.k, p.ldk, ta, kb, tk);
                         qk = product<NT, NT>(s, tq, qk);
                         kk = product<NT, NT>(s, tk, kk);
                     }
@@ -284,10 +232,12 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                 float qv[8], kv[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) qv[e] = kv[e] = 0.f;
+                bf16x8 tq[NT], tk[NT];
+                rows(p.q, p.ldq, ta, kb, tq);
+                rows(p.k, p.ldk, ta, kb, tk);
 #pragma unroll
                 for (int n = NT - 1; n >= 0; --n) {
-                    const u32x4 a = __builtin_bit_cast(u32x4, fragment(p.qf, key + (kb * 4 + ta) * NT + n, l));
-                    const u32x4 b = __builtin_bit_cast(u32x4, fragment(p.kf, key + (kb * 4 + ta) * NT + n, l));
+                    const u32x4 a = __builtin_bit_cast(u32x4, tq[n]), b = __builtin_bit_cast(u32x4, tk[n]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         qv[e] += __uint_as_float(e & 1 ? a[e / 2] & 0xffff0000u : a[e / 2] << 16);
@@ -338,39 +288,51 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                 st_elem(p.db, o, db, p.gate_bf16);
             }
         }
-        // + C1 k to dq, + C1^T q + (C2 + C2^T) k to dk
+        // + C1^T q to dk, + C1 k to dq and (C2 + C2^T) k to dk
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            bf16x8 c1[2][NX], c1t[2][NX], c2[2][NX];
+        for (int side = 0; side < 2; ++side) {
+            if (side) __syncthreads();
+            constexpr int kPieces = kDeltaC * 4 * KB / 256;
+            bf16x8 x[kPieces][NT];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float x1[8], x1t[8], x2[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int m = 16 * (2 * th + t) + r, o = 32 * b + perm(q, e);
-                    x1[e] = sh.C1[m][o];
-                    x1t[e] = sh.C1[o][m];
-                    x2[e] = sh.C2[m][o] + sh.C2[o][m];
-                }
-                split<NX>(x1, c1[t]);
-                split<NX>(x1t, c1t[t]);
-                split<NX>(x2, c2[t]);
+            for (int i = 0; i < kPieces; ++i) {
+                const int row = (tid + 256 * i) / (4 * KB), m = (tid + 256 * i) % (4 * KB);
+                load8<NT>(side ? p.k : p.q, (at.row0 + row) * (side ? p.ldk : p.ldq) + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, x[i]);
             }
 #pragma unroll
-            for (int c = 0; c < KB; ++c) {
-                bf16x8 kt[NT], qt[NT];
+            for (int i = 0; i < kPieces; ++i) sh.x.put8((tid + 256 * i) / (4 * KB), (tid + 256 * i) % (4 * KB), x[i]);
+            __syncthreads();
+            const uint32_t gx = Staged<32 * KB, NT, kDeltaC>::key_get_place(r, q);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    kt[n] = fragment(p.ktf, key + (b * 2 * KB + ch * KB + c) * NT + n, l);
-                    qt[n] = fragment(p.qtf, key + (b * 2 * KB + ch * KB + c) * NT + n, l);
-                }
+            for (int b = 0; b < 2; ++b) {
+                bf16x8 c1[2][NX], c2[2][NX];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    oS[c][t] = product<NT, NX>(kt, c1[t], oS[c][t]);
-                    dG[c][t] = product<NT, NX>(qt, c1t[t], dG[c][t]);
-                    dG[c][t] = product<NT, NX>(kt, c2[t], dG[c][t]);
+                    float x1[8], x2[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int m = 16 * (2 * th + t) + r, o = 32 * b + perm(q, e);
+                        x1[e] = side ? sh.C1[m][o] : sh.C1[o][m];
+                        if (side) x2[e] = sh.C2[m][o] + sh.C2[o][m];
+                    }
+                    split<NX>(x1, c1[t]);
+                    if (side) split<NX>(x2, c2[t]);
                 }
-                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int c = 0; c < KB; ++c) {
+                    bf16x8 xt[NT];
+                    sh.x.key_get(gx, ch * KB + c, b, xt);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (side) {
+                            oS[c][t] = product<NT, NX>(xt, c1[t], oS[c][t]);
+                            dG[c][t] = product<NT, NX>(xt, c2[t], dG[c][t]);
+                        } else {
+                            dG[c][t] = product<NT, NX>(xt, c1[t], dG[c][t]);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         // a shared key head's gradients are summed over its value heads, always in the same order
@@ -391,7 +353,7 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                const int row = 16 * (2 * th + t) + r, chan = 16 * (ch * KB + c) + 4 * q;
+                const int row = 16 * (2 * th + t) + r, tile = ch * KB + c, chan = 32 * (tile / 2) + 8 * q + 4 * (tile % 2);
                 if (!last || row >= at.n || chan >= p.dk) continue;
                 const long o = ((at.row0 + row) * p.Hk + hk) * p.dk + chan;
 #pragma unroll

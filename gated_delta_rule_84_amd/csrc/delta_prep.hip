@@ -12,29 +12,42 @@ __device__ __forceinline__ int tri_block(bool upper, int i) { return upper ? (i 
 
 template <int NT, int KB, bool BWD>
 __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaParams p) {
-    constexpr int D = 32 * KB, LD = D + 8;
-    __shared__ __attribute__((aligned(16))) uint16_t Kt[NT][kDeltaC][LD];
-    __shared__ __attribute__((aligned(16))) uint16_t Qt[NT][kDeltaC][LD];
+    constexpr int D = 32 * KB;
+    __shared__ __attribute__((aligned(16))) Staged<D, NT, kDeltaC> k;
     __shared__ __attribute__((aligned(16))) float As[kDeltaC][kUtN + 4];
-    __shared__ __attribute__((aligned(16))) float Ps[kDeltaC][kUtN + 4];
     __shared__ float Xs[4][16][16];
     __shared__ ChunkGates gt;
     const int hv = blockIdx.x % p.Hv, slot = blockIdx.x / p.Hv, hk = hv / p.group;
     const Place at = place_of(p, slot);
     if (at.n <= 0) return;  // uniform over the workgroup
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r = l & 15, q = l >> 4;
-    for (int i = tid; i < kDeltaC * D / 8; i += 256) {
-        const int row = i / (D / 8), ch = i % (D / 8) * 8;
-        const bool there = row < at.n && ch < p.dk;
-        bf16x8 t[NT];
-        load8<NT>(p.k, (at.row0 + row) * p.ldk + (long)hk * p.dk + ch, there, t);
+    constexpr int kPieces = kDeltaC * D / 8 / 256;
+    {
+        bf16x8 t[kPieces][NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) *reinterpret_cast<bf16x8 *>(&Kt[n][row][ch]) = t[n];
-        load8<NT>(p.q, (at.row0 + row) * p.ldq + (long)hk * p.dk + ch, there, t);
+        for (int i = 0; i < kPieces; ++i) {
+            const int row = (tid + 256 * i) / (D / 8), m = (tid + 256 * i) % (D / 8);
+            load8<NT>(p.k, (at.row0 + row) * p.ldk + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, t[i]);
+        }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) *reinterpret_cast<bf16x8 *>(&Qt[n][row][ch]) = t[n];
+        for (int i = 0; i < kPieces; ++i) k.put8((tid + 256 * i) / (D / 8), (tid + 256 * i) % (D / 8), t[i]);
     }
     if (w == 0) make_gates(p, at, hv, l, gt);
+    // this wave's places of the scores, a tile of rows (forward t, backward s) and a block of columns, and q of their tokens
+    constexpr int kMine = 2;  // the second only for waves 0 and 1
+    bf16x8 qf[kMine][BWD ? 2 : 1][KB][NT];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int c = w + 4 * m, a = tri_tile(BWD, c), b = tri_block(BWD, c);
+#pragma unroll
+        for (int z = 0; z < (BWD ? 2 : 1); ++z) {
+            const int row = 16 * (BWD ? 2 * b + z : a) + r;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                load8<NT>(p.q, (at.row0 + row) * p.ldq + (long)hk * p.dk + 32 * kb + 8 * q, c < 6 && row < at.n && 32 * kb + 8 * q < p.dk,
+                          qf[m][z][kb]);
+        }
+    }
     __syncthreads();
     const long head = (long)slot * p.Hv + hv;
     if (w == 0) {
@@ -43,75 +56,100 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaParams p) {
         gp[64 + l] = gt.behind[l] * gt.beta[l];
         if (l == 0) gp[128] = gt.whole;
     }
-    // row tile w against the column tiles up to it
-    bf16x8 ak[KB][NT], aq[KB][NT];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            ak[kb][n] = *reinterpret_cast<const bf16x8 *>(&Kt[n][16 * w + r][32 * kb + 8 * q]);
-            aq[kb][n] = *reinterpret_cast<const bf16x8 *>(&Qt[n][16 * w + r][32 * kb + 8 * q]);
-        }
-    for (int j = 0; j < 4; ++j) {
-        f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
-        if (j <= w) {
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                bf16x8 b[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const bf16x8 *>(&Kt[n][16 * j + r][32 * kb + 8 * q]);
-                kk = product<NT, NT>(ak[kb], b, kk);
-                qk = product<NT, NT>(aq[kb], b, qk);
-            }
-        }
-        const int s = 16 * j + r;
+    // rows s, columns t of a pair of tiles: decays times beta (0 above the diagonal)
+    auto decays = [&](int t, int s0) __attribute__((always_inline)) {
+        f32x4 e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = 16 * w + 4 * q + i;
-            const float eb = t >= s ? gt.decay(t, s) * gt.beta[s] : 0.f;
-            As[t][s] = t > s ? eb * kk[i] : 0.f;
-            Ps[t][s] = t >= s ? eb * qk[i] : 0.f;
+            const float x = gt.decay(t, s0 + i) * gt.beta[s0 + i];
+            e[i] = t >= s0 + i ? x : 0.f;
         }
+        return e;
+    };
+    {   // A: columns t of tile w against the rows of every tile up to it
+        bf16x8 kt[KB][NT];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) k.get8(16 * w + r, 4 * kb + q, kt[kb]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+            if (j <= w) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    bf16x8 ks[NT];
+                    k.get8(16 * j + r, 4 * kb + q, ks);
+                    x = product<NT, NT>(ks, kt[kb], x);
+                }
+                x *= decays(16 * w + r, 16 * j + 4 * q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j == w && 4 * q + i == r) x[i] = 0.f;  // the diagonal
+            }
+            *reinterpret_cast<f32x4 *>(&As[16 * w + r][16 * j + 4 * q]) = x;
+        }
+    }
+    // the scores, formed in the orientation in which two tiles are an operand
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int c = w + 4 * m, a = tri_tile(BWD, c), b = tri_block(BWD, c);
+        if (c >= 6) continue;
+        f32x4 x[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int o = 2 * b + z;  // forward the tile of s, backward of t
+            x[z] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            if (BWD ? o < a : o > a) continue;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                bf16x8 ks[NT];
+                k.get8(16 * (BWD ? a : o) + r, 4 * kb + q, ks);
+                x[z] = BWD ? product<NT, NT>(qf[m][BWD ? z : 0][kb], ks, x[z]) : product<NT, NT>(ks, qf[m][0][kb], x[z]);
+            }
+            if constexpr (BWD) {
+                const int s = 16 * a + r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 16 * o + 4 * q + i;
+                    const float e = gt.decay(t, s) * gt.beta[s];
+                    x[z][i] *= t >= s ? e : 0.f;
+                }
+            } else {
+                x[z] *= decays(16 * a + r, 16 * o + 4 * q);
+            }
+        }
+        constexpr int NP = BWD || NT == 3 ? 3 : 2;  // forward, only o reads them
+        bf16x8 t[NP];
+        split<NP>(x[0], x[1], t);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) put_fragment(p.pf, head * kDeltaTri + NP * c + n, l, t[n]);
     }
     __syncthreads();
     ut_transform<kUtN + 4>(As, As, Xs, w, l);
-    for (int i = w; i < 12; i += 4) {
-        const float(*M)[kUtN + 4] = i < 6 ? As : Ps;
-        const int c = i % 6, a = tri_tile(BWD, c), b = tri_block(BWD, c);
+    for (int c = w; c < 6; c += 4) {
+        const int a = tri_tile(BWD, c), b = tri_block(BWD, c);
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int m = 16 * a + r, n = 32 * b + perm(q, e);
-            x[e] = BWD ? M[n][m] : M[m][n];
+            x[e] = BWD ? As[n][m] : As[m][n];
         }
         bf16x8 t[3];
         split<3>(x, t);
-        char *out = i < 6 ? p.tf : p.pf;
 #pragma unroll
-        for (int n = 0; n < 3; ++n) put_fragment(out, head * kDeltaTri + 3 * c + n, l, t[n]);
+        for (int n = 0; n < 3; ++n) put_fragment(p.tf, head * kDeltaTri + 3 * c + n, l, t[n]);
     }
-    if (hv % p.group) return;
-    const long key = (long)slot * p.Hk + hk;
-    for (int i = w; i < 4 * KB * NT; i += 4) {  // k and q by rows: block kb of channels, tile a, term n
-        const int n = i % NT, a = i / NT % 4, kb = i / NT / 4;
-        const uint16_t *kr = &Kt[n][16 * a + r][32 * kb + 4 * q], *qr = &Qt[n][16 * a + r][32 * kb + 4 * q];
-        const u32x2 k0 = *reinterpret_cast<const u32x2 *>(kr), k1 = *reinterpret_cast<const u32x2 *>(kr + 16);
-        const u32x2 q0 = *reinterpret_cast<const u32x2 *>(qr), q1 = *reinterpret_cast<const u32x2 *>(qr + 16);
-        put_fragment(p.kf, key * (4 * KB * NT) + i, l, as_bf16x8((u32x4){k0[0], k0[1], k1[0], k1[1]}));
-        put_fragment(p.qf, key * (4 * KB * NT) + i, l, as_bf16x8((u32x4){q0[0], q0[1], q1[0], q1[1]}));
-    }
-    for (int i = w; i < 4 * KB * NT; i += 4) {  // and by channels: block tb of tokens, tile a of channels
-        const int n = i % NT, a = i / NT % (2 * KB), tb = i / NT / (2 * KB);
-        u32x4 kw, qw;
+    if (p.raw || hv % p.group) return;  // uniform over the workgroup
+    const long key = ((long)slot * p.Hk + hk) * (4 * KB * NT);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const int t0 = 32 * tb + perm(q, e), c = 16 * a + r;
-            kw[e / 2] = Kt[n][t0][c] | (uint32_t)Kt[n][t0 + 1][c] << 16;
-            if (BWD) qw[e / 2] = Qt[n][t0][c] | (uint32_t)Qt[n][t0 + 1][c] << 16;
+    for (int m = 0; m < 2; ++m)  // block kb of channels, tile w of tokens, terms
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            bf16x8 t[NT];
+            const int row = 16 * w + r, ch = 32 * kb + 8 * q;
+            load8<NT>(m ? p.q : p.k, (at.row0 + row) * (m ? p.ldq : p.ldk) + (long)hk * p.dk + ch, row < at.n && ch < p.dk, t);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) put_fragment(m ? p.qf : p.kf, key + (kb * 4 + w) * NT + n, key_place(r, q), t[n]);
         }
-        put_fragment(p.ktf, key * (4 * KB * NT) + i, l, as_bf16x8(kw));
-        if (BWD) put_fragment(p.qtf, key * (4 * KB * NT) + i, l, as_bf16x8(qw));
-    }
 }
 
 template <bool BWD>
@@ -131,10 +169,11 @@ size_t delta_workspace(DeltaParams &p, bool bwd, char *base) {
     };
     const size_t nt = p.io_bf16 ? 1 : 3, key = (size_t)p.nslot * p.Hk * 4 * delta_blocks(p.dk) * nt * 1024;
     const size_t heads = (size_t)p.nslot * p.Hv;
-    p.kf = take(key);
-    p.ktf = take(key);
+    // 16 bytes at a time go only to and from 16-byte places
+    const auto aligned = [](const void *x, int64_t ld) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (ld & 7) == 0; };
+    p.raw = p.io_bf16 && aligned(p.q, p.ldq) && aligned(p.k, p.ldk);
+    p.kf = take(key);  // also where they are not used: the size does not depend on addresses
     p.qf = take(key);
-    p.qtf = bwd ? take(key) : nullptr;
     p.tf = take(heads * kDeltaTri * 1024);
     p.pf = take(heads * kDeltaTri * 1024);
     p.gates = reinterpret_cast<float *>(take(heads * kDeltaGates * 4));
