@@ -20,6 +20,7 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWide = 512;  // most threads of a row
 constexpr int E = 8;  // channels of a lane's piece
 
 typedef uint32_t wu4 __attribute__((ext_vector_type(4), aligned(2)));
@@ -57,24 +58,30 @@ __device__ __forceinline__ void put(void *base, long at, const float (&x)[E]) {
     }
 }
 
-// act(z) and its slope.  The sigmoid's complement is formed by itself: 1 - sigmoid loses digits.
+// act(z) and its slope, from m = e^{-|z|}: the sigmoid and its complement are 1 / (1 + m) and m / (1 + m), neither
+// formed by subtracting the other.  e^x is 2^(x log2 e), by the hardware's 2^t, times 1 + (what rounding t left out) ln 2;
+// the reciprocal is the hardware's with one Newton step.  (The library's e^x and division made the backward pass of
+// 4 x 4,096 x 16 heads of 128 bound by arithmetic, 147 us.)
 __device__ __forceinline__ void activation(int act, float z, float &a, float &slope) {
     if (act == 0) {
         a = z;
         slope = 1.f;
         return;
     }
-    const float m = expf(-fabsf(z)), big = 1.f / (1.f + m), small = m * big;
-    const float s = z >= 0.f ? big : z < 0.f ? small : z, t = z >= 0.f ? small : big;  // NaN stays
+    constexpr float log2e = 1.44269504f, ln2 = 0.69314718f;
+    const float x = -fabsf(z), u = x * log2e;
+    float m = __builtin_amdgcn_exp2f(u);
+    if (u > -150.f) m = fmaf(m, fmaf(x, log2e, -u) * ln2, m);  // else 0, and the difference may be infinite
+    const float d = 1.f + m, r0 = __builtin_amdgcn_rcpf(d), big = fmaf(fmaf(-d, r0, 1.f), r0, r0), small = m * big;
+    const float s = z < 0.f ? small : big, c = z < 0.f ? big : small;
     if (act == 1) {
         a = s;
-        slope = s * t;
+        slope = s * c;
     } else {
-        a = z * s;
-        slope = s * fmaf(z, t, 1.f);
+        const bool far = x == -INFINITY;  // z s and z c of an infinite z
+        a = far ? fmaxf(z, 0.f) : z * s;
+        slope = far ? s : s * fmaf(z, c, 1.f);
     }
-    if (act == 2 && z == -INFINITY) a = 0.f;
-    if (act == 2 && fabsf(z) == INFINITY) slope = s;
 }
 
 __device__ __forceinline__ float inverse(float kappa, float ss, float eps) {
@@ -82,10 +89,12 @@ __device__ __forceinline__ float inverse(float kappa, float ss, float eps) {
     return m > 0.f || m != m ? 1.f / sqrtf(m) : 0.f;
 }
 
+constexpr int kWaves = kWide / 64;
+
 // Sums of N values over a row's lanes: P of a wave (P a power of two), or the whole workgroup with WIDE, through
-// `room`, of which successive sums use different halves.
+// `room`, of which successive sums use different thirds.
 template <bool WIDE, int N>
-__device__ __forceinline__ void row_sum(float (&x)[N], int P, float (*room)[8], int &half) {
+__device__ __forceinline__ void row_sum(float (&x)[N], int P, float (*room)[2 * kWaves], int &third) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
         for (int s = 1; s < (WIDE ? 64 : P); s <<= 1) x[i] += __shfl_xor(x[i], s);
@@ -94,25 +103,48 @@ __device__ __forceinline__ void row_sum(float (&x)[N], int P, float (*room)[8], 
         if (waves > 1) {
             if ((threadIdx.x & 63) == 0)
 #pragma unroll
-                for (int i = 0; i < N; ++i) room[half][(threadIdx.x >> 6) * 2 + i] = x[i];
+                for (int i = 0; i < N; ++i) room[third][(threadIdx.x >> 6) * 2 + i] = x[i];
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 x[i] = 0.f;
-                for (int w = 0; w < waves; ++w) x[i] += room[half][w * 2 + i];
+                for (int w = 0; w < waves; ++w) x[i] += room[third][w * 2 + i];
             }
-            half = half == 2 ? 0 : half + 1;
+            third = third == 2 ? 0 : third + 1;
         }
     }
 }
 
-// NV pieces per lane.  WIDE: a workgroup per row; else P lanes.
+// A lane's pieces of one row, as stored.
+template <bool BF, int NV, bool BWD>
+struct Row {
+    Piece<BF> x[NV], z[NV], r[NV], dy[BWD ? NV : 1], dn[BWD ? NV : 1];
+    __device__ __forceinline__ void load(const NormParams &p, uint32_t row, bool live, int lane, int P) {
+        const uint32_t token = row / (uint32_t)p.H, head = row - token * p.H;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int ch = (v * P + lane) * E;
+            const bool there = live && ch < p.d;
+            const long c = (long)head * p.d + ch;
+            x[v].load(p.x, token * p.ldx + c, there);
+            if (p.z) z[v].load(p.z, token * p.ldz + c, there);
+            if (p.res) r[v].load(p.res, token * p.ldr + c, there);
+            if constexpr (BWD) {
+                dy[v].load(p.dy, (long)row * p.d + ch, there);
+                if (p.next) dn[v].load(p.dn, (long)row * p.d + ch, there);
+            }
+        }
+    }
+};
+
+// NV pieces per lane.  WIDE: a workgroup per row; else P lanes.  A workgroup stays for many rows, with the weights
+// in registers, and asks for a row while it works on the one before.
 template <bool BF, int NV, bool WIDE, bool BWD>
-__global__ void __launch_bounds__(kThreads) block_norm_kernel(NormParams p) {
-    __shared__ float room[3][8];
+__global__ void __launch_bounds__(WIDE ? kWide : kThreads) block_norm_kernel(NormParams p) {
+    __shared__ float room[3][2 * kWaves];
     const int P = WIDE ? blockDim.x : p.lanes, groups = WIDE ? 1 : kThreads / P;
     const int lane = WIDE ? threadIdx.x : threadIdx.x % P, gl = WIDE ? 0 : threadIdx.x / P;
-    int half = 0;
+    int third = 0;
     float w[NV][E], w2[NV][E], sw[BWD ? NV : 1][E], sw2[BWD ? NV : 1][E];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -124,53 +156,44 @@ __global__ void __launch_bounds__(kThreads) block_norm_kernel(NormParams p) {
             if constexpr (BWD) sw[v][e] = sw2[v][e] = 0.f;
         }
     }
-    for (int64_t first = (int64_t)blockIdx.x * groups; first < p.rows; first += (int64_t)gridDim.x * groups) {
-        const int64_t row = first + gl;
-        const bool live = row < p.rows;
-        const int64_t token = live ? row / p.H : 0;
-        const int head = live ? (int)(row - token * p.H) : 0;
-        Piece<BF> X[NV], Z[NV], R[NV], DY[BWD ? NV : 1], DN[BWD ? NV : 1];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int ch = (v * P + lane) * E;
-            const bool there = live && ch < p.d;
-            const long c = (long)head * p.d + ch;
-            X[v].load(p.x, token * p.ldx + c, there);
-            if (p.z) Z[v].load(p.z, token * p.ldz + c, there);
-            if (p.res) R[v].load(p.res, token * p.ldr + c, there);
-            if constexpr (BWD) {
-                DY[v].load(p.dy, row * p.d + ch, there);
-                if (p.next) DN[v].load(p.dn, row * p.d + ch, there);
-            }
-        }
+    const uint32_t rows = (uint32_t)p.rows, step = gridDim.x * groups;
+    constexpr bool kAhead = !BWD || NV == 1;  // two pieces of every tensor twice are more than the registers
+    Row<BF, NV, BWD> next;
+    uint32_t row = blockIdx.x * groups + gl;
+    if constexpr (kAhead) next.load(p, row, row < rows, lane, P);
+    for (uint32_t first = blockIdx.x * groups; first < rows; first += step, row += step) {
+        const bool live = row < rows;
+        if constexpr (!kAhead) next.load(p, row, live, lane, P);
+        const Row<BF, NV, BWD> in = next;
+        if (kAhead && first + step < rows) next.load(p, row + step, row + step < rows, lane, P);
         float ss[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int e = 0; e < E; ++e) ss[0] = fmaf(X[v].get(e), X[v].get(e), ss[0]);
+            for (int e = 0; e < E; ++e) ss[0] = fmaf(in.x[v].get(e), in.x[v].get(e), ss[0]);
         float r = 1.f;
         if (p.norm) {
-            row_sum<WIDE, 1>(ss, P, room, half);
+            row_sum<WIDE, 1>(ss, P, room, third);
             r = inverse(p.kappa, ss[0], p.eps);
         }
-        float h[NV][E], both[2] = {0.f, 0.f};
+        float h[NV][E], a[NV][E], slope[NV][E], both[2] = {0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                float a = 1.f, slope;
-                if (p.z) activation(p.act, Z[v].get(e), a, slope);
-                const float u = X[v].get(e) * r * w[v][e];
-                h[v][e] = p.scale * (a * u);
-                if (p.res) h[v][e] = fmaf(p.res_scale, R[v].get(e), h[v][e]);
+                a[v][e] = 1.f;
+                slope[v][e] = 0.f;
+                if (p.z) activation(p.act, in.z[v].get(e), a[v][e], slope[v][e]);
+                h[v][e] = p.scale * (a[v][e] * (in.x[v].get(e) * r * w[v][e]));
+                if (p.res) h[v][e] = fmaf(p.res_scale, in.r[v].get(e), h[v][e]);
                 both[0] = fmaf(h[v][e], h[v][e], both[0]);
                 if constexpr (BWD) {
-                    if (p.next) both[1] = fmaf(DN[v].get(e) * w2[v][e], h[v][e], both[1]);
+                    if (p.next) both[1] = fmaf(in.dn[v].get(e) * w2[v][e], h[v][e], both[1]);
                 }
             }
         float r2 = 0.f;
         if (p.next) {
-            row_sum<WIDE, 2>(both, P, room, half);
+            row_sum<WIDE, 2>(both, P, room, third);
             r2 = inverse(p.next_kappa, both[0], p.eps);
         }
         if constexpr (!BWD) {
@@ -178,55 +201,48 @@ __global__ void __launch_bounds__(kThreads) block_norm_kernel(NormParams p) {
             for (int v = 0; v < NV; ++v) {
                 const int ch = (v * P + lane) * E;
                 if (!live || ch >= p.d) continue;
-                put<BF>(p.y, row * p.d + ch, h[v]);
+                put<BF>(p.y, (long)row * p.d + ch, h[v]);
                 if (!p.next) continue;
 #pragma unroll
                 for (int e = 0; e < E; ++e) h[v][e] = h[v][e] * r2 * w2[v][e];
-                put<BF>(p.n, row * p.d + ch, h[v]);
+                put<BF>(p.n, (long)row * p.d + ch, h[v]);
             }
         } else {
             const float back = p.next_kappa * r2 * r2 * both[1];  // of r2 h
             float dot[1] = {0.f};
-            float dz[NV][E];
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    float dh = DY[v].get(e);
+                    float dh = in.dy[v].get(e);
                     if (p.next) {
-                        const float dn = DN[v].get(e), hat = r2 * h[v][e];
-                        sw2[v][e] = fmaf(dn, hat, sw2[v][e]);
+                        const float dn = in.dn[v].get(e);
+                        sw2[v][e] = fmaf(dn, r2 * h[v][e], sw2[v][e]);
                         dh += r2 * (dn * w2[v][e] - back * h[v][e]);
                     }
-                    float a = 1.f, slope = 0.f;
-                    if (p.z) activation(p.act, Z[v].get(e), a, slope);
-                    const float hat = X[v].get(e) * r, g = p.scale * dh;
-                    dz[v][e] = g * (hat * w[v][e]) * slope;
+                    const float hat = in.x[v].get(e) * r, g = p.scale * dh, ga = g * a[v][e];
+                    slope[v][e] *= g * (hat * w[v][e]);
                     h[v][e] = dh;
-                    const float ga = g * a;
                     sw[v][e] = fmaf(ga, hat, sw[v][e]);
-                    dot[0] = fmaf(ga * w[v][e], hat, dot[0]);
+                    a[v][e] = ga * w[v][e];
+                    dot[0] = fmaf(a[v][e], hat, dot[0]);
                 }
-            if (p.norm) row_sum<WIDE, 1>(dot, P, room, half);
-            const float k = p.norm ? p.kappa * dot[0] : 0.f;
+            if (p.norm) row_sum<WIDE, 1>(dot, P, room, third);
+            const float k = p.norm ? p.kappa * dot[0] * r : 0.f;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int ch = (v * P + lane) * E;
                 if (!live || ch >= p.d) continue;
-                float o[E];
+                const long o = (long)row * p.d + ch;
                 if (p.res) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = p.res_scale * h[v][e];
-                    put<BF>(p.dres, row * p.d + ch, o);
+                    for (int e = 0; e < E; ++e) h[v][e] *= p.res_scale;
+                    put<BF>(p.dres, o, h[v]);
                 }
-                if (p.z) put<BF>(p.dz, row * p.d + ch, dz[v]);
+                if (p.z) put<BF>(p.dz, o, slope[v]);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float a = 1.f, slope;
-                    if (p.z) activation(p.act, Z[v].get(e), a, slope);
-                    o[e] = r * (p.scale * h[v][e] * a * w[v][e] - k * (X[v].get(e) * r));
-                }
-                put<BF>(p.dx, row * p.d + ch, o);
+                for (int e = 0; e < E; ++e) a[v][e] = r * (a[v][e] - k * in.x[v].get(e));
+                put<BF>(p.dx, o, a[v]);
             }
         }
     }
@@ -290,12 +306,12 @@ template <bool BF, bool BWD>
 const void *pick(int nv, bool wide) {
     if (!wide) return reinterpret_cast<const void *>(&block_norm_kernel<BF, 1, false, BWD>);
     return nv == 1   ? reinterpret_cast<const void *>(&block_norm_kernel<BF, 1, true, BWD>)
-           : nv == 2 ? reinterpret_cast<const void *>(&block_norm_kernel<BF, 2, true, BWD>)
-                     : reinterpret_cast<const void *>(&block_norm_kernel<BF, 4, true, BWD>);
+                     : reinterpret_cast<const void *>(&block_norm_kernel<BF, 2, true, BWD>);
 }
 
-constexpr int kMaxBlocks = 1024;  // of a backward pass: its workgroups keep the weights' sums
-constexpr int64_t kMaxGrid = (1 << 24) - 1;
+// Workgroups: what the chip holds at once, so that each stays for many rows.  Of 256 threads 8 fit a compute unit in
+// the forward pass and 4 in the backward pass, which has twice the registers.
+constexpr int kBlocks = 2048, kBlocksBwd = 1024;
 
 struct Plan {
     bool wide;
@@ -306,12 +322,13 @@ Plan plan(NormParams &p, bool bwd) {
     Plan r;
     const int pieces = p.d / E;
     r.wide = pieces > 64;
-    r.nv = r.wide ? (pieces <= kThreads ? 1 : pieces <= 2 * kThreads ? 2 : 4) : 1;
+    r.nv = pieces <= kWide ? 1 : 2;
     r.threads = r.wide ? ((pieces + r.nv - 1) / r.nv + 63) / 64 * 64 : kThreads;
     p.lanes = 1;
     while (!r.wide && p.lanes < pieces) p.lanes <<= 1;
     const int64_t groups = r.wide ? 1 : kThreads / p.lanes, blocks = (p.rows + groups - 1) / groups;
-    p.blocks = (int)std::min<int64_t>(blocks, bwd ? kMaxBlocks : kMaxGrid);
+    const int most = (bwd ? kBlocksBwd : kBlocks) * kThreads / r.threads;
+    p.blocks = (int)std::min<int64_t>(blocks, most);
     return r;
 }
 

@@ -14,6 +14,11 @@ __device__ const u32x4 kNothing = {0, 0, 0, 0};  // what is copied for rows and 
 // LDS traffic waited for, global memory not.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// 4 bytes per lane, global -> LDS; lane l writes dst + 4 l.
+__device__ __forceinline__ void dma4(const void *src, void *dst) {
+    __builtin_amdgcn_global_load_lds((gbl_void_t)src, (lds_void_t)dst, 4, 0, 0);
+}
+
 __device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
 template <int I, int N, class F>
@@ -70,7 +75,7 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
     typedef Plan<NT, KB, BWD> P;
     __shared__ __attribute__((aligned(16))) char sets[P::sets][P::size * 1024];
-    __shared__ __attribute__((aligned(16))) float gring[2][kDeltaGates];
+    __shared__ __attribute__((aligned(16))) float gring[2][kDeltaGates], nowhere[64];
     const int head = blockIdx.x % heads8;
     if (head >= p.nseq * p.Hv) return;  // uniform over the workgroup
     const int seq = head / p.Hv, hv = head % p.Hv, hk = hv / p.group;
@@ -115,17 +120,42 @@ __global__ void __launch_bounds__(64 * (NW + kLoaders)) delta_chain_kernel(Delta
                 for (int f = 0; f < 6 * P::nP; f += kLoaders) dma16(s + f * 1024, to + (P::atP + half + f) * 1024);
             }
         };
+        // Brings chunk c's operands to the XCD's cache: 4 bytes of every 128-byte line, to nowhere.  The workgroups of a head
+        // share the work.
+        const int parts = gridDim.x / heads8, part = blockIdx.x / heads8;
+        auto touch = [&](int c) __attribute__((always_inline)) {
+            const int pos = BWD ? nc - 1 - c : c, n = len - pos * kDeltaC;
+            const long slot = slot0 + pos, kh = slot * p.Hk + hk, vh = slot * p.Hv + hv;
+            auto lines = [&](const char *from, int bytes) __attribute__((always_inline)) {
+                for (int i = half * 8192; i < bytes; i += kLoaders * 8192) dma4(from + min(i + l * 128, bytes - 128), nowhere);
+            };
+            auto keys = [&](const void *x, int64_t ld, const char *made) __attribute__((always_inline)) {
+                if (NT == 1 && p.raw) {
+                    const int row = min(l, n - 1), ch = min(64 * half, p.dk - 8);  // 128 bytes of each row a wave
+                    dma4(static_cast<const uint16_t *>(x) + (row0 + (long)pos * kDeltaC + row) * ld + (long)hk * p.dk + ch, nowhere);
+                } else {
+                    lines(made + kh * P::key * 1024, P::key * 1024);
+                }
+            };
+            if (part == 0) keys(p.k, p.ldk, p.kf);
+            if (part == min(1, parts - 1)) keys(p.q, p.ldq, p.qf);
+            if (part == min(2, parts - 1)) lines(p.tf + vh * kDeltaTri * 1024, kDeltaTri * 1024);
+            if (part == min(3, parts - 1)) lines(p.pf + vh * kDeltaTri * 1024, 6 * P::nP * 1024);
+        };
         if (nc > 0) copy(0, true, true);
+        if (nc > 1) touch(1);
         for (int c = 0; c < nc; ++c) {
             wait_copies();  // this chunk's are there
             lds_barrier();  // and the chunk before is done
             if constexpr (P::sets == 2) {
                 if (c + 1 < nc) copy(c + 1, true, true);
+                if (c + 2 < nc) touch(c + 2);
             } else {
                 lds_barrier();  // q, T and Q are no longer read
                 if (c + 1 < nc) copy(c + 1, false, true);
                 lds_barrier();  // nor is k
                 if (c + 1 < nc) copy(c + 1, true, false);
+                if (c + 2 < nc) touch(c + 2);
             }
         }
         return;
