@@ -242,6 +242,10 @@ __device__ __forceinline__ void load8(const void *base, long at, bool there, bf1
     }
 }
 
+// A barrier for what goes through shared memory: global memory is not waited for (__syncthreads waits for loads that are
+// asked for ahead).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // A range-checked buffer: loads from outside give 0, stores to outside are dropped.  A lane that is
 // to be left out adds kNowhere to its offset.
 typedef __amdgpu_buffer_rsrc_t Buf;
@@ -305,6 +309,15 @@ struct Staged {
             for (int i = 0; i < 4; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
         }
     }
+    // a lane's part of a column from row 32 b on in the order of perm, at put_place(j, q)
+    __device__ __forceinline__ void column(uint32_t at, int b, bf16x8 (&t)[NT]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const u32x2 x = *(lds_u32x2)(base() + (at ^ (uint32_t)(2 * b) << 5) + n * kTerm);
+            const u32x2 y = *(lds_u32x2)(base() + (at ^ (uint32_t)(2 * b + 1) << 5) + n * kTerm);
+            t[n] = as_bf16x8((u32x4){x[0], x[1], y[0], y[1]});
+        }
+    }
     // rows 8 m .. 8 m + 7 of column j, put or got whole
     __device__ __forceinline__ void put8(int j, int m, const bf16x8 (&t)[NT]) {
 #pragma unroll
@@ -340,17 +353,18 @@ struct Staged {
     }
 };
 
-// The gates of a chunk, in shared memory.  P is summed in 64 bits: behind a strong decay the
-// difference of two fp32 sums would have lost the weak ones.  A gate of -inf cuts: it adds nothing to P,
-// and decays across it are 0.
+// The gates of a chunk, in shared memory.  P, here in units of ln 2, is summed in 64 bits: behind a strong decay the
+// difference of two fp32 sums would have lost the weak ones.  A gate of -inf cuts: it adds nothing to P, and decays across
+// it are 0.  The difference is rounded once, so the hardware's 2^x is as exact as an fp32 e^x.
 struct ChunkGates {
     double P[kDeltaC];
     int cut[kDeltaC];
     float beta[kDeltaC], front[kDeltaC], behind[kDeltaC];
     float whole;
 
+    static __device__ __forceinline__ float power(float x) { return __builtin_amdgcn_exp2f(x); }
     __device__ __forceinline__ float decay(int t, int s) const {
-        const float e = expf((float)(P[t] - P[s]));
+        const float e = power((float)(P[t] - P[s]));
         return cut[t] == cut[s] ? e : 0.f;
     }
 };
@@ -361,7 +375,7 @@ __device__ __forceinline__ void make_gates(const DeltaParams &p, const Place &at
     const long row = at.row0 + lane;
     const float g = there ? ld_elem(p.g, row * p.ldg + hv, p.gate_bf16) : 0.f;
     const bool cuts = g == -INFINITY;
-    double P = cuts ? 0.0 : (double)g;
+    double P = cuts ? 0.0 : (double)g * 1.4426950408889634;
     int cut = cuts;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -377,9 +391,9 @@ __device__ __forceinline__ void make_gates(const DeltaParams &p, const Place &at
     c.P[lane] = P;
     c.cut[lane] = cut;
     c.beta[lane] = there ? ld_elem(p.b, row * p.ldb + hv, p.gate_bf16) : 0.f;
-    c.front[lane] = cut == 0 ? expf((float)P) : 0.f;
-    c.behind[lane] = cut == lc ? expf((float)(last - P)) : 0.f;
-    if (lane == 63) c.whole = lc == 0 ? expf((float)P) : 0.f;
+    c.front[lane] = cut == 0 ? c.power((float)P) : 0.f;
+    c.behind[lane] = cut == lc ? c.power((float)(last - P)) : 0.f;
+    if (lane == 63) c.whole = lc == 0 ? c.power((float)P) : 0.f;
 }
 
 }  // namespace

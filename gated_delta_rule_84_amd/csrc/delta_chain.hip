@@ -11,9 +11,6 @@ constexpr int kGroup = 12;    // most fragments that a wave reads ahead
 
 __device__ const u32x4 kNothing = {0, 0, 0, 0};  // what is copied for rows and channels that are not there
 
-// LDS traffic waited for, global memory not.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 // 4 bytes per lane, global -> LDS; lane l writes dst + 4 l.
 __device__ __forceinline__ void dma4(const void *src, void *dst) {
     __builtin_amdgcn_global_load_lds((gbl_void_t)src, (lds_void_t)dst, 4, 0, 0);

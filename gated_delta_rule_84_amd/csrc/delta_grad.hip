@@ -19,28 +19,32 @@
 namespace gdr {
 namespace {
 
-constexpr int kLC = kDeltaC + 4;
-
 template <int NT, int KB>
 struct GradShared {
     union {
         struct {
             Staged<32 * KB, 3, 32> S, G;
             Staged<64, 3, 32> D, Y;
-        };
+        } block[2];  // of 32 columns: one is read while the next is written
         struct {
-            float C1[kDeltaC][kLC], C2[kDeltaC][kLC];  // [t][s]
-            Staged<32 * KB, NT, kDeltaC> x;            // k or q
+            Staged<kDeltaC, NT == 1 ? 2 : 3, kDeltaC> C1, C2;  // rows s, columns t
+            Staged<32 * KB, NT, kDeltaC> x[NT == 1 ? 2 : 1];     // q and k, with fp32 one after the other
         };
     };
-    float col_m[2][kDeltaC], col_pair[2][kDeltaC], row_m[2][kDeltaC], read[2][kDeltaC], write[2][kDeltaC], dot[4];
+    float col_m[2][kDeltaC], col_pair[2][kDeltaC], row_m[4][kDeltaC], read[4][kDeltaC], write[4][kDeltaC], dot[8];
     ChunkGates gt;
 };
 
+template <int N>
+__device__ __forceinline__ float turned(float x) {  // by N lanes within 16
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, true));
+}
+
 __device__ __forceinline__ float row_lanes(float x) {  // over the 16 lanes of a quarter
-#pragma unroll
-    for (int s = 1; s < 16; s <<= 1) x += __shfl_xor(x, s);
-    return x;
+    x += turned<8>(x);
+    x += turned<4>(x);
+    x += turned<2>(x);
+    return x + turned<1>(x);
 }
 
 __device__ __forceinline__ float quarters(float x) {  // over the four quarters
@@ -48,217 +52,233 @@ __device__ __forceinline__ float quarters(float x) {  // over the four quarters
     return x + __shfl_xor(x, 32);
 }
 
-// Four waves: wave (th, ch) has token tiles 2 th and 2 th + 1 and half ch of the channels.
+// Eight waves: wave (th, cq) has token tiles 2 th and 2 th + 1 and quarter cq of the channels.
 template <int NT, int KB>
-__global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
+    constexpr int CT = KB / 2;           // channel tiles of a wave
     __shared__ __attribute__((aligned(16))) GradShared<NT, KB> sh;
     const int hk = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
     const Place at = place_of(p, slot);
     if (at.n <= 0) return;  // uniform over the workgroup
-    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 1, ch = w & 1;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 2, cq = w & 3;
     const int na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv), jblocks = (nj + 1) / 2;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    // all of k or q as it lies, 8 channels a turn
+    auto bring = [&](const void *x, int64_t ld, auto &to) __attribute__((always_inline)) {
+        constexpr int kPieces = kDeltaC * 4 * KB / 512;
+        bf16x8 t[kPieces][NT];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int row = (tid + 512 * i) / (4 * KB), m = (tid + 512 * i) % (4 * KB);
+            load8<NT>(x, (at.row0 + row) * ld + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, t[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) to.put8((tid + 512 * i) / (4 * KB), (tid + 512 * i) % (4 * KB), t[i]);
+    };
 #pragma unroll 1
     for (int h = 0; h < p.group; ++h) {
         int l = tid & 63;
         asm volatile("" : "+v"(l));  // addresses are formed for each head: kept over the heads they would take the registers
         const int r = l & 15, q = l >> 4;
         const int hv = hk * p.group + h;
-        const long vh = (long)slot * p.Hv + hv, base = vh * nj * (na + 4) * 256;
-        const float *ST = p.ckpt + base, *GT = p.back + base;
-        if (h) __syncthreads();
+        const long vh = (long)slot * p.Hv + hv;
+        // wave w brings column tile w & 1 of a block, a quarter of its row tiles: of S and G, and of D and y
+        const float *from = p.ckpt + vh * nj * (na + 4) * 256, *back = p.back + vh * nj * (na + 4) * 256;
+        const long dout = (long)hv * p.dv;
+        f32x4 a[CT], b[CT], d, y;
+        bf16x8 fo[2][NT], fn[2][NT];
+        auto ask = [&](int jb) __attribute__((always_inline)) {
+            const int jt = 2 * jb + (w & 1);
+            const long tiles = (long)min(jt, nj - 1) * (na + 4) * 256;
+            const int there = jt < nj ? 1024 : 0;  // bytes of a tile
+            const Buf s = buffer(from + tiles, there * na), g = buffer(back + tiles, there * na);
+            const Buf sd = buffer(from + tiles + na * 256, there * 4), gy = buffer(back + tiles + na * 256, there * 4);
+            auto tile = [&](Buf x, int n) __attribute__((always_inline)) {
+                return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(x, n * 1024 + l * 16, 0, 0));
+            };
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                a[c] = tile(s, (w >> 1) * CT + c);
+                b[c] = tile(g, (w >> 1) * CT + c);
+            }
+            d = tile(sd, w >> 1);
+            y = tile(gy, w >> 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {  // do, by rows: its columns in the operands' order
+                const int row = 16 * (2 * th + t) + r, j = 32 * jb + 4 * q;
+                load44<NT>(p.dout, (at.row0 + row) * p.Hv * p.dv + dout + j, row < at.n && j < p.dv, row < at.n && j + 16 < p.dv, fn[t]);
+            }
+        };
+        float dot = 0.f;
+        auto put = [&](int to) __attribute__((always_inline)) {
+            // formed again for each block: kept for all tiles they would take the registers of the sums
+            uint32_t pS = Staged<32 * KB, 3, 32>::put_place(16 * (w & 1) + r, q), pD = Staged<64, 3, 32>::put_place(16 * (w & 1) + r, q);
+            asm volatile("" : "+v"(pS), "+v"(pD));
+            auto &o = sh.block[to];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                o.S.put(pS, (w >> 1) * CT + c, a[c]);
+                o.G.put(pS, (w >> 1) * CT + c, b[c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dot = fmaf(a[c][i], b[c][i], dot);
+            }
+            o.D.put(pD, w >> 1, d);
+            o.Y.put(pD, w >> 1, y);
+        };
+        ask(0);
         if (w == 0) make_gates(p, at, hv, l, sh.gt);
-        f32x4 oS[KB][2], yS[KB][2], dG[KB][2], n1[2][2], n2[2][2];  // [channel tile][token tile], [s tile][token tile]
+        f32x4 oS[CT][2], yS[CT][2], dG[CT][2], n1[2], n2[2];  // [channel tile][token tile]; rows s of tile cq, [token tile]
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int c = 0; c < KB; ++c) oS[c][t] = yS[c][t] = dG[c][t] = zero;
-            n1[0][t] = n1[1][t] = n2[0][t] = n2[1][t] = zero;
+            for (int c = 0; c < CT; ++c) oS[c][t] = yS[c][t] = dG[c][t] = zero;
+            n1[t] = n2[t] = zero;
         }
-        float dot = 0.f;
-#pragma unroll 1
+        put(0);
         for (int jb = 0; jb < jblocks; ++jb) {
-            // formed again for each block: kept for all tiles they would take the registers of the sums
-            uint32_t pS = Staged<32 * KB, 3, 32>::put_place(16 * (w & 1) + r, q), gS = Staged<32 * KB, 3, 32>::get_place(r, q);
-            uint32_t pD = Staged<64, 3, 32>::put_place(16 * (w & 1) + r, q), gD = Staged<64, 3, 32>::get_place(r, q);
-            asm volatile("" : "+v"(pS), "+v"(gS), "+v"(pD), "+v"(gD));
-            // wave w brings column tile w & 1 of the block, half of its row tiles
-            {
-                const int jt = 2 * jb + (w & 1);
-                const bool there = jt < nj;
-                const float *s = ST + (long)jt * (na + 4) * 256 + l * 4, *g = GT + (long)jt * (na + 4) * 256 + l * 4;
-                f32x4 a[KB], b[KB], d[2], y[2];
+            uint32_t gS = Staged<32 * KB, 3, 32>::get_place(r, q), gD = Staged<64, 3, 32>::get_place(r, q);
+            asm volatile("" : "+v"(gS), "+v"(gD));
+            auto &in = sh.block[jb & 1];
 #pragma unroll
-                for (int c = 0; c < KB; ++c) {
-                    const int tile = (w >> 1) * KB + c;
-                    a[c] = b[c] = zero;
-                    if (there && tile < na) {
-                        a[c] = *reinterpret_cast<const f32x4 *>(s + tile * 256);
-                        b[c] = *reinterpret_cast<const f32x4 *>(g + tile * 256);
-                    }
-                }
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int tile = na + (w >> 1) * 2 + c;
-                    d[c] = y[c] = zero;
-                    if (there) {
-                        d[c] = *reinterpret_cast<const f32x4 *>(s + tile * 256);
-                        y[c] = *reinterpret_cast<const f32x4 *>(g + tile * 256);
-                    }
-                }
-                __syncthreads();  // the block before is no longer read
-#pragma unroll
-                for (int c = 0; c < KB; ++c) {
-                    sh.S.put(pS, (w >> 1) * KB + c, a[c]);
-                    sh.G.put(pS, (w >> 1) * KB + c, b[c]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dot = fmaf(a[c][i], b[c][i], dot);
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    sh.D.put(pD, (w >> 1) * 2 + c, d[c]);
-                    sh.Y.put(pD, (w >> 1) * 2 + c, y[c]);
-                }
-            }
-            bf16x8 fo[2][NT], fy[2][3], fd[2][3];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {  // do, by rows: its columns in the operands' order
-                const int row = 16 * (2 * th + t) + r;
-                const long o = ((at.row0 + row) * p.Hv + hv) * p.dv;
-                const int j = 32 * jb + 4 * q;
-                load44<NT>(p.dout, o + j, row < at.n && j < p.dv, row < at.n && j + 16 < p.dv, fo[t]);
-            }
-            __syncthreads();
+                for (int n = 0; n < NT; ++n) fo[t][n] = fn[t][n];
+            ask(jb + 1);      // zeros behind the last block
+            lds_barrier();    // this block is written, and the one before no longer read
+            bf16x8 fy[2][3], fd[2][3];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                sh.Y.get(gD, 2 * th + t, fy[t]);
-                sh.D.get(gD, 2 * th + t, fd[t]);
+                in.Y.get(gD, 2 * th + t, fy[t]);
+                in.D.get(gD, 2 * th + t, fd[t]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            bf16x8 ds[3];
+            in.D.get(gD, cq, ds);
+            // for tiles above the diagonal too (two thirds of them are not), which are not used: no branch among the products
+            products<3, NT, 2>([&](int, int i) { return ds[i]; }, [&](int k, int j) { return fo[k][j]; }, [&](int k) -> f32x4 & { return n1[k]; });
+            products<3, 3, 2>([&](int, int i) { return ds[i]; }, [&](int k, int j) { return fy[k][j]; }, [&](int k) -> f32x4 & { return n2[k]; });
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int sa = 2 * m + ch;  // s tiles of this wave
-                if (sa > 2 * th + 1) continue;
-                bf16x8 d[3];
-                sh.D.get(gD, sa, d);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (sa > 2 * th + t) continue;
-                    n1[m][t] = product<3, NT>(d, fo[t], n1[m][t]);
-                    n2[m][t] = product<3, 3>(d, fy[t], n2[m][t]);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < KB; ++c) {
+            for (int c = 0; c < CT; ++c) {
                 bf16x8 s[3], g[3];
-                sh.S.get(gS, ch * KB + c, s);
-                sh.G.get(gS, ch * KB + c, g);
+                in.S.get(gS, cq * CT + c, s);
+                in.G.get(gS, cq * CT + c, g);
                 products<3, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fo[k][j]; },
                                    [&](int k) -> f32x4 & { return oS[c][k]; });
                 products<3, 3, 4>([&](int k, int i) { return k < 2 ? s[i] : g[i]; }, [&](int k, int j) { return k < 2 ? fy[k][j] : fd[k - 2][j]; },
                                   [&](int k) -> f32x4 & { return k < 2 ? yS[c][k] : dG[c][k - 2]; });
-                __builtin_amdgcn_sched_barrier(0);  // no operands of later tiles in registers yet
+            }
+            put(jb + 1 & 1);  // among the products
+#pragma unroll
+            for (int i = 0; i < 78; ++i) {  // a matrix instruction takes the time of four others
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
             }
         }
+        __syncthreads();
+        if constexpr (NT == 1) {
+            bring(p.q, p.ldq, sh.x[0]);
+            bring(p.k, p.ldk, sh.x[1]);
+        }
         // tile t of the rows of k or q, block kb of channels
-        auto rows = [&](const void *x, int64_t ld, int t, int kb, bf16x8 (&to)[NT]) __attribute__((always_inline)) {
-            const int row = 16 * t + r, c = 32 * kb + 8 * q;
-            load8<NT>(x, (at.row0 + row) * ld + (long)hk * p.dk + c, row < at.n && c < p.dk, to);
+        auto rows = [&](bool key, int t, int kb, bf16x8 (&to)[NT]) __attribute__((always_inline)) {
+            if constexpr (NT == 1) {
+                sh.x[key].get8(16 * t + r, 4 * kb + q, to);
+            } else {
+                const int row = 16 * t + r, c = 32 * kb + 8 * q;
+                load8<NT>(key ? p.k : p.q, (at.row0 + row) * (key ? p.ldk : p.ldq) + (long)hk * p.dk + c, row < at.n && c < p.dk, to);
+            }
         };
         __syncthreads();
-        // pairs of tokens: rows s, columns t
-        float cm[2][4] = {}, cp[2][4] = {}, rm[2] = {0.f, 0.f};
+        // pairs of tokens: rows s of tile cq, columns t
+        float cm[4] = {}, cp[4] = {};
+        const int s0 = 16 * cq + 4 * q;
+        const f32x4 betas = *reinterpret_cast<const f32x4 *>(&sh.gt.beta[s0]);
+        double Ps[4];
+        int cuts[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Ps[i] = sh.gt.P[s0 + i];
+            cuts[i] = sh.gt.cut[s0 + i];
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int ta = 2 * th + t, tt = 16 * ta + r;
+            f32x4 c1 = zero, c2 = zero;
+            float rm = 0.f;
+            if (cq <= ta) {
+                f32x4 qk = zero, kk = zero;
+                const double Pt = sh.gt.P[tt];
+                const int cut = sh.gt.cut[tt];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int sa = 2 * m + ch;
-                f32x4 c1 = zero, c2 = zero;
-                __builtin_amdgcn_sched_barrier(0);
-                if (sa <= ta) {
-                    f32x4 qk = zero, kk = zero;
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        bf16x8 s[NT], tq[NT], tk[NT];
-                        rows(p.k, p.ldk, sa, kb, s);
-                        rows(p.q, p.ldq, ta, kb, tq);
-                        rows(p.k, p.ldk, ta, kb, tk);
-                        qk = product<NT, NT>(s, tq, qk);
-                        kk = product<NT, NT>(s, tk, kk);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int s = 16 * sa + 4 * q + i;
-                        const float e = tt >= s ? sh.gt.decay(tt, s) : 0.f, beta = sh.gt.beta[s];
-                        const float a1 = tt >= s ? n1[m][t][i] : 0.f, a2 = tt > s ? n2[m][t][i] : 0.f;
-                        c1[i] = e * beta * a1;
-                        c2[i] = -e * beta * a2;
-                        const float pair = tt >= s ? e * (a1 * qk[i] - a2 * kk[i]) : 0.f;
-                        cp[m][i] += pair;
-                        if (tt > s) {  // a token's own pair does not pass its gate
-                            rm[t] += pair * beta;
-                            cm[m][i] += pair * beta;
-                        }
-                    }
+                for (int kb = 0; kb < KB; ++kb) {
+                    bf16x8 s[NT], tq[NT], tk[NT];
+                    rows(true, cq, kb, s);
+                    rows(false, ta, kb, tq);
+                    rows(true, ta, kb, tk);
+                    products<NT, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return k ? tk[j] : tq[j]; },
+                                        [&](int k) -> f32x4 & { return k ? kk : qk; });
                 }
-                *reinterpret_cast<f32x4 *>(&sh.C1[tt][16 * sa + 4 * q]) = c1;
-                *reinterpret_cast<f32x4 *>(&sh.C2[tt][16 * sa + 4 * q]) = c2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int s = s0 + i;
+                    const float x = sh.gt.power((float)(Pt - Ps[i])), e = tt >= s && cut == cuts[i] ? x : 0.f;
+                    const float a1 = tt >= s ? n1[t][i] : 0.f, a2 = tt > s ? n2[t][i] : 0.f;
+                    c1[i] = e * betas[i] * a1;
+                    c2[i] = -e * betas[i] * a2;
+                    const float pair = tt >= s ? e * (a1 * qk[i] - a2 * kk[i]) : 0.f;
+                    cp[i] += pair;
+                    const float through = tt > s ? pair * betas[i] : 0.f;  // a token's own pair does not pass its gate
+                    rm += through;
+                    cm[i] += through;
+                }
             }
-            rm[t] = quarters(rm[t]);
-            if (q == 0) sh.row_m[ch][tt] = rm[t];
+            sh.C1.put(sh.C1.put_place(tt, q), cq, c1);
+            sh.C2.put(sh.C2.put_place(tt, q), cq, c2);
+            rm = quarters(rm);
+            if (q == 0) sh.row_m[cq][tt] = rm;
         }
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = row_lanes(cm[m][i]), z = row_lanes(cp[m][i]);
-                if (r == 0) {
-                    sh.col_m[th][16 * (2 * m + ch) + 4 * q + i] = x;
-                    sh.col_pair[th][16 * (2 * m + ch) + 4 * q + i] = z;
-                }
+        for (int i = 0; i < 4; ++i) {
+            const float x = row_lanes(cm[i]), z = row_lanes(cp[i]);
+            if (r == 0) {
+                sh.col_m[th][s0 + i] = x;
+                sh.col_pair[th][s0 + i] = z;
             }
+        }
         // what the states give, and its dot products with q and k
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int ta = 2 * th + t, tt = 16 * ta + r;
             const float front = sh.gt.front[tt], behind = sh.gt.behind[tt], beta = sh.gt.beta[tt];
             float read = 0.f, write = 0.f;
+            bf16x8 tq[NT], tk[NT];
+            rows(false, ta, cq * CT / 2, tq);
+            rows(true, ta, cq * CT / 2, tk);
 #pragma unroll
-            for (int c = 0; c < KB; c += 2) {
-                const int kb = (ch * KB + c) / 2;
-                __builtin_amdgcn_sched_barrier(0);
-                float qv[8], kv[8];
+            for (int c = 0; c < CT; ++c) {
+                const int odd = (cq * CT + c) & 1;  // the tile has channels 4 odd .. 4 odd + 3 of the lane's eight
 #pragma unroll
-                for (int e = 0; e < 8; ++e) qv[e] = kv[e] = 0.f;
-                bf16x8 tq[NT], tk[NT];
-                rows(p.q, p.ldq, ta, kb, tq);
-                rows(p.k, p.ldk, ta, kb, tk);
+                for (int i = 0; i < 4; ++i) {
+                    float qv = 0.f, kv = 0.f;
 #pragma unroll
-                for (int n = NT - 1; n >= 0; --n) {
-                    const u32x4 a = __builtin_bit_cast(u32x4, tq[n]), b = __builtin_bit_cast(u32x4, tk[n]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        qv[e] += __uint_as_float(e & 1 ? a[e / 2] & 0xffff0000u : a[e / 2] << 16);
-                        kv[e] += __uint_as_float(e & 1 ? b[e / 2] & 0xffff0000u : b[e / 2] << 16);
+                    for (int n = NT - 1; n >= 0; --n) {
+                        const u32x4 u = __builtin_bit_cast(u32x4, tq[n]), v = __builtin_bit_cast(u32x4, tk[n]);
+                        const uint32_t x = odd ? u[2 + i / 2] : u[i / 2], z = odd ? v[2 + i / 2] : v[i / 2];
+                        qv += __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+                        kv += __uint_as_float(i & 1 ? z & 0xffff0000u : z << 16);
                     }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int cc = c + e / 4, i = e % 4;
-                    const float fo = front * oS[cc][t][i], fy = front * yS[cc][t][i], bg = behind * dG[cc][t][i];
-                    oS[cc][t][i] = fo;
-                    dG[cc][t][i] = fmaf(beta, bg, -fy);
-                    read += qv[e] * fo - kv[e] * fy;
-                    write = fmaf(kv[e], bg, write);
+                    const float fo_ = front * oS[c][t][i], fy_ = front * yS[c][t][i], bg = behind * dG[c][t][i];
+                    oS[c][t][i] = fo_;
+                    dG[c][t][i] = fmaf(beta, bg, -fy_);
+                    read += qv * fo_ - kv * fy_;
+                    write = fmaf(kv, bg, write);
                 }
             }
             read = quarters(read);
             write = quarters(write);
             if (q == 0) {
-                sh.read[ch][tt] = read;
-                sh.write[ch][tt] = write;
+                sh.read[cq][tt] = read;
+                sh.write[cq][tt] = write;
             }
         }
 #pragma unroll
@@ -266,8 +286,13 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
         if (l == 0) sh.dot[w] = dot;
         __syncthreads();
         if (w == 0) {
-            float db = sh.write[0][l] + sh.write[1][l], up = db * sh.gt.beta[l];
-            float down = sh.read[0][l] + sh.read[1][l] + sh.row_m[0][l] + sh.row_m[1][l];
+            float db = 0.f, down = 0.f, dots = 0.f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                db += sh.write[m][l];
+                down += sh.read[m][l] + sh.row_m[m][l];
+            }
+            float up = db * sh.gt.beta[l];
             const float mine = up;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
@@ -275,12 +300,14 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                 down -= sh.col_m[m][l];
             }
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {  // sums over this token and the later ones, and over the earlier ones
-                const float x = __shfl_down(down, d), y = __shfl_up(up, d);
-                if (l + d < 64) down += x;
-                if (l >= d) up += y;
+            for (int s = 1; s < 64; s <<= 1) {  // sums over this token and the later ones, and over the earlier ones
+                const float x = __shfl_down(down, s), z = __shfl_up(up, s);
+                if (l + s < 64) down += x;
+                if (l >= s) up += z;
             }
-            const float kept = sh.gt.whole * (sh.dot[0] + sh.dot[1] + sh.dot[2] + sh.dot[3]);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) dots += sh.dot[m];
+            const float kept = sh.gt.whole * dots;
             const bool cuts = l ? sh.gt.cut[l] != sh.gt.cut[l - 1] : sh.gt.cut[0] != 0;
             if (l < at.n) {
                 const long o = (at.row0 + l) * p.Hv + hv;
@@ -291,58 +318,51 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
         // + C1^T q to dk, + C1 k to dq and (C2 + C2^T) k to dk
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            if (side) __syncthreads();
-            constexpr int kPieces = kDeltaC * 4 * KB / 256;
-            bf16x8 x[kPieces][NT];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int row = (tid + 256 * i) / (4 * KB), m = (tid + 256 * i) % (4 * KB);
-                load8<NT>(side ? p.k : p.q, (at.row0 + row) * (side ? p.ldk : p.ldq) + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, x[i]);
+            if constexpr (NT == 3) {
+                if (side) __syncthreads();
+                bring(side ? p.k : p.q, side ? p.ldk : p.ldq, sh.x[0]);
+                __syncthreads();
             }
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) sh.x.put8((tid + 256 * i) / (4 * KB), (tid + 256 * i) % (4 * KB), x[i]);
-            __syncthreads();
-            const uint32_t gx = Staged<32 * KB, NT, kDeltaC>::key_get_place(r, q);
+            const uint32_t gx = Staged<32 * KB, NT, kDeltaC>::key_get_place(r, q), gc = sh.C1.get_place(r, q);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                bf16x8 c1[2][NX], c2[2][NX];
+                bf16x8 c1[2][NX], c2[2][NX], c2t[2][NX];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    float x1[8], x2[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int m = 16 * (2 * th + t) + r, o = 32 * b + perm(q, e);
-                        x1[e] = side ? sh.C1[m][o] : sh.C1[o][m];
-                        if (side) x2[e] = sh.C2[m][o] + sh.C2[o][m];
+                    const int ta = 2 * th + t;
+                    const uint32_t pc = sh.C1.put_place(16 * ta + r, q);
+                    if (side) {
+                        sh.C1.column(pc, b, c1[t]);
+                        sh.C2.column(pc, b, c2[t]);
+                        sh.C2.get(gc, ta, c2t[t], b);
+                    } else {
+                        sh.C1.get(gc, ta, c1[t], b);
                     }
-                    split<NX>(x1, c1[t]);
-                    if (side) split<NX>(x2, c2[t]);
                 }
 #pragma unroll
-                for (int c = 0; c < KB; ++c) {
+                for (int c = 0; c < CT; ++c) {
                     bf16x8 xt[NT];
-                    sh.x.key_get(gx, ch * KB + c, b, xt);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (side) {
-                            oS[c][t] = product<NT, NX>(xt, c1[t], oS[c][t]);
-                            dG[c][t] = product<NT, NX>(xt, c2[t], dG[c][t]);
-                        } else {
-                            dG[c][t] = product<NT, NX>(xt, c1[t], dG[c][t]);
-                        }
+                    sh.x[NT == 1 ? side : 0].key_get(gx, cq * CT + c, b, xt);
+                    if (side) {
+                        products<NT, NX, 4>([&](int, int i) { return xt[i]; }, [&](int k, int j) { return k < 2 ? c1[k][j] : c2[k - 2][j]; },
+                                            [&](int k) -> f32x4 & { return k < 2 ? oS[c][k] : dG[c][k - 2]; });
+                        products<NT, NX, 2>([&](int, int i) { return xt[i]; }, [&](int k, int j) { return c2t[k][j]; },
+                                            [&](int k) -> f32x4 & { return dG[c][k]; });
+                    } else {
+                        products<NT, NX, 2>([&](int, int i) { return xt[i]; }, [&](int k, int j) { return c1[k][j]; },
+                                            [&](int k) -> f32x4 & { return dG[c][k]; });
                     }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
         // a shared key head's gradients are summed over its value heads, always in the same order
         const bool last = h == p.group - 1;
 #pragma unroll
-        for (int c = 0; c < KB; ++c)
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (p.group > 1) {
-                    f32x4 *sum = reinterpret_cast<f32x4 *>(p.sum) + ((((long)slot * p.Hk + hk) * 4 + w) * KB + c) * 256 + t * 128 + l;
+                    f32x4 *sum = reinterpret_cast<f32x4 *>(p.sum) + ((((long)slot * p.Hk + hk) * 8 + w) * CT + c) * 256 + t * 128 + l;
                     if (h) {
                         oS[c][t] += sum[0];
                         dG[c][t] += sum[64];
@@ -352,8 +372,7 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                         sum[64] = dG[c][t];
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                const int row = 16 * (2 * th + t) + r, tile = ch * KB + c, chan = 32 * (tile / 2) + 8 * q + 4 * (tile % 2);
+                const int row = 16 * (2 * th + t) + r, tile = cq * CT + c, chan = 32 * (tile / 2) + 8 * q + 4 * (tile % 2);
                 if (!last || row >= at.n || chan >= p.dk) continue;
                 const long o = ((at.row0 + row) * p.Hk + hk) * p.dk + chan;
 #pragma unroll
@@ -369,6 +388,7 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                     }
                 }
             }
+        if (!last) __syncthreads();
     }
 }
 
@@ -380,7 +400,7 @@ hipError_t launch_delta_grad(const DeltaParams &p0, hipStream_t s) {
     const int kb = delta_blocks(p.dk);
     const void *fn = p.io_bf16 ? (kb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<1, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<1, 4>))
                                : (kb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<3, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<3, 4>));
-    return hipLaunchKernel(fn, dim3((unsigned)p.nslot * p.Hk), dim3(256), args, 0, s);
+    return hipLaunchKernel(fn, dim3((unsigned)p.nslot * p.Hk), dim3(512), args, 0, s);
 }
 
 }  // namespace gdr
