@@ -22,16 +22,16 @@ namespace {
 template <int NT, int KB>
 struct GradShared {
     union {
-        struct {
+        struct {  // a block of 32 columns of the state before, of the gradient behind, of D and of y
             Staged<32 * KB, 3, 32> S, G;
             Staged<64, 3, 32> D, Y;
-        } block[2];  // of 32 columns: one is read while the next is written
-        struct {
-            Staged<kDeltaC, NT == 1 ? 2 : 3, kDeltaC> C1, C2;  // rows s, columns t
-            Staged<32 * KB, NT, kDeltaC> x[NT == 1 ? 2 : 1];     // q and k, with fp32 one after the other
+        };
+        struct {  // then the pairs' matrices (rows s, columns t), and q and k (with fp32 one after the other)
+            Staged<kDeltaC, NT == 1 ? 2 : 3, kDeltaC> C1, C2;
+            Staged<32 * KB, NT, kDeltaC> x[NT == 1 ? 2 : 1];
         };
     };
-    float col_m[2][kDeltaC], col_pair[2][kDeltaC], row_m[4][kDeltaC], read[4][kDeltaC], write[4][kDeltaC], dot[8];
+    float col_m[2][kDeltaC], col_pair[2][kDeltaC], row_m[2][kDeltaC], read[2][kDeltaC], write[2][kDeltaC], dot[4];
     ChunkGates gt;
 };
 
@@ -52,29 +52,30 @@ __device__ __forceinline__ float quarters(float x) {  // over the four quarters
     return x + __shfl_xor(x, 32);
 }
 
-// Eight waves: wave (th, cq) has token tiles 2 th and 2 th + 1 and quarter cq of the channels.
+// Four waves: wave (th, cq) has token tiles 2 th and 2 th + 1 and half cq of the channels; of pairs of tokens the s
+// tiles cq and cq + 2.  Two workgroups fit a compute unit: one waits while the other works.
 template <int NT, int KB>
-__global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
-    constexpr int CT = KB / 2;           // channel tiles of a wave
+    constexpr int CT = KB;               // channel tiles of a wave
     __shared__ __attribute__((aligned(16))) GradShared<NT, KB> sh;
     const int hk = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
     const Place at = place_of(p, slot);
     if (at.n <= 0) return;  // uniform over the workgroup
-    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 2, cq = w & 3;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 1, cq = w & 1;
     const int na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv), jblocks = (nj + 1) / 2;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     // all of k or q as it lies, 8 channels a turn
     auto bring = [&](const void *x, int64_t ld, auto &to) __attribute__((always_inline)) {
-        constexpr int kPieces = kDeltaC * 4 * KB / 512;
+        constexpr int kPieces = kDeltaC * 4 * KB / 256;
         bf16x8 t[kPieces][NT];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int row = (tid + 512 * i) / (4 * KB), m = (tid + 512 * i) % (4 * KB);
+            const int row = (tid + 256 * i) / (4 * KB), m = (tid + 256 * i) % (4 * KB);
             load8<NT>(x, (at.row0 + row) * ld + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, t[i]);
         }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) to.put8((tid + 512 * i) / (4 * KB), (tid + 512 * i) % (4 * KB), t[i]);
+        for (int i = 0; i < kPieces; ++i) to.put8((tid + 256 * i) / (4 * KB), (tid + 256 * i) % (4 * KB), t[i]);
     };
 #pragma unroll 1
     for (int h = 0; h < p.group; ++h) {
@@ -83,11 +84,11 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
         const int r = l & 15, q = l >> 4;
         const int hv = hk * p.group + h;
         const long vh = (long)slot * p.Hv + hv;
-        // wave w brings column tile w & 1 of a block, a quarter of its row tiles: of S and G, and of D and y
+        // wave w brings column tile w & 1 of a block, half of its row tiles: of S and G, and of D and y
         const float *from = p.ckpt + vh * nj * (na + 4) * 256, *back = p.back + vh * nj * (na + 4) * 256;
         const long dout = (long)hv * p.dv;
-        f32x4 a[CT], b[CT], d, y;
-        bf16x8 fo[2][NT], fn[2][NT];
+        f32x4 a[CT], b[CT], d[2], y[2];
+        bf16x8 fo[2][NT];
         auto ask = [&](int jb) __attribute__((always_inline)) {
             const int jt = 2 * jb + (w & 1);
             const long tiles = (long)min(jt, nj - 1) * (na + 4) * 256;
@@ -102,76 +103,70 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
                 a[c] = tile(s, (w >> 1) * CT + c);
                 b[c] = tile(g, (w >> 1) * CT + c);
             }
-            d = tile(sd, w >> 1);
-            y = tile(gy, w >> 1);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                d[c] = tile(sd, (w >> 1) * 2 + c);
+                y[c] = tile(gy, (w >> 1) * 2 + c);
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {  // do, by rows: its columns in the operands' order
                 const int row = 16 * (2 * th + t) + r, j = 32 * jb + 4 * q;
-                load44<NT>(p.dout, (at.row0 + row) * p.Hv * p.dv + dout + j, row < at.n && j < p.dv, row < at.n && j + 16 < p.dv, fn[t]);
+                load44<NT>(p.dout, (at.row0 + row) * p.Hv * p.dv + dout + j, row < at.n && j < p.dv, row < at.n && j + 16 < p.dv, fo[t]);
             }
         };
         float dot = 0.f;
-        auto put = [&](int to) __attribute__((always_inline)) {
-            // formed again for each block: kept for all tiles they would take the registers of the sums
-            uint32_t pS = Staged<32 * KB, 3, 32>::put_place(16 * (w & 1) + r, q), pD = Staged<64, 3, 32>::put_place(16 * (w & 1) + r, q);
-            asm volatile("" : "+v"(pS), "+v"(pD));
-            auto &o = sh.block[to];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                o.S.put(pS, (w >> 1) * CT + c, a[c]);
-                o.G.put(pS, (w >> 1) * CT + c, b[c]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dot = fmaf(a[c][i], b[c][i], dot);
-            }
-            o.D.put(pD, w >> 1, d);
-            o.Y.put(pD, w >> 1, y);
-        };
-        ask(0);
         if (w == 0) make_gates(p, at, hv, l, sh.gt);
-        f32x4 oS[CT][2], yS[CT][2], dG[CT][2], n1[2], n2[2];  // [channel tile][token tile]; rows s of tile cq, [token tile]
+        f32x4 oS[CT][2], yS[CT][2], dG[CT][2], n1[2][2], n2[2][2];  // [channel tile][token tile], [s tile][token tile]
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int c = 0; c < CT; ++c) oS[c][t] = yS[c][t] = dG[c][t] = zero;
-            n1[t] = n2[t] = zero;
+            n1[0][t] = n1[1][t] = n2[0][t] = n2[1][t] = zero;
         }
-        put(0);
+#pragma unroll 1
         for (int jb = 0; jb < jblocks; ++jb) {
-            uint32_t gS = Staged<32 * KB, 3, 32>::get_place(r, q), gD = Staged<64, 3, 32>::get_place(r, q);
-            asm volatile("" : "+v"(gS), "+v"(gD));
-            auto &in = sh.block[jb & 1];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) fo[t][n] = fn[t][n];
-            ask(jb + 1);      // zeros behind the last block
-            lds_barrier();    // this block is written, and the one before no longer read
-            bf16x8 fy[2][3], fd[2][3];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                in.Y.get(gD, 2 * th + t, fy[t]);
-                in.D.get(gD, 2 * th + t, fd[t]);
-            }
-            bf16x8 ds[3];
-            in.D.get(gD, cq, ds);
-            // for tiles above the diagonal too (two thirds of them are not), which are not used: no branch among the products
-            products<3, NT, 2>([&](int, int i) { return ds[i]; }, [&](int k, int j) { return fo[k][j]; }, [&](int k) -> f32x4 & { return n1[k]; });
-            products<3, 3, 2>([&](int, int i) { return ds[i]; }, [&](int k, int j) { return fy[k][j]; }, [&](int k) -> f32x4 & { return n2[k]; });
+            // formed again for each block: kept for all tiles they would take the registers of the sums
+            uint32_t pS = Staged<32 * KB, 3, 32>::put_place(16 * (w & 1) + r, q), gS = Staged<32 * KB, 3, 32>::get_place(r, q);
+            uint32_t pD = Staged<64, 3, 32>::put_place(16 * (w & 1) + r, q), gD = Staged<64, 3, 32>::get_place(r, q);
+            asm volatile("" : "+v"(pS), "+v"(gS), "+v"(pD), "+v"(gD));
+            ask(jb);
+            lds_barrier();  // the block before is no longer read
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
-                bf16x8 s[3], g[3];
-                in.S.get(gS, cq * CT + c, s);
-                in.G.get(gS, cq * CT + c, g);
+                sh.S.put(pS, (w >> 1) * CT + c, a[c]);
+                sh.G.put(pS, (w >> 1) * CT + c, b[c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dot = fmaf(a[c][i], b[c][i], dot);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sh.D.put(pD, (w >> 1) * 2 + c, d[c]);
+                sh.Y.put(pD, (w >> 1) * 2 + c, y[c]);
+            }
+            lds_barrier();
+            bf16x8 fy[2][3], fd[2][3], s[3], g[3];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sh.Y.get(gD, 2 * th + t, fy[t]);
+                sh.D.get(gD, 2 * th + t, fd[t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (2 * m > 2 * th + 1) continue;  // above the diagonal
+                sh.D.get(gD, 2 * m + cq, s);
+                products<3, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fo[k][j]; }, [&](int k) -> f32x4 & { return n1[m][k]; });
+                products<3, 3, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fy[k][j]; }, [&](int k) -> f32x4 & { return n2[m][k]; });
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                sh.S.get(gS, cq * CT + c, s);
+                sh.G.get(gS, cq * CT + c, g);
                 products<3, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fo[k][j]; },
                                    [&](int k) -> f32x4 & { return oS[c][k]; });
                 products<3, 3, 4>([&](int k, int i) { return k < 2 ? s[i] : g[i]; }, [&](int k, int j) { return k < 2 ? fy[k][j] : fd[k - 2][j]; },
                                   [&](int k) -> f32x4 & { return k < 2 ? yS[c][k] : dG[c][k - 2]; });
-            }
-            put(jb + 1 & 1);  // among the products
-#pragma unroll
-            for (int i = 0; i < 78; ++i) {  // a matrix instruction takes the time of four others
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+                __builtin_amdgcn_sched_barrier(0);  // no operands of later tiles in registers yet
             }
         }
         __syncthreads();
@@ -189,61 +184,70 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
             }
         };
         __syncthreads();
-        // pairs of tokens: rows s of tile cq, columns t
-        float cm[4] = {}, cp[4] = {};
-        const int s0 = 16 * cq + 4 * q;
-        const f32x4 betas = *reinterpret_cast<const f32x4 *>(&sh.gt.beta[s0]);
-        double Ps[4];
-        int cuts[4];
+        // pairs of tokens: rows s of tiles cq and cq + 2, columns t
+        float rm[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            Ps[i] = sh.gt.P[s0 + i];
-            cuts[i] = sh.gt.cut[s0 + i];
+        for (int m = 0; m < 2; ++m) {
+            const int sa = 2 * m + cq, s0 = 16 * sa + 4 * q;
+            float cm[4] = {}, cp[4] = {};
+            const f32x4 betas = *reinterpret_cast<const f32x4 *>(&sh.gt.beta[s0]);
+            double Ps[4];
+            int cuts[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Ps[i] = sh.gt.P[s0 + i];
+                cuts[i] = sh.gt.cut[s0 + i];
+            }
+            bf16x8 s[KB][NT];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) rows(true, sa, kb, s[kb]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int ta = 2 * th + t, tt = 16 * ta + r;
+                f32x4 c1 = zero, c2 = zero;
+                if (sa <= ta) {
+                    f32x4 qk = zero, kk = zero;
+                    const double Pt = sh.gt.P[tt];
+                    const int cut = sh.gt.cut[tt];
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        bf16x8 tq[NT], tk[NT];
+                        rows(false, ta, kb, tq);
+                        rows(true, ta, kb, tk);
+                        products<NT, NT, 2>([&](int, int i) { return s[kb][i]; }, [&](int k, int j) { return k ? tk[j] : tq[j]; },
+                                            [&](int k) -> f32x4 & { return k ? kk : qk; });
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int s = s0 + i;
+                        const float x = sh.gt.power((float)(Pt - Ps[i])), e = tt >= s && cut == cuts[i] ? x : 0.f;
+                        const float a1 = tt >= s ? n1[m][t][i] : 0.f, a2 = tt > s ? n2[m][t][i] : 0.f;
+                        c1[i] = e * betas[i] * a1;
+                        c2[i] = -e * betas[i] * a2;
+                        const float pair = tt >= s ? e * (a1 * qk[i] - a2 * kk[i]) : 0.f;
+                        cp[i] += pair;
+                        const float through = tt > s ? pair * betas[i] : 0.f;  // a token's own pair does not pass its gate
+                        rm[t] += through;
+                        cm[i] += through;
+                    }
+                }
+                sh.C1.put(sh.C1.put_place(tt, q), sa, c1);
+                sh.C2.put(sh.C2.put_place(tt, q), sa, c2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = row_lanes(cm[i]), z = row_lanes(cp[i]);
+                if (r == 0) {
+                    sh.col_m[th][s0 + i] = x;
+                    sh.col_pair[th][s0 + i] = z;
+                }
+            }
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int ta = 2 * th + t, tt = 16 * ta + r;
-            f32x4 c1 = zero, c2 = zero;
-            float rm = 0.f;
-            if (cq <= ta) {
-                f32x4 qk = zero, kk = zero;
-                const double Pt = sh.gt.P[tt];
-                const int cut = sh.gt.cut[tt];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    bf16x8 s[NT], tq[NT], tk[NT];
-                    rows(true, cq, kb, s);
-                    rows(false, ta, kb, tq);
-                    rows(true, ta, kb, tk);
-                    products<NT, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return k ? tk[j] : tq[j]; },
-                                        [&](int k) -> f32x4 & { return k ? kk : qk; });
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int s = s0 + i;
-                    const float x = sh.gt.power((float)(Pt - Ps[i])), e = tt >= s && cut == cuts[i] ? x : 0.f;
-                    const float a1 = tt >= s ? n1[t][i] : 0.f, a2 = tt > s ? n2[t][i] : 0.f;
-                    c1[i] = e * betas[i] * a1;
-                    c2[i] = -e * betas[i] * a2;
-                    const float pair = tt >= s ? e * (a1 * qk[i] - a2 * kk[i]) : 0.f;
-                    cp[i] += pair;
-                    const float through = tt > s ? pair * betas[i] : 0.f;  // a token's own pair does not pass its gate
-                    rm += through;
-                    cm[i] += through;
-                }
-            }
-            sh.C1.put(sh.C1.put_place(tt, q), cq, c1);
-            sh.C2.put(sh.C2.put_place(tt, q), cq, c2);
-            rm = quarters(rm);
-            if (q == 0) sh.row_m[cq][tt] = rm;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = row_lanes(cm[i]), z = row_lanes(cp[i]);
-            if (r == 0) {
-                sh.col_m[th][s0 + i] = x;
-                sh.col_pair[th][s0 + i] = z;
-            }
+            rm[t] = quarters(rm[t]);
+            if (q == 0) sh.row_m[cq][16 * (2 * th + t) + r] = rm[t];
         }
         // what the states give, and its dot products with q and k
 #pragma unroll
@@ -251,19 +255,17 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
             const int ta = 2 * th + t, tt = 16 * ta + r;
             const float front = sh.gt.front[tt], behind = sh.gt.behind[tt], beta = sh.gt.beta[tt];
             float read = 0.f, write = 0.f;
-            bf16x8 tq[NT], tk[NT];
-            rows(false, ta, cq * CT / 2, tq);
-            rows(true, ta, cq * CT / 2, tk);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
-                const int odd = (cq * CT + c) & 1;  // the tile has channels 4 odd .. 4 odd + 3 of the lane's eight
+                bf16x8 tq[NT], tk[NT];
+                rows(false, ta, (cq * CT + c) / 2, tq);
+                rows(true, ta, (cq * CT + c) / 2, tk);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float qv = 0.f, kv = 0.f;
 #pragma unroll
-                    for (int n = NT - 1; n >= 0; --n) {
-                        const u32x4 u = __builtin_bit_cast(u32x4, tq[n]), v = __builtin_bit_cast(u32x4, tk[n]);
-                        const uint32_t x = odd ? u[2 + i / 2] : u[i / 2], z = odd ? v[2 + i / 2] : v[i / 2];
+                    for (int n = NT - 1; n >= 0; --n) {  // an even tile has the first four of the lane's eight channels
+                        const uint32_t x = __builtin_bit_cast(u32x4, tq[n])[c % 2 * 2 + i / 2], z = __builtin_bit_cast(u32x4, tk[n])[c % 2 * 2 + i / 2];
                         qv += __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
                         kv += __uint_as_float(i & 1 ? z & 0xffff0000u : z << 16);
                     }
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
         if (w == 0) {
             float db = 0.f, down = 0.f, dots = 0.f;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
+            for (int m = 0; m < 2; ++m) {
                 db += sh.write[m][l];
                 down += sh.read[m][l] + sh.row_m[m][l];
             }
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
                 if (l >= s) up += z;
             }
 #pragma unroll
-            for (int m = 0; m < 8; ++m) dots += sh.dot[m];
+            for (int m = 0; m < 4; ++m) dots += sh.dot[m];
             const float kept = sh.gt.whole * dots;
             const bool cuts = l ? sh.gt.cut[l] != sh.gt.cut[l - 1] : sh.gt.cut[0] != 0;
             if (l < at.n) {
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(DeltaParams p) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (p.group > 1) {
-                    f32x4 *sum = reinterpret_cast<f32x4 *>(p.sum) + ((((long)slot * p.Hk + hk) * 8 + w) * CT + c) * 256 + t * 128 + l;
+                    f32x4 *sum = reinterpret_cast<f32x4 *>(p.sum) + ((((long)slot * p.Hk + hk) * 4 + w) * CT + c) * 256 + t * 128 + l;
                     if (h) {
                         oS[c][t] += sum[0];
                         dG[c][t] += sum[64];
@@ -400,7 +402,7 @@ hipError_t launch_delta_grad(const DeltaParams &p0, hipStream_t s) {
     const int kb = delta_blocks(p.dk);
     const void *fn = p.io_bf16 ? (kb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<1, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<1, 4>))
                                : (kb == 2 ? reinterpret_cast<const void *>(&delta_grad_kernel<3, 2>) : reinterpret_cast<const void *>(&delta_grad_kernel<3, 4>));
-    return hipLaunchKernel(fn, dim3((unsigned)p.nslot * p.Hk), dim3(512), args, 0, s);
+    return hipLaunchKernel(fn, dim3((unsigned)p.nslot * p.Hk), dim3(256), args, 0, s);
 }
 
 }  // namespace gdr
