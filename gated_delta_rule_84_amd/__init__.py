@@ -973,6 +973,8 @@ def _nbytes(t) -> int:
 
 def _room(workspace, need: int, device):
     """`workspace` where it holds `need` bytes, else a new one (None for 0)."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
     if not need or _nbytes(workspace) >= need:
         return workspace
     return torch.empty(need, dtype=torch.uint8, device=device)
@@ -1056,25 +1058,63 @@ def _ld(name, t, inner) -> int:
     return 0 if t is None or t.is_contiguous() else _row_stride(name, t, inner)
 
 
+def _ld_flat(name, t) -> int:
+    """_ld of a tensor [.., heads] whose last axis alone is a row."""
+    return 0 if t.is_contiguous() else _row_stride(name, t.unsqueeze(-1), t.shape[-1])
+
+
+def _addresses(**tensors):
+    """Device addresses of tensors whose types, shapes and strides the caller has checked; ValueError for one that is
+    not on the current device."""
+    found = []
+    here = None
+    for name, t in tensors.items():
+        if t is None:
+            found.append(None)
+            continue
+        at = t.get_device()
+        if at != here:
+            if at < 0:
+                raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
+            if here is None:
+                here = torch._C._cuda_getDevice()
+            if at != here:
+                raise ValueError(f"{name}: tensor on {t.device}, current device is cuda:{here}")
+        found.append(t.data_ptr())
+    return found
+
+
+def _dense(name, t, shape, dtype):
+    """ValueError unless t, where there is one, is a dense tensor of that shape and type."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous tensor {shape} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+
+
 def _delta_desc(q, k, v, log_gate, beta, step=False) -> DeltaDesc:
     lead = 1 if step else 2
-    qs, vs = tuple(q.shape), tuple(v.shape)
-    if (len(qs) != lead + 2 or tuple(k.shape) != qs or len(vs) != lead + 2 or vs[:lead] != qs[:lead]
-            or tuple(log_gate.shape) != vs[:-1] or tuple(beta.shape) != vs[:-1]):
+    qs, vs, gs = q.shape, v.shape, log_gate.shape
+    if (len(qs) != lead + 2 or k.shape != qs or len(vs) != lead + 2 or vs[:lead] != qs[:lead] or gs != vs[:-1]
+            or beta.shape != gs):
         T = "" if step else "T, "
-        raise ValueError(f"expected q, k [B, {T}Hk, dk], v [B, {T}Hv, dv] and log_gate, beta [B, {T}Hv], got {qs}, "
-                         f"{tuple(k.shape)}, {vs}, {tuple(log_gate.shape)} and {tuple(beta.shape)}")
+        raise ValueError(f"expected q, k [B, {T}Hk, dk], v [B, {T}Hv, dv] and log_gate, beta [B, {T}Hv], got {tuple(qs)}, "
+                         f"{tuple(k.shape)}, {tuple(vs)}, {tuple(gs)} and {tuple(beta.shape)}")
     if k.dtype != q.dtype or v.dtype != q.dtype or log_gate.dtype != beta.dtype:
         raise ValueError(f"q, k and v must have one type, and log_gate and beta, got {q.dtype}, {k.dtype}, {v.dtype}, "
                          f"{log_gate.dtype} and {beta.dtype}")
     Hk, dk, Hv, dv = qs[-2], qs[-1], vs[-2], vs[-1]
     return DeltaDesc(qs[0], 1 if step else qs[1], Hk, Hv, dk, dv, _dtype_code(q), _dtype_code(log_gate), _ld("q", q, Hk * dk),
-                     _ld("k", k, Hk * dk), _ld("v", v, Hv * dv), _ld("log_gate", log_gate.unsqueeze(-1), Hv),
-                     _ld("beta", beta.unsqueeze(-1), Hv))
+                     _ld("k", k, Hk * dk), _ld("v", v, Hv * dv), _ld_flat("log_gate", log_gate), _ld_flat("beta", beta))
 
 
-def _packed(seq_offsets):
-    return None if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
+def _packed(seq_offsets, desc):
+    """Sequences of a call (None where its rows are not packed) and the shape of its states."""
+    if seq_offsets is None:
+        return None, (desc.B, desc.Hv, desc.dk, desc.dv)
+    n = seq_offsets.numel() - 1
+    if n < 0 or seq_offsets.dtype != torch.int32 or not seq_offsets.is_contiguous():
+        raise ValueError(f"seq_offsets: expected a contiguous tensor [n + 1] of int32, got {tuple(seq_offsets.shape)} of "
+                         f"{seq_offsets.dtype}")
+    return n, (n, desc.Hv, desc.dk, desc.dv)
 
 
 @_on_its_stream
@@ -1085,14 +1125,19 @@ def delta_fwd(q, k, v, log_gate, beta, *, S0=None, seq_offsets=None, want_state=
 
     q, k [B, T, Hk, dk], v [B, T, Hv, dv], log_gate, beta [B, T, Hv], Hv a multiple of Hk; all may be slices of a fused
     projection's output.  seq_offsets [n + 1] int32 cuts the T rows of a B = 1 batch into packed sequences; S0
-    [B or n, Hv, dk, dv] fp32.  Returns (o like v, ST like S0 or None, ckpt, a flat fp32 tensor for delta_bwd, or None).  Rows of o that belong to no packed sequence are left unwritten."""
-    desc, n = _delta_desc(q, k, v, log_gate, beta), _packed(seq_offsets)
+    [B or n, Hv, dk, dv] fp32.  Returns (o like v, ST like S0 or None, ckpt, a flat fp32 tensor for delta_bwd, or None).
+    Rows of o that belong to no packed sequence are left unwritten."""
+    desc = _delta_desc(q, k, v, log_gate, beta)
+    n, states = _packed(seq_offsets, desc)
     f32 = torch.float32
+    _dense("S0", S0, states, f32)
     o = v.new_empty(v.shape)
-    ST = v.new_empty((desc.B if n is None else n, desc.Hv, desc.dk, desc.dv), dtype=f32) if want_state else None
+    ST = v.new_empty(states, dtype=f32) if want_state else None
     ckpt = v.new_empty(gdr_delta_ckpt_size(desc, n or 0) // 4, dtype=f32) if want_ckpt else None
     workspace = _room(workspace, gdr_delta_workspace_size(desc, n or 0), v.device)
-    rc = gdr_delta_fwd(desc, q, k, v, log_gate, beta, seq_offsets, n or 0, S0, o, ST, ckpt, workspace, _nbytes(workspace), stream)
+    a = _addresses(q=q, k=k, v=v, log_gate=log_gate, beta=beta, seq_offsets=seq_offsets, S0=S0, o=o, ST=ST, ckpt=ckpt,
+                   workspace=workspace)
+    rc = _lib.gdr_delta_fwd(ctypes.byref(desc), *a[:6], n or 0, *a[6:], _nbytes(workspace), _stream(stream))
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_delta_fwd")
     return o, ST, ckpt
@@ -1102,12 +1147,18 @@ def delta_fwd(q, k, v, log_gate, beta, *, S0=None, seq_offsets=None, want_state=
 def delta_bwd(q, k, v, log_gate, beta, d_o, ckpt, *, dST=None, seq_offsets=None, want_dS0=True, workspace=None, stream=None):
     """Backward pass of delta_fwd with its inputs and its ckpt: gradients d_o of o (dense) and dST of ST.
     Returns (dq, dk, dv, dlog_gate, dbeta, dS0 or None), dense, in their inputs' types; dS0 fp32."""
-    desc, n = _delta_desc(q, k, v, log_gate, beta), _packed(seq_offsets)
+    desc = _delta_desc(q, k, v, log_gate, beta)
+    n, states = _packed(seq_offsets, desc)
+    f32 = torch.float32
+    _dense("d_o", d_o, tuple(v.shape), v.dtype)
+    _dense("dST", dST, states, f32)
+    _dense("ckpt", ckpt, (gdr_delta_ckpt_size(desc, n or 0) // 4,), f32)
     dq, dk, dv, dg, db = (t.new_empty(t.shape) for t in (q, k, v, log_gate, beta))
-    dS0 = (v.new_empty((desc.B if n is None else n, desc.Hv, desc.dk, desc.dv), dtype=torch.float32) if want_dS0 else None)
+    dS0 = v.new_empty(states, dtype=f32) if want_dS0 else None
     workspace = _room(workspace, gdr_delta_workspace_size(desc, n or 0, True), v.device)
-    rc = gdr_delta_bwd(desc, q, k, v, log_gate, beta, seq_offsets, n or 0, ckpt, d_o, dST, dq, dk, dv, dg, db, dS0, workspace,
-                       _nbytes(workspace), stream)
+    a = _addresses(q=q, k=k, v=v, log_gate=log_gate, beta=beta, seq_offsets=seq_offsets, ckpt=ckpt, d_o=d_o, dST=dST, dq=dq, dk=dk,
+                   dv=dv, dlog_gate=dg, dbeta=db, dS0=dS0, workspace=workspace)
+    rc = _lib.gdr_delta_bwd(ctypes.byref(desc), *a[:6], n or 0, *a[6:], _nbytes(workspace), _stream(stream))
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_delta_bwd")
     return dq, dk, dv, dg, db, dS0
@@ -1118,8 +1169,11 @@ def delta_step(S, q, k, v, log_gate, beta, *, out=None, stream=None):
     """One token of the delta rule for every sequence: q, k [B, Hk, dk], v [B, Hv, dv], log_gate, beta [B, Hv]; S
     [B, Hv, dk, dv] fp32 is updated in place.  Returns o [B, Hv, dv]."""
     desc = _delta_desc(q, k, v, log_gate, beta, step=True)
+    _dense("S", S, (desc.B, desc.Hv, desc.dk, desc.dv), torch.float32)
+    _dense("out", out, tuple(v.shape), v.dtype)
     o = out if out is not None else v.new_empty(v.shape)
-    rc = gdr_delta_step(desc, q, k, v, log_gate, beta, S, o, stream)
+    a = _addresses(q=q, k=k, v=v, log_gate=log_gate, beta=beta, S=S, o=o)
+    rc = _lib.gdr_delta_step(ctypes.byref(desc), *a, _stream(stream))
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_delta_step")
     return o
@@ -1135,12 +1189,15 @@ def _norm_desc(x, norm, weight, gate, act, scale, residual, res_scale, eps, next
         raise ValueError(f"act must be None, 'none', 'linear', 'sigmoid' or 'silu', got {act!r}")
     if (gate is None) != (_ACTS[act] is None):
         raise ValueError(f"a gate needs an act, and an act a gate, got act {act!r}")
-    shape = tuple(x.shape)
+    shape = x.shape
     if len(shape) != 4:
-        raise ValueError(f"expected x [B, T, H, d], got {shape}")
+        raise ValueError(f"expected x [B, T, H, d], got {tuple(shape)}")
     for name, t in (("gate", gate), ("residual", residual)):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != x.dtype):
-            raise ValueError(f"{name}: expected {shape} {x.dtype} like x, got {tuple(t.shape)} {t.dtype}")
+        if t is not None and (t.shape != shape or t.dtype != x.dtype):
+            raise ValueError(f"{name}: expected {tuple(shape)} {x.dtype} like x, got {tuple(t.shape)} {t.dtype}")
+    for name, t in (("weight", weight), ("next_weight", next_weight)):
+        if t is not None and (t.numel() != shape[-1] or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected a contiguous tensor [{shape[-1]}], got {tuple(t.shape)}")
     if weight is not None and next_weight is not None and weight.dtype != next_weight.dtype:
         raise ValueError(f"weight and next_weight must have one type, got {weight.dtype} and {next_weight.dtype}")
     B, T, H, d = shape
@@ -1164,7 +1221,9 @@ def block_norm(x, *, norm="rms", weight=None, gate=None, act=None, scale=1.0, re
     desc = _norm_desc(x, norm, weight, gate, act, scale, residual, res_scale, eps, next_norm, next_weight)
     y = out if out is not None else x.new_empty(x.shape)
     n = x.new_empty(x.shape) if desc.next_norm else None
-    rc = gdr_block_norm_fwd(desc, x, gate, residual, weight, next_weight, y, n, stream)
+    _dense("out", out, tuple(x.shape), x.dtype)
+    a = _addresses(x=x, gate=gate, residual=residual, weight=weight, next_weight=next_weight, y=y, n=n)
+    rc = _lib.gdr_block_norm_fwd(ctypes.byref(desc), *a, _stream(stream))
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_block_norm_fwd")
     return y, n
@@ -1182,8 +1241,11 @@ def block_norm_bwd(x, dy, *, dn=None, norm="rms", weight=None, gate=None, act=No
     dw, dw_next = (None if w is None else w.new_empty(w.shape, dtype=torch.float32) for w in (weight, next_weight))
     if dw is not None or dw_next is not None:
         workspace = _room(workspace, gdr_block_norm_bwd_workspace_size(desc), x.device)
-    rc = gdr_block_norm_bwd(desc, x, gate, residual, weight, next_weight, dy, dn, dx, dgate, dres, dw, dw_next, workspace,
-                            _nbytes(workspace), stream)
+    _dense("dy", dy, tuple(x.shape), x.dtype)
+    _dense("dn", dn, tuple(x.shape), x.dtype)
+    a = _addresses(x=x, gate=gate, residual=residual, weight=weight, next_weight=next_weight, dy=dy, dn=dn, dx=dx, dgate=dgate,
+                   dresidual=dres, dweight=dw, dnext_weight=dw_next, workspace=workspace)
+    rc = _lib.gdr_block_norm_bwd(ctypes.byref(desc), *a, _nbytes(workspace), _stream(stream))
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_block_norm_bwd")
     return dx, dgate, dres, dw, dw_next
