@@ -1,4 +1,4 @@
-// delta.hpp -- parameter block, launchers and device pieces of the trainable delta rule
+// delta.hpp -- launchers and device pieces of the trainable delta rule
 // (delta_prep.hip, delta_chain.hip, delta_grad.hip, delta_step.hip; entry points in delta_api.hip).
 // Not installed.
 //
@@ -23,41 +23,14 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "delta_place.hpp"
 #include "gdr_device.hpp"
 #include "gdr_mfma.hpp"
 
 namespace gdr {
 
-constexpr int kDeltaC = 64;        // tokens of a chunk
 constexpr int kDeltaGates = 256;   // floats kept per (slot, value head), a fragment: front, behind * beta, whole
 constexpr int kDeltaTri = 18;      // fragments of a triangular 64 x 64 matrix: 6 places of 3 terms
-
-// Parameters of one call, already validated by the entry points.
-struct DeltaParams {
-    int B, T, Hk, Hv, dk, dv, group;
-    int io_bf16, gate_bf16;
-    const void *q, *k, *v, *g, *b;
-    int64_t ldq, ldk, ldv, ldg, ldb;  // elements between tokens
-    const int32_t *off;               // [nseq + 1] or NULL: borders of packed sequences
-    int nseq;                         // sequences (B when dense)
-    int chunks;                       // dense: chunks of a sequence
-    int nslot;                        // chunk slots of the call
-    const float *S0;
-    void *o;
-    float *ST;
-    float *ckpt;  // per (slot, value head) the tiles of the state before the chunk and of its D; NULL: not kept
-    const void *dout;
-    const float *dST;
-    void *dq, *dkk, *dvv, *dg, *db;
-    float *dS0;
-    // workspace
-    int raw;         // k and q are copied to shared memory as they are (bf16, 16-byte aligned rows)
-    char *kf, *qf;   // per (slot, key head), as operands: not used when raw
-    char *tf, *pf;   // per (slot, value head), as operands: T and Q, or their transposes (backward)
-    float *gates;
-    float *back;  // like ckpt: the gradient of the state behind the chunk, and y
-    float *sum;   // gradients of q and k of shared key heads while they are summed
-};
 
 // Parameters of a single-token step.
 struct DeltaStepParams {
@@ -90,64 +63,16 @@ inline int delta_blocks(int d) { return d <= 64 ? 2 : 4; }
 
 namespace {
 
-// Where a slot lies: the rows row0 .. row0 + n - 1 (of B * T) of sequence seq; n <= 0 for none.  Sequence i
-// of a packed call takes the slots from off[i] / 64 + i on, which no other sequence reaches; offsets are
-// held inside 0 .. T, so that no access passes the tensors whatever they are.
-struct Place {
-    int seq, n;
-    long row0;
-};
-
-__device__ __forceinline__ int offset_at(const DeltaParams &p, int i) { return min(max(p.off[i], 0), p.T); }
-
-__device__ __forceinline__ int first_slot(const DeltaParams &p, int seq) {
-    return p.off ? offset_at(p, seq) / kDeltaC + seq : seq * p.chunks;
-}
-
-// Tokens and the first row of a sequence.
-__device__ __forceinline__ int tokens_of(const DeltaParams &p, int seq, long &row0) {
-    if (!p.off) {
-        row0 = (long)seq * p.T;
-        return p.T;
-    }
-    const int a = offset_at(p, seq), b = offset_at(p, seq + 1);
-    row0 = a;
-    return b > a ? b - a : 0;
-}
-
-__device__ __forceinline__ Place place_of(const DeltaParams &p, int slot) {
-    Place r;
-    if (p.off) {
-        int lo = 0, hi = p.nseq - 1;  // the last sequence whose first slot is not behind this one
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (first_slot(p, mid) <= slot) lo = mid;
-            else hi = mid - 1;
-        }
-        r.seq = lo;
-    } else {
-        r.seq = slot / p.chunks;
-    }
-    long start;
-    const int len = tokens_of(p, r.seq, start), c = slot - first_slot(p, r.seq);
-    r.row0 = start + (long)c * kDeltaC;
-    r.n = c < 0 ? 0 : min(kDeltaC, len - c * kDeltaC);
-    return r;
-}
-
 // Index of the 32-block of a contraction that element e of lane quarter q stands for: the rows of two
 // accumulator tiles above each other, so that a product's result is the next one's operand as it lies.
 __device__ __forceinline__ int perm(int q, int e) { return e < 4 ? 4 * q + e : 12 + 4 * q + e; }
 
-// Eight fp32 values as three bf16 terms.
-struct Split3 {
-    bf16x8 t[3];
-};
-
+// The upper halves of two fp32 values, cut, as a pair of bf16.
 __device__ __forceinline__ uint32_t high_halves(float a, float b) {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
+// Eight fp32 values as NT bf16 terms.
 template <int NT>
 __device__ __forceinline__ void split(const float (&x)[8], bf16x8 (&t)[NT]) {
     float r[8];
