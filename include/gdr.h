@@ -564,7 +564,8 @@ typedef struct gdr_delta_desc {
  *             n_seq is 0 for dense batches.  One workspace serves one call at a time: calls, or graphs, that may run at the
  *             same time need one each.
  * Pointers need their element's alignment only, S0, ST, ckpt, dST and dS0 16 bytes.  Outputs overlap no input and no
- * other output.  Results are deterministic.
+ * other output.  Results are deterministic: the same call gives the same bits.  A call with another number of sequences or
+ * heads may sum in another order.
  */
 size_t gdr_delta_workspace_size(const gdr_delta_desc *desc, int32_t n_seq, int32_t backward);
 size_t gdr_delta_ckpt_size(const gdr_delta_desc *desc, int32_t n_seq);

@@ -411,9 +411,16 @@ def test_offsets_past_32_bits():
     o, ST, ck = g.delta_fwd(q, k, v, a, b, seq_offsets=off, want_ckpt=True)
     assert ck.numel() * 4 > 1 << 32
     grads = g.delta_bwd(q, k, v, a, b, do, ck, seq_offsets=off)
-    end = [x[:, T - tail:].contiguous() for x in (q, k, v, a, b, do)]
-    o2, S2, ck2 = g.delta_fwd(*end[:5], want_ckpt=True)
-    grads2 = g.delta_bwd(*end, ck2)
-    assert torch.equal(o[:, T - tail:], o2) and torch.equal(ST[1:], S2) and torch.equal(grads[5][1:], grads2[5])
-    for x, y in zip(grads[:5], grads2[:5]):
-        assert torch.equal(x[:, T - tail:], y)
+    # A call with other numbers of sequences and heads may sum in another order (a state's columns on one wave or on two), so
+    # the last sequence alone need not give the same bits: some of its heads are held to the reference, with the bounds above.
+    heads = [0, 17, 31, 47]
+    end = [to_np(x[0, T - tail:, heads]) for x in (q, k, v, a, b, do)]
+    ow, Sw, _ = ref.forward(*end[:5])
+    want = ref.backward(*end)
+    _close("o", to_np(o[0, T - tail:, heads]), ow, _tol(128, "bf16", "bf16", own=False))
+    _close("ST", to_np(ST[1, heads]), Sw, _tol(128, "f32", "bf16"))
+    for name, got, exact in zip(("dq", "dk", "dv"), grads, want):
+        _close(name, to_np(got[0, T - tail:, heads]), exact, _tol(128, "bf16", "bf16", True, own=False))
+    _close("dlog_gate", to_np(grads[3][0, T - tail:, heads]), want[3], _tol(128, "f32", "bf16", True), want[6])
+    _close("dbeta", to_np(grads[4][0, T - tail:, heads]), want[4], _tol(128, "f32", "bf16", True), want[7])
+    _close("dS0", to_np(grads[5][1, heads]), want[5], _tol(128, "f32", "bf16", True))
