@@ -139,6 +139,8 @@ struct Row {
 
 // NV pieces per lane.  WIDE: a workgroup per row; else P lanes.  A workgroup stays for many rows, with the weights
 // in registers, and asks for a row while it works on the one before.
+// Bound by HBM: 65,536 rows of 2,048 bf16 with a residual and both norms 223 us, 4.8 TB/s (a workgroup to a row, which
+// read the weights each time, 537); 262,144 heads of 128 with a gate 48 us forward, 4.2 TB/s, 99 backward, 4.1 TB/s.
 template <bool BF, int NV, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(WIDE ? kWide : kThreads) block_norm_kernel(NormParams p) {
     __shared__ float room[3][2 * kWaves];
