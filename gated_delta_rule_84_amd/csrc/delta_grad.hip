@@ -67,23 +67,23 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), th = w >> 1, cq = w & 1;
     const int na = delta_row_tiles(p.dk), nj = delta_col_tiles(p.dv), jblocks = (nj + 1) / 2;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    // all of k or q as it lies, 8 channels a turn
-    auto bring = [&](const void *x, int64_t ld, auto &to) __attribute__((always_inline)) {
-        constexpr int kPieces = kDeltaC * 4 * KB / 256;
-        bf16x8 t[kPieces][NT];
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int row = (tid + 256 * i) / (4 * KB), m = (tid + 256 * i) % (4 * KB);
-            load8<NT>(x, (at.row0 + row) * ld + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, t[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) to.put8((tid + 256 * i) / (4 * KB), (tid + 256 * i) % (4 * KB), t[i]);
-    };
 #pragma unroll 1
     for (int h = 0; h < p.group; ++h) {
         int l = tid & 63;
         asm volatile("" : "+v"(l));  // addresses are formed for each head: kept over the heads they would take the registers
-        const int r = l & 15, q = l >> 4;
+        const int r = l & 15, q = l >> 4, mine = 64 * w + l;
+        // all of k or q as it lies, 8 channels a turn
+        auto bring = [&](const void *x, int64_t ld, auto &to) __attribute__((always_inline)) {
+            constexpr int kPieces = kDeltaC * 4 * KB / 256;
+            bf16x8 t[kPieces][NT];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int row = (mine + 256 * i) / (4 * KB), m = (mine + 256 * i) % (4 * KB);
+                load8<NT>(x, (at.row0 + row) * ld + (long)hk * p.dk + 8 * m, row < at.n && 8 * m < p.dk, t[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) to.put8((mine + 256 * i) / (4 * KB), (mine + 256 * i) % (4 * KB), t[i]);
+        };
         const int hv = hk * p.group + h;
         const long vh = (long)slot * p.Hv + hv;
         // wave w brings column tile w & 1 of a block, half of its row tiles: of S and G, and of D and y
