@@ -278,6 +278,12 @@ struct Staged {
     }
 };
 
+// x of another lane.  The caller's own lane number goes in: the shuffle intrinsics' indices, which do not depend on it, are formed
+// before loops and take registers over them.
+__device__ __forceinline__ int of_lane(int x, int from) { return __builtin_amdgcn_ds_bpermute(4 * from, x); }
+__device__ __forceinline__ float of_lane(float x, int from) { return __int_as_float(of_lane(__float_as_int(x), from)); }
+__device__ __forceinline__ double of_lane(double x, int from) { return __hiloint2double(of_lane(__double2hiint(x), from), of_lane(__double2loint(x), from)); }
+
 // The gates of a chunk, in shared memory.  P, here in units of ln 2, is summed in 64 bits: behind a strong decay the
 // difference of two fp32 sums would have lost the weak ones.  A gate of -inf cuts: it adds nothing to P, and decays across
 // it are 0.  The difference is rounded once, so the hardware's 2^x is as exact as an fp32 e^x.
@@ -304,8 +310,8 @@ __device__ __forceinline__ void make_gates(const DeltaParams &p, const Place &at
     int cut = cuts;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const double up = __shfl_up(P, d);
-        const int cu = __shfl_up(cut, d);
+        const double up = of_lane(P, lane - d);
+        const int cu = of_lane(cut, lane - d);
         if (lane >= d) {
             P += up;
             cut += cu;

@@ -47,9 +47,9 @@ __device__ __forceinline__ float row_lanes(float x) {  // over the 16 lanes of a
     return x + turned<1>(x);
 }
 
-__device__ __forceinline__ float quarters(float x) {  // over the four quarters
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
+__device__ __forceinline__ float quarters(float x, int l) {  // over the four quarters
+    x += of_lane(x, l ^ 16);
+    return x + of_lane(x, l ^ 32);
 }
 
 // Four waves: wave (th, cq) has token tiles 2 th and 2 th + 1 and half cq of the channels; of pairs of tokens the s
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                 sh.D.get(gD, 2 * m + cq, s);
                 products<3, NT, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fo[k][j]; }, [&](int k) -> f32x4 & { return n1[m][k]; });
                 products<3, 3, 2>([&](int, int i) { return s[i]; }, [&](int k, int j) { return fy[k][j]; }, [&](int k) -> f32x4 & { return n2[m][k]; });
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            rm[t] = quarters(rm[t]);
+            rm[t] = quarters(rm[t], l);
             if (q == 0) sh.row_m[cq][16 * (2 * th + t) + r] = rm[t];
         }
         // what the states give, and its dot products with q and k
@@ -278,15 +279,15 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
                     write = fmaf(kv, bg, write);
                 }
             }
-            read = quarters(read);
-            write = quarters(write);
+            read = quarters(read, l);
+            write = quarters(write, l);
             if (q == 0) {
                 sh.read[cq][tt] = read;
                 sh.write[cq][tt] = write;
             }
         }
 #pragma unroll
-        for (int s = 1; s < 64; s <<= 1) dot += __shfl_xor(dot, s);
+        for (int s = 1; s < 64; s <<= 1) dot += of_lane(dot, l ^ s);
         if (l == 0) sh.dot[w] = dot;
         __syncthreads();
         if (w == 0) {
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
             }
 #pragma unroll
             for (int s = 1; s < 64; s <<= 1) {  // sums over this token and the later ones, and over the earlier ones
-                const float x = __shfl_down(down, s), z = __shfl_up(up, s);
+                const float x = of_lane(down, l + s), z = of_lane(up, l - s);
                 if (l + s < 64) down += x;
                 if (l >= s) up += z;
             }
