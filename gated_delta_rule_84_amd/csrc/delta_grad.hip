@@ -54,8 +54,8 @@ __device__ __forceinline__ float quarters(float x, int l) {  // over the four qu
 
 // Four waves: wave (th, cq) has token tiles 2 th and 2 th + 1 and half cq of the channels; of pairs of tokens the s
 // tiles cq and cq + 2.  Two workgroups fit a compute unit: one waits while the other works (4 x 4,096 tokens, 16 heads of 128 x 128,
-// bf16: 363 us at best, 387 on the mean; eight waves and one workgroup 438 to 540).  It moves 0.86 GB, and the matrix cores are busy
-// for a fifth of its time: what it waits for is the splits and the way through shared memory.
+// bf16: 326 us at best, 356 on the mean; eight waves and one workgroup 438 to 540).  It moves 1.21 GB, 3.7 TB/s: four fifths of it
+// states and their gradients, each read once; the matrix cores are busy for a quarter of its time.
 template <int NT, int KB>
 __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaParams p) {
     constexpr int NX = NT == 1 ? 2 : 3;  // terms of what only outputs of the io type read
