@@ -285,8 +285,13 @@ __device__ __forceinline__ float of_lane(float x, int from) { return __int_as_fl
 __device__ __forceinline__ double of_lane(double x, int from) { return __hiloint2double(of_lane(__double2hiint(x), from), of_lane(__double2loint(x), from)); }
 
 // The gates of a chunk, in shared memory.  P, here in units of ln 2, is summed in 64 bits: behind a strong decay the
-// difference of two fp32 sums would have lost the weak ones.  A gate of -inf cuts: it adds nothing to P, and decays across
-// it are 0.  The difference is rounded once, so the hardware's 2^x is as exact as an fp32 e^x.
+// difference of two fp32 sums would have lost the weak ones.  A gate below kDeltaCut cuts: it adds nothing to P, and decays
+// across it are 0 (as they are in fp32 whatever they multiply: |S| < 2^128, and 2^128 e^-256 < 2^-241).  Without the cut a
+// gate of -1e30, a mask of the type's lowest value among them, would take every later one of the chunk out of P.  So
+// |P| <= 64 * 256 log2 e < 2^15 but for growth, and differences are exact to 2^-37.  The difference is rounded once, so
+// the hardware's 2^x is as exact as an fp32 e^x.
+constexpr float kDeltaCut = -256.f;
+
 struct ChunkGates {
     double P[kDeltaC];
     int cut[kDeltaC];
@@ -305,7 +310,7 @@ __device__ __forceinline__ void make_gates(const DeltaParams &p, const Place &at
     const bool there = lane < at.n;
     const long row = at.row0 + lane;
     const float g = there ? ld_elem(p.g, row * p.ldg + hv, p.gate_bf16) : 0.f;
-    const bool cuts = g == -INFINITY;
+    const bool cuts = g < kDeltaCut;
     double P = cuts ? 0.0 : (double)g * 1.4426950408889634;
     int cut = cuts;
 #pragma unroll

@@ -522,10 +522,10 @@ int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *
  * state keeps fp32's precision whatever the types; outputs are rounded once.  (gdr_chunk_fwd is the forward pass of
  * dense batches at the precision of its two-term states, and takes gates per channel, write keys and gates of the value.)
  *
- * A log gate of -inf is a hard reset: the state before it is forgotten, and the gate's gradient is 0.  Gates above
- * 0 grow the state; where a product of gates passes fp32's range the results are not finite.  NaN and infinities in
- * q, k, v or beta make the results of their sequence and head (and, in the gradients of q and k, of the heads that share
- * them) up to its end, or start in the backward pass, not finite.
+ * A log gate below -256, -inf and a type's lowest value among them, is a hard reset: the state before it, where it is finite,
+ * is forgotten (e^-256 is 0 beside any fp32 value), and the gate's gradient is 0.  Gates above 0 grow the state; where a
+ * product of gates passes fp32's range the results are not finite.  NaN and infinities in q, k, v or beta make
+ * the results of their sequence and head (and, in the gradients of q and k, of the heads that share them) up to its end, or start in the backward pass, not finite.
  */
 #define GDR_DELTA_CHUNK 64
 
