@@ -1146,14 +1146,16 @@ def delta_fwd(q, k, v, log_gate, beta, *, S0=None, seq_offsets=None, want_state=
 @_on_its_stream
 def delta_bwd(q, k, v, log_gate, beta, d_o, ckpt, *, dST=None, seq_offsets=None, want_dS0=True, workspace=None, stream=None):
     """Backward pass of delta_fwd with its inputs and its ckpt: gradients d_o of o (dense) and dST of ST.
-    Returns (dq, dk, dv, dlog_gate, dbeta, dS0 or None), dense, in their inputs' types; dS0 fp32."""
+    Returns (dq, dk, dv, dlog_gate, dbeta, dS0 or None), dense, in their inputs' types; dS0 fp32.  Gradients of rows that
+    belong to no packed sequence are 0."""
     desc = _delta_desc(q, k, v, log_gate, beta)
     n, states = _packed(seq_offsets, desc)
     f32 = torch.float32
     _dense("d_o", d_o, tuple(v.shape), v.dtype)
     _dense("dST", dST, states, f32)
     _dense("ckpt", ckpt, (gdr_delta_ckpt_size(desc, n or 0) // 4,), f32)
-    dq, dk, dv, dg, db = (t.new_empty(t.shape) for t in (q, k, v, log_gate, beta))
+    # the library leaves rows of no packed sequence as they are; which ones there are only the device knows
+    dq, dk, dv, dg, db = (t.new_empty(t.shape) if n is None else t.new_zeros(t.shape) for t in (q, k, v, log_gate, beta))
     dS0 = v.new_empty(states, dtype=f32) if want_dS0 else None
     workspace = _room(workspace, gdr_delta_workspace_size(desc, n or 0, True), v.device)
     a = _addresses(q=q, k=k, v=v, log_gate=log_gate, beta=beta, seq_offsets=seq_offsets, ckpt=ckpt, d_o=d_o, dST=dST, dq=dq, dk=dk,
