@@ -44,6 +44,7 @@ struct DeltaStepParams {
 
 // Bytes of the workspace, and the pointers into it.
 size_t delta_workspace(DeltaParams &p, bool bwd, char *base);
+long delta_chain_threads(const DeltaParams &p);  // of the recurrence's launch
 hipError_t launch_delta_fwd(const DeltaParams &p, hipStream_t s);
 hipError_t launch_delta_bwd(const DeltaParams &p, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaParams &p, bool bwd, hipStream_t s);

@@ -52,6 +52,7 @@ int delta_call(const gdr_delta_desc *d, const int32_t *seq_off, int32_t n_seq, D
     const long long slots = seq_off ? d->T / GDR_DELTA_CHUNK + (long long)n_seq : (long long)d->B * p.chunks;
     if (slots * d->Hv > kMaxThreads / 512) return GDR_EUNSUPPORTED;  // of a launch
     if ((long long)p.nseq * d->Hv > kMaxThreads / 512 - 8) return GDR_EUNSUPPORTED;
+    if (!step && delta_chain_threads(p) > kMaxThreads) return GDR_EUNSUPPORTED;
     p.nslot = d->T > 0 ? (int)slots : 0;
     c.rows = (long long)d->B * d->T;
     c.states = (long long)p.nseq * d->Hv * d->dk * d->dv;

@@ -499,23 +499,47 @@ const void *pick(int nt, int kb, int nw, bool split) {
     return nt == 1 ? (kb == 2 ? of(one(), two()) : of(one(), four())) : (kb == 2 ? of(three(), two()) : of(three(), four()));
 }
 
-}  // namespace
+// How the chains of a call are launched.
+struct Launch {
+    int heads;      // value heads of sequences, a multiple of 8, so that the workgroups of one head run on one of the 8 XCDs
+                    // (workgroups go round them in turn) and share its operands in that one's cache
+    bool split;     // two waves to a tile
+    int nw;         // waves of a workgroup that have tiles
+    int groups;     // workgroups of a head
+    unsigned threads() const { return 64 * (nw + kLoaders); }
+};
 
-hipError_t launch_delta_chain(const DeltaParams &p0, bool bwd, hipStream_t s) {
-    DeltaParams p = p0;
-    // a multiple of 8, so that the workgroups of one head run on one of the 8 XCDs (workgroups go round
-    // them in turn) and share its operands in that one's cache
-    int heads = (int)(((long)p.nseq * p.Hv + 7) / 8 * 8);
-    void *args[] = {&p, &heads};
-    const int nt = p.io_bf16 ? 1 : 3, kb = delta_blocks(p.dk), tiles = (p.dv + 15) / 16;
+Launch plan(const DeltaParams &p, bool keep) {
+    Launch r;
+    r.heads = (int)(((long)p.nseq * p.Hv + 7) / 8 * 8);
+    const int nt = p.io_bf16 ? 1 : 3, kb = delta_blocks(p.dk), tiles = delta_col_tiles(p.dv);
     // Two tiles to a workgroup while a compute unit has one such workgroup at most: then the time is that of one chunk after
     // the other.  Their two waves each (16 heads of 1,024 tokens, 128 x 128, bf16, kept: 55 us, with one wave to a tile 61, four tiles to a
     // workgroup 66; 64 heads 70, 72, 75).  With more heads four tiles share what is copied (80 heads 78 us, two to a workgroup 111).
-    const bool few = (long)heads * ((tiles + 1) / 2) <= 256, keep = p.ckpt != nullptr;
-    const bool split = few && !(nt == 3 && kb == 4 && keep);  // (64 heads, fp32, kept: split 266 us, not 156)
-    const int nw = few && !split ? 2 : 4, per = few ? 2 : 4;
-    const void *fn = bwd ? pick<true, true>(nt, kb, nw, split) : keep ? pick<false, true>(nt, kb, nw, split) : pick<false, false>(nt, kb, nw, split);
-    return hipLaunchKernel(fn, dim3((unsigned)heads * ((tiles + per - 1) / per)), dim3(64 * (nw + kLoaders)), args, 0, s);
+    const bool few = (long)r.heads * ((tiles + 1) / 2) <= 256;
+    r.split = few && !(nt == 3 && kb == 4 && keep);  // (64 heads, fp32, kept: split 266 us, not 156)
+    r.nw = few && !r.split ? 2 : 4;
+    const int per = few ? 2 : 4;
+    r.groups = (tiles + per - 1) / per;
+    return r;
+}
+
+}  // namespace
+
+long delta_chain_threads(const DeltaParams &p) {
+    const Launch r = plan(p, false);  // what is kept changes only launches of at most 256 workgroups
+    return (long)r.heads * r.groups * r.threads();
+}
+
+hipError_t launch_delta_chain(const DeltaParams &p0, bool bwd, hipStream_t s) {
+    DeltaParams p = p0;
+    const bool keep = p.ckpt != nullptr;
+    Launch r = plan(p, keep);
+    void *args[] = {&p, &r.heads};
+    const int nt = p.io_bf16 ? 1 : 3, kb = delta_blocks(p.dk);
+    const void *fn = bwd ? pick<true, true>(nt, kb, r.nw, r.split)
+                     : keep ? pick<false, true>(nt, kb, r.nw, r.split) : pick<false, false>(nt, kb, r.nw, r.split);
+    return hipLaunchKernel(fn, dim3((unsigned)r.heads * r.groups), dim3(r.threads()), args, 0, s);
 }
 
 hipError_t launch_delta_fwd(const DeltaParams &p, hipStream_t s) {

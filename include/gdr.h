@@ -536,9 +536,9 @@ int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *
  *   io_dtype: q, k, v, o and their gradients;  gate_dtype: log_gate, beta and their gradients
  *   ldq, ldk, ldv, ldg, ldb  elements between successive tokens (b, t) of q, k, v, log_gate and beta; 0 means dense,
  *            larger for slices of a fused projection's output
- * B * T below 2^30, heads at most 65536, Hk * dk, Hv * dv and the strides (a step's excepted) at most 2^20, and chunks
- * times value heads times 512 below 2^32 (else GDR_EUNSUPPORTED); chunks are B * ceil(T / 64), or floor(T / 64) + n_seq
- * when packed. */
+ * B * T below 2^30, heads at most 65536, Hk * dk, Hv * dv and the strides (a step's excepted) at most 2^20, chunks
+ * times value heads times 512 below 2^32, and sequences times value heads, rounded up to 8, times 512 below 2^32, for dv > 64
+ * times 768 but for a step (else GDR_EUNSUPPORTED); chunks are B * ceil(T / 64), or floor(T / 64) + n_seq when packed. */
 typedef struct gdr_delta_desc {
     int32_t B, T, Hk, Hv, dk, dv;
     int32_t io_dtype;
