@@ -576,12 +576,12 @@ def gdr_delta_ckpt_size(desc: DeltaDesc, n_seq: int = 0) -> int:
     return int(_lib.gdr_delta_ckpt_size(ctypes.byref(desc), int(n_seq)))
 
 
-def _delta_kinds(desc: DeltaDesc, rows: int, n_seq):
+def _delta_kinds(desc: DeltaDesc, rows: int, n_seq, step=False):
     """(count, dtype) of q and k, v, the gates, the states, ckpt and offsets; None for a descriptor that the library
-    rejects."""
+    rejects (a step ignores T)."""
     io, gt = _TORCH_DTYPE.get(desc.io_dtype), _TORCH_DTYPE.get(desc.gate_dtype)
     n = 0 if n_seq is None else int(n_seq)
-    if io is None or gt is None or min(desc.B, desc.T, desc.Hk, desc.Hv, desc.dk, desc.dv, n) < 0:
+    if io is None or gt is None or min(desc.B, 0 if step else desc.T, desc.Hk, desc.Hv, desc.dk, desc.dv, n) < 0:
         return None
     f32, square = torch.float32, desc.dk * desc.dv
     return ((rows * desc.Hk * desc.dk, io), (rows * desc.Hv * desc.dv, io), (rows * desc.Hv, gt),
@@ -630,7 +630,7 @@ def gdr_delta_bwd(desc: DeltaDesc, q, k, v, log_gate, beta, seq_off, n_seq: int,
 
 
 def gdr_delta_step(desc: DeltaDesc, q, k, v, log_gate, beta, S, o, stream=None) -> int:
-    kinds = _delta_kinds(desc, desc.B, None)
+    kinds = _delta_kinds(desc, desc.B, None, step=True)
     if kinds is not None:
         key, value, gate, state = kinds[:4]
         _check_all((("q", q) + key, ("k", k) + key, ("v", v) + value, ("log_gate", log_gate) + gate, ("beta", beta) + gate,

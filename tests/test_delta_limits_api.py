@@ -34,3 +34,19 @@ def test_chains_of_a_launch(g, dv, most):
     assert g.gdr_delta_workspace_size(over) == 0 and g.gdr_delta_ckpt_size(over) == 0
     fits = _delta(g, B=most, T=1, Hk=1, Hv=1, dk=8, dv=dv)
     assert g.gdr_delta_workspace_size(fits) > 0 and g.gdr_delta_ckpt_size(fits) > 0
+
+
+@pytest.mark.parametrize("T", [-1, -(2 ** 31), 0, 1, 2 ** 31 - 1])
+def test_step_checks_its_tensors_whatever_T_is(g, T):
+    """A step ignores the descriptor's T, and the binding's checks of its tensors do too."""
+    B, Hk, Hv, dk, dv = 2, 2, 4, 16, 24
+    d = _delta(g, B=B, T=T, Hk=Hk, Hv=Hv, dk=dk, dv=dv)
+    bf = torch.bfloat16
+    have = dict(q=torch.zeros(B, Hk, dk, dtype=bf), k=torch.zeros(B, Hk, dk, dtype=bf), v=torch.zeros(B, Hv, dv, dtype=bf),
+                gate=torch.zeros(B, Hv), beta=torch.zeros(B, Hv), S=torch.zeros(B, Hv, dk, dv), o=torch.zeros(B, Hv, dv, dtype=bf))
+    names = dict(gate="log_gate")
+    for name, t in have.items():
+        with pytest.raises(ValueError, match=f"{names.get(name, name)}: expected .* elements"):
+            _step(g, d, **dict(have, **{name: t[:1]}))
+        with pytest.raises(ValueError, match=f"{names.get(name, name)}: expected dtype"):
+            _step(g, d, **dict(have, **{name: t.double()}))
