@@ -15,7 +15,7 @@ int check_delta_desc(const gdr_delta_desc *d) {
     if (!d || d->B < 0 || d->T < 0 || d->Hk < 0 || d->Hv < 0) return GDR_EINVAL;
     if (d->io_dtype != GDR_BF16 && d->io_dtype != GDR_F32) return GDR_EINVAL;
     if (d->gate_dtype != GDR_BF16 && d->gate_dtype != GDR_F32) return GDR_EINVAL;
-    if (d->Hk == 0 ? d->Hv != 0 : d->Hv % d->Hk != 0) return GDR_EINVAL;
+    if (d->Hk == 0 ? d->Hv != 0 : d->Hv == 0 || d->Hv % d->Hk != 0) return GDR_EINVAL;
     if (d->dk < 8 || d->dk > 128 || (d->dk & 7) || d->dv < 8 || d->dv > 128 || (d->dv & 7)) return GDR_EUNSUPPORTED;
     if ((long long)d->B * d->T > 0x3fffffffLL || d->Hk > 65536 || d->Hv > 65536) return GDR_EUNSUPPORTED;
     return GDR_OK;

@@ -530,8 +530,8 @@ int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *
 #define GDR_DELTA_CHUNK 64
 
 /* Descriptor of the trainable delta rule.
- *   B, T >= 0 (T is ignored by a step), Hk >= 0 key heads, Hv a multiple of Hk (else GDR_EINVAL): value head h goes with
- *            key head h / (Hv / Hk)
+ *   B, T >= 0 (T is ignored by a step), Hk >= 0 key heads, Hv a multiple of Hk, 0 only where Hk is (else GDR_EINVAL): value
+ *            head h goes with key head h / (Hv / Hk)
  *   dk, dv   multiples of 8 in [8, 128]                        (else GDR_EUNSUPPORTED)
  *   io_dtype: q, k, v, o and their gradients;  gate_dtype: log_gate, beta and their gradients
  *   ldq, ldk, ldv, ldg, ldb  elements between successive tokens (b, t) of q, k, v, log_gate and beta; 0 means dense,

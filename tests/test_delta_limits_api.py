@@ -50,3 +50,10 @@ def test_step_checks_its_tensors_whatever_T_is(g, T):
             _step(g, d, **dict(have, **{name: t[:1]}))
         with pytest.raises(ValueError, match=f"{names.get(name, name)}: expected dtype"):
             _step(g, d, **dict(have, **{name: t.double()}))
+
+
+def test_key_heads_without_value_heads(g):
+    """Nothing would be computed, and the gradients of q and k of these heads, which are 0, would be left unwritten."""
+    d = _delta(g, Hk=2, Hv=0)
+    assert _fwd(g, d) == g.GDR_EINVAL and _bwd(g, d) == g.GDR_EINVAL and _step(g, d) == g.GDR_EINVAL
+    assert g.gdr_delta_workspace_size(d) == 0 and g.gdr_delta_ckpt_size(d) == 0
