@@ -973,11 +973,11 @@ def _nbytes(t) -> int:
 
 def _room(workspace, need: int, device):
     """`workspace` where it holds `need` bytes, else a new one (None for 0)."""
+    if need and _nbytes(workspace) < need:
+        return torch.empty(need, dtype=torch.uint8, device=device)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    if not need or _nbytes(workspace) >= need:
-        return workspace
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace
 
 
 def _scan_desc(x, alpha, log_gate, coupled, step=False) -> Desc:

@@ -57,3 +57,29 @@ def test_key_heads_without_value_heads(g):
     d = _delta(g, Hk=2, Hv=0)
     assert _fwd(g, d) == g.GDR_EINVAL and _bwd(g, d) == g.GDR_EINVAL and _step(g, d) == g.GDR_EINVAL
     assert g.gdr_delta_workspace_size(d) == 0 and g.gdr_delta_ckpt_size(d) == 0
+
+
+def test_workspace_that_is_not_used(g):
+    """A workspace that is too small is replaced, whatever its strides are; one that is used is dense."""
+    every_other = torch.zeros(64, dtype=torch.uint8)[::2]
+    new = g._room(every_other, 33, "cpu")
+    assert new.numel() == 33 and new.is_contiguous()
+    with pytest.raises(ValueError, match="workspace"):
+        g._room(every_other, 32, "cpu")
+    dense = torch.zeros(64, dtype=torch.uint8)
+    assert g._room(dense, 64, "cpu") is dense and g._room(dense, 0, "cpu") is dense and g._room(None, 0, "cpu") is None
+
+
+@pytest.mark.gpu
+def test_small_strided_workspace_is_replaced(g):
+    """As scan_fwd, scan_bwd and qk_prep_bwd always did."""
+    x, a = torch.rand(1, 600, 2, 64, device="cuda"), torch.rand(1, 600, 2, 64, device="cuda")
+    small = torch.zeros(16, dtype=torch.uint8, device="cuda")[::2]
+    y, ST, ck = g.scan_fwd(x, a, want_ckpt=True)
+    y2, S2, ck2 = g.scan_fwd(x, a, want_ckpt=True, workspace=small)
+    assert torch.equal(y, y2) and torch.equal(ST, S2) and torch.equal(ck, ck2)
+    assert all(torch.equal(p, r) for p, r in zip([t for t in g.scan_bwd(x, a, x, ck) if t is not None],
+                                                 [t for t in g.scan_bwd(x, a, x, ck, workspace=small) if t is not None]))
+    w = torch.rand(64, device="cuda")
+    assert all(torch.equal(p, r) for p, r in zip(g.qk_prep_bwd(x, a, x, a, wq=w, wk=w),
+                                                 g.qk_prep_bwd(x, a, x, a, wq=w, wk=w, workspace=small)))
