@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(WIDE ? kWide : kThreads) block_norm_kernel(Nor
                 put<BF>(p.n, (long)row * p.d + ch, h[v]);
             }
         } else {
-            const float back = p.next_kappa * r2 * r2 * both[1];  // of r2 h
+            // of r2 h; r2^2 would pass fp32's range in a row of zeros with an eps below 2^-128
+            const float back = p.next_kappa * r2 * (r2 * both[1]);
             float dot[1] = {0.f};
 #pragma unroll
             for (int v = 0; v < NV; ++v)
