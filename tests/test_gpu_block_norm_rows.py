@@ -1,10 +1,11 @@
-"""Block norm: rows of zeros with an eps of almost nothing.  Tolerances as derived in test_gpu_block_norm.py."""
+"""Block norm: rows of zeros with an eps of almost nothing, and workgroups that stay for several rows, in the forms that
+test_gpu_block_norm.py gives one row each.  Tolerances as derived there."""
 import numpy as np
 import pytest
 
 from oracle import block_norm as ref
 from tests.gpu_util import gpu, to_np
-from tests.test_gpu_block_norm import U, _norm_close
+from tests.test_gpu_block_norm import U, _check, _norm_close
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,17 @@ def test_rows_of_zeros_with_a_tiny_eps(d, eps):
             _norm_close(f"dx {row}", flat(dx)[row], want[0][row], 256 * U)
         _norm_close("dw_next", to_np(dw2), want[4], (256 + 4) * U)
         assert (n[0, 0] == 0).all() and torch.isfinite(n).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rows", [(4104, 2000), (8192, 1700)])
+def test_many_wide_rows(io, d, rows):
+    """Two pieces a lane, without the next row's loads ahead: at most 910 workgroups backward, two or three rows each."""
+    _check(1, rows, 1, d, io=io, act="sigmoid")
+
+
+@pytest.mark.parametrize("d,rows", [(64, 70001), (128, 40001), (40, 70001)])
+def test_many_narrow_rows_in_fp32(d, rows):
+    """Workgroups take at most 65,536 rows of 64 channels, or 32,768 of 128, at once: the rest is their second round."""
+    _check(1, rows, 1, d, io="f32", wt="bf16", residual=False, next_norm="none")
+    _check(1, rows, 1, d, io="f32", act=None)
