@@ -1120,8 +1120,8 @@ def _packed(seq_offsets, desc):
 @_on_its_stream
 def delta_fwd(q, k, v, log_gate, beta, *, S0=None, seq_offsets=None, want_state=True, want_ckpt=False, workspace=None,
               stream=None):
-    """Trainable delta rule S = a S + beta k (v - a S^T k)^T, o = S^T q with a = exp(log_gate), every product and state at
-    fp32's precision.
+    """Trainable delta rule S = a S + beta k (v - a S^T k)^T, o = S^T q with a = exp(log_gate).  States have fp32's
+    precision whatever the types; factors that only a bf16 o reads are cut to 16 bits.
 
     q, k [B, T, Hk, dk], v [B, T, Hv, dv], log_gate, beta [B, T, Hv], Hv a multiple of Hk; all may be slices of a fused
     projection's output.  seq_offsets [n + 1] int32 cuts the T rows of a B = 1 batch into packed sequences; S0

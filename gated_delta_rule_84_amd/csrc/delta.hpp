@@ -13,11 +13,13 @@
 //     y = T^T (Q^T do + behind beta k G),   dv = y
 //     dS = whole G + q^T (front do) - k^T (front y)
 //
-// Products run on bf16 matrix cores and lose nothing: an fp32 operand is split into three bf16
-// terms that hold all of its 24 bits (bits cut, not rounded: the terms sum to it exactly), a bf16 one
-// is its own only term.  The products of terms i, j with i + j < 3 are summed in fp32; what is left out
-// is about 2^-24 of the result.  bf16 cores do such a product in 3/16 (one exact operand) to 6/16 of
-// the time of the fp32 ones.
+// Products run on bf16 matrix cores: an fp32 operand is split into three bf16 terms that hold all of its 24 bits (bits cut,
+// not rounded: the terms sum to it exactly), a bf16 one is its own only term.  The products of terms i, j with i + j < 3 are
+// summed in fp32: with a bf16 operand that is all of them; of two fp32 ones the rest, of the product's own sign, is up to 2^-21
+// of it and 2^-24.5 on the mean.  bf16 cores do such a product in 3/16 (one exact operand) to 6/16 of the time of the fp32 ones.
+// Two terms (16 bits) are kept of operands that only a bf16 output reads, and of two such ones the products i + j < 2: up to
+// 2^-15 of a product with a bf16 operand left out (2^-17 on the mean), 2^-13 of the others (2^-15.4), in 2/16 and 3/16 of
+// the time; the output's own rounding is up to 2^-8.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -518,14 +518,23 @@ int gdr_scan_step(const gdr_desc *desc, const void *x, int64_t ldx, const void *
  *     S_t = a_t S_{t-1} + beta_t k_t (v_t - a_t S_{t-1}^T k_t)^T,   o_t = S_t^T q_t
  *
  * with a = exp(log_gate), over dense batches or packed sequences, with key heads shared by groups of value
- * heads, inputs that may be slices of a fused projection's output, and a backward pass.  Every product and
- * state keeps fp32's precision whatever the types; outputs are rounded once.  (gdr_chunk_fwd is the forward pass of
+ * heads, inputs that may be slices of a fused projection's output, and a backward pass.  (gdr_chunk_fwd is the forward pass of
  * dense batches at the precision of its two-term states, and takes gates per channel, write keys and gates of the value.)
+ *
+ * Sums are formed in fp32, and outputs are rounded once.  Whatever the types, states, dv, dS0 and the gradients of the gates
+ * have fp32's precision: a product of two fp32 operands is up to 2^-21 of itself too near to 0 (2^-24.5 on the mean), one with
+ * a bf16 operand is exact.  With bf16 io, operands that only o, dq or dk read are cut to 16 bits: beside its rounding, o is
+ * off by up to 2^-15 of the sum of |q| |a S| (over channels) and 2^-13 of that of the sizes of what its chunk's tokens add (mean
+ * 2^-17 and 2^-15), dq and dk by 2^-15 of the sizes of what pairs of tokens of a chunk add.  An output whose terms cancel far
+ * enough has fewer right bits than bf16 holds.  A step keeps fp32's precision throughout.
  *
  * A log gate below -256, -inf and a type's lowest value among them, is a hard reset: the state before it, where it is finite,
  * is forgotten (e^-256 is 0 beside any fp32 value), and the gate's gradient is 0.  Gates above 0 grow the state; where a
- * product of gates passes fp32's range the results are not finite.  NaN and infinities in q, k, v or beta make
- * the results of their sequence and head (and, in the gradients of q and k, of the heads that share them) up to its end, or start in the backward pass, not finite.
+ * product of gates passes fp32's range the results are not finite.
+ *
+ * NaN and infinities in an input of a token reach the results of its sequence and head (in the gradients of q and k, of the
+ * heads that share them) from the first token of its chunk of GDR_DELTA_CHUNK on, earlier tokens than itself among them, and in
+ * the backward pass those of the whole sequence.  Other chunks before it, sequences, batch rows and heads are as without them.
  */
 #define GDR_DELTA_CHUNK 64
 
