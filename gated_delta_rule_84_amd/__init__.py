@@ -1025,7 +1025,8 @@ def scan_fwd(x, alpha, *, beta=None, log_gate=False, coupled=False, S0=None, seq
 def scan_bwd(x, alpha, dy, ckpt, *, beta=None, log_gate=False, coupled=False, S0=None, dST=None, seq_offsets=None,
              workspace=None, stream=None):
     """Backward pass of scan_fwd with its inputs and its ckpt (None where T <= 256): gradients dy of y (dense) and
-    dST of ST.  Returns (dx, dalpha, dbeta or None, dS0): dalpha is the gradient of alpha as stored."""
+    dST of ST.  Returns (dx, dalpha, dbeta or None, dS0): dalpha is the gradient of alpha as stored.  Rows that belong to no
+    packed sequence are left unwritten."""
     desc = _scan_desc(x, alpha, log_gate, coupled)
     n_seq = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
     dev = x.device

@@ -139,8 +139,9 @@ struct Row {
 
 // NV pieces per lane.  WIDE: a workgroup per row; else P lanes.  A workgroup stays for many rows, with the weights
 // in registers, and asks for a row while it works on the one before.
-// Bound by HBM: 65,536 rows of 2,048 bf16 with a residual and both norms 223 us, 4.8 TB/s (a workgroup to a row, which
-// read the weights each time, 537); 262,144 heads of 128 with a gate 48 us forward, 4.2 TB/s, 99 backward, 4.1 TB/s.
+// Whole rows are bound by HBM: 65,536 rows of 2,048 bf16 with a residual and both norms 221 us, 4.9 TB/s (a workgroup to a row,
+// which read the weights each time, 537).  Heads with a gate are bound by arithmetic: 262,144 of 128 channels take 48 us forward (4.2
+// TB/s), 41 of them for 48 vector instructions an element, and 98 backward (3.4 TB/s), 65 of them for 75.
 template <bool BF, int NV, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(WIDE ? kWide : kThreads) block_norm_kernel(NormParams p) {
     __shared__ float room[3][2 * kWaves];
@@ -312,8 +313,10 @@ const void *pick(int nv, bool wide) {
                      : reinterpret_cast<const void *>(&block_norm_kernel<BF, 2, true, BWD>);
 }
 
-// Workgroups: what the chip holds at once, so that each stays for many rows.  Of 256 threads 8 fit a compute unit in
-// the forward pass and 4 in the backward pass, which has twice the registers.
+// Workgroups at most, so that each stays for many rows of a large call.  They are more than the chip holds at once: of 256 threads
+// with one piece a lane 5 fit a compute unit forward (88 registers; fp32 112: 4) and 3 backward (137; fp32 161), 1,280 and 768 on 256
+// units, so some start when others have ended.  Forward that costs nothing (1,280: heads 48 us, join 222, as with 2,048);
+// backward it does (768: heads of 128 81 us against 98, the fp32 join of 2,331 x 1,000 22 against 24).
 constexpr int kBlocks = 2048, kBlocksBwd = 1024;
 
 struct Plan {

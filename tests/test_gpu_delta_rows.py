@@ -48,3 +48,14 @@ def test_zeroed_rows_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, grads))
         torch.ones(1000, device="cuda").sum().item()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_packed_sequences_without_any_row(io):
+    """T = 0: states pass through, forward and backward, and the gradients have no rows."""
+    torch, g = gpu()
+    c = Case(B=1, T=0, Hk=1, Hv=2, dk=128, dv=72, off=[0, 0, 0, 0], io=io)
+    o, ST, ck = c.forward(want_ckpt=True)
+    grads = c.backward(ck)
+    assert o.numel() == 0 and torch.equal(ST, c.S0) and torch.equal(grads[5], c.dST)
+    assert all(x.shape == y.shape for x, y in zip(grads, c.inputs))
